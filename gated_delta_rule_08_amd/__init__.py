@@ -23,7 +23,8 @@ __all__ = [
     "PRO_L2NORM_QK", "PRO_SIGMOID", "gdr_chunk_backward", "gdr_chunk_backward_workspace_bytes",
     "gdr_chunk_backward_workspace_bytes_ranged",
     "gdr_decode_multi_ex", "gdr_chunk_prefill_varlen_ex", "SCHED_FUSED", "SCHED_SPLIT",
-    "gdr_chunk_prefill_noalloc",
+    "gdr_chunk_prefill_noalloc", "gdr_attn_prefill", "gdr_attn_prefill_varlen", "gdr_attn_backward",
+    "gdr_attn_backward_workspace_bytes", "gdr_attn_decode", "gdr_attn_decode_workspace_bytes", "gdr_attn_append",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -46,7 +47,10 @@ EXPORTED_SYMBOLS = ("gdr_decode_step", "gdr_decode_step_ex", "gdr_chunk_prefill_
                     "gdr_decode_multi", "gdr_chunk_prefill",
                     "gdr_chunk_prefill_varlen", "gdr_chunk_prefill_varlen_workspace_bytes",
                     "gdr_chunk_prefill_workspace_bytes", "gdr_status_string",
-                    "gdr_abi_version")
+                    "gdr_abi_version",
+                    "gdr_attn_prefill", "gdr_attn_prefill_varlen", "gdr_attn_backward",
+                    "gdr_attn_backward_workspace_bytes", "gdr_attn_decode",
+                    "gdr_attn_decode_workspace_bytes", "gdr_attn_append")
 CHUNK = 64
 _lib = None
 
@@ -104,6 +108,20 @@ def load_library():
     lib.gdr_chunk_prefill_workspace_bytes_ex.restype = ctypes.c_size_t
     lib.gdr_chunk_prefill_varlen_workspace_bytes_ex.argtypes = [i] * 9
     lib.gdr_chunk_prefill_varlen_workspace_bytes_ex.restype = ctypes.c_size_t
+    lib.gdr_attn_prefill.argtypes = [i] * 9 + [f] + [vp] * 6
+    lib.gdr_attn_prefill.restype = i
+    lib.gdr_attn_prefill_varlen.argtypes = [i] * 10 + [f] + [vp] * 8
+    lib.gdr_attn_prefill_varlen.restype = i
+    lib.gdr_attn_backward.argtypes = [i] * 9 + [f] + [vp] * 10 + [ctypes.c_size_t, vp]
+    lib.gdr_attn_backward.restype = i
+    lib.gdr_attn_backward_workspace_bytes.argtypes = [i] * 9
+    lib.gdr_attn_backward_workspace_bytes.restype = ctypes.c_size_t
+    lib.gdr_attn_decode.argtypes = [i] * 10 + [f] + [vp] * 9 + [ctypes.c_size_t, vp]
+    lib.gdr_attn_decode.restype = i
+    lib.gdr_attn_decode_workspace_bytes.argtypes = [i] * 9
+    lib.gdr_attn_decode_workspace_bytes.restype = ctypes.c_size_t
+    lib.gdr_attn_append.argtypes = [i] * 8 + [vp] * 8
+    lib.gdr_attn_append.restype = i
     lib.gdr_status_string.argtypes = [i]
     lib.gdr_status_string.restype = ctypes.c_char_p
     lib.gdr_abi_version.argtypes = []
@@ -457,3 +475,179 @@ def gdr_chunk_backward(gate: str, q, k, v, alpha, beta, state_in, grad_o, grad_s
         _ptr(grad_k), _ptr(grad_v), _ptr(grad_alpha), _ptr(grad_beta), _ptr(grad_state_in),
         _ptr(workspace), ws_bytes, _stream(stream)))
 
+
+
+def _attn_checks(q, k, v, o, extra=()):
+    """Shapes and types common to the attention calls; returns Hq, Hkv, d."""
+    if q.dim() < 2 or k.dim() != q.dim() or k.shape != v.shape or o.shape != q.shape or k.shape[-1] != q.shape[-1]:
+        raise ValueError("q, k, v, o shapes disagree")
+    if any(t.dtype != q.dtype for t in (k, v, o, *extra)) or q.dtype not in _DTYPES:
+        raise ValueError("q, k, v, o (pages, gradients) must share dtype fp32 or bf16")
+    Hq, Hkv = q.shape[-2], k.shape[-2]
+    if (Hkv == 0 and Hq) or (Hkv and Hq % Hkv):
+        raise ValueError("the query heads must be a multiple of the key heads")
+    return Hq, Hkv, q.shape[-1]
+
+
+def _int32(name, t, shape):
+    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must be int32 %s" % (name, list(shape)))
+
+
+def _attn_call(dev, stream, call):
+    """Runs call(stream pointer) with `dev` current: a launch belongs to
+    the tensors' device, whichever device is current."""
+    if dev.index == torch.cuda.current_device():
+        _check(call(_stream(stream)))
+        return
+    with torch.cuda.device(dev):
+        _check(call(_stream(stream)))
+
+
+def _scale(scale, d):
+    return float(d) ** -0.5 if scale is None else float(scale)
+
+
+def gdr_attn_prefill(q, k, v, o, lse=None, window: int = 0, sinks: int = 0, scale: Optional[float] = None,
+                     stream=None) -> None:
+    """Causal attention of a prompt, full (``window`` 0) or over the last
+    ``window`` positions and the first ``sinks`` keys.
+
+    q, o [B,Tq,Hq,d] and k, v [B,Tk,Hkv,d] share a dtype (fp32 or bf16), d is
+    64 or 128 and Hq a multiple of Hkv; the queries are the last Tq of the Tk
+    positions.  ``lse`` (optional, fp32 [B,Tq,Hq]) receives the log-sum-exp
+    that :func:`gdr_attn_backward` needs.  ``scale`` defaults to d ** -0.5.
+    """
+    if q.dim() != 4 or k.dim() != 4 or k.shape[0] != q.shape[0]:
+        raise ValueError("q must be [B,Tq,Hq,d], k and v [B,Tk,Hkv,d]")
+    Hq, Hkv, d = _attn_checks(q, k, v, o)
+    B, Tq, Tk = q.shape[0], q.shape[1], k.shape[1]
+    if lse is not None and (lse.shape != q.shape[:3] or lse.dtype != torch.float32):
+        raise ValueError("lse must be fp32 [B,Tq,Hq]")
+    _same_device(q, k, v, o, lse)
+    lib = load_library()
+    _attn_call(q.device, stream, lambda st: lib.gdr_attn_prefill(
+        _DTYPES[q.dtype], B, Tq, Tk, Hq, Hkv, d, int(window), int(sinks), _scale(scale, d), _ptr(q), _ptr(k), _ptr(v),
+        _ptr(o), _ptr(lse), st))
+
+
+def gdr_attn_prefill_varlen(q, k, v, cu_q, cu_k, o, lse=None, max_seqlen_q: Optional[int] = None, window: int = 0,
+                            sinks: int = 0, scale: Optional[float] = None, stream=None) -> None:
+    """:func:`gdr_attn_prefill` of packed sequences: q, o [total_q,Hq,d], k, v
+    [total_k,Hkv,d], lse [total_q,Hq]; cu_q and cu_k [N+1] are int32 device
+    offsets.  max_seqlen_q bounds every sequence's queries; if None it is read
+    from cu_q (one device-to-host copy)."""
+    if q.dim() != 3:
+        raise ValueError("q must be [total_q,Hq,d], k and v [total_k,Hkv,d]")
+    Hq, Hkv, d = _attn_checks(q, k, v, o)
+    N = cu_q.numel() - 1
+    if N < 0:
+        raise ValueError("cu_q must be [N+1]")
+    _int32("cu_q", cu_q, (N + 1,))
+    _int32("cu_k", cu_k, (N + 1,))
+    if lse is not None and (lse.shape != q.shape[:2] or lse.dtype != torch.float32):
+        raise ValueError("lse must be fp32 [total_q,Hq]")
+    _same_device(q, k, v, cu_q, cu_k, o, lse)
+    if max_seqlen_q is None:
+        cu = cu_q.cpu()
+        max_seqlen_q = int((cu[1:] - cu[:-1]).max()) if N > 0 else 0
+    lib = load_library()
+    _attn_call(q.device, stream, lambda st: lib.gdr_attn_prefill_varlen(
+        _DTYPES[q.dtype], N, q.shape[0], k.shape[0], int(max_seqlen_q), Hq, Hkv, d, int(window), int(sinks),
+        _scale(scale, d), _ptr(q), _ptr(k), _ptr(v), _ptr(cu_q), _ptr(cu_k), _ptr(o), _ptr(lse), st))
+
+
+def gdr_attn_backward_workspace_bytes(dtype, B: int, Tq: int, Tk: int, Hq: int, Hkv: int, d: int, window: int = 0,
+                                      sinks: int = 0) -> int:
+    return int(load_library().gdr_attn_backward_workspace_bytes(_DTYPES[dtype], B, Tq, Tk, Hq, Hkv, d, int(window),
+                                                                int(sinks)))
+
+
+def gdr_attn_backward(q, k, v, o, lse, grad_o, grad_q, grad_k, grad_v, window: int = 0, sinks: int = 0,
+                      scale: Optional[float] = None, workspace=None, stream=None) -> None:
+    """Gradients of sum(grad_o * o) through :func:`gdr_attn_prefill`, written
+    into grad_q, grad_k, grad_v (shapes and dtype of q, k, v).  o and lse are
+    what the forward wrote for the same q, k, v, window, sinks and scale.
+    workspace: a device tensor of at least gdr_attn_backward_workspace_bytes
+    bytes, or None to have one allocated for this call."""
+    if q.dim() != 4 or k.dim() != 4 or k.shape[0] != q.shape[0]:
+        raise ValueError("q must be [B,Tq,Hq,d], k and v [B,Tk,Hkv,d]")
+    Hq, Hkv, d = _attn_checks(q, k, v, o, (grad_o, grad_q, grad_k, grad_v))
+    B, Tq, Tk = q.shape[0], q.shape[1], k.shape[1]
+    if grad_o.shape != q.shape or grad_q.shape != q.shape or grad_k.shape != k.shape or grad_v.shape != k.shape:
+        raise ValueError("gradient shapes must match the inputs")
+    if lse.shape != q.shape[:3] or lse.dtype != torch.float32:
+        raise ValueError("lse must be fp32 [B,Tq,Hq]")
+    _same_device(q, k, v, o, lse, grad_o, grad_q, grad_k, grad_v, workspace)
+    if workspace is None:
+        workspace = _workspace(gdr_attn_backward_workspace_bytes(q.dtype, B, Tq, Tk, Hq, Hkv, d, window, sinks),
+                               q.device, stream)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    lib = load_library()
+    _attn_call(q.device, stream, lambda st: lib.gdr_attn_backward(
+        _DTYPES[q.dtype], B, Tq, Tk, Hq, Hkv, d, int(window), int(sinks), _scale(scale, d), _ptr(q), _ptr(k), _ptr(v),
+        _ptr(o), _ptr(lse), _ptr(grad_o), _ptr(grad_q), _ptr(grad_k), _ptr(grad_v), _ptr(workspace), ws_bytes, st))
+
+
+def _page_checks(k_pages, v_pages, page_table, Hkv, d, N):
+    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.shape[1] != Hkv or k_pages.shape[3] != d:
+        raise ValueError("k_pages and v_pages must be [num_pages,Hkv,page_size,d]")
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be int32 [sequences,max_pages]")
+    _int32("page_table", page_table, (N, page_table.shape[1]))
+    return k_pages.shape[2], k_pages.shape[0], page_table.shape[1]
+
+
+def gdr_attn_decode_workspace_bytes(dtype, B: int, Hq: int, Hkv: int, d: int, page_size: int, max_pages: int,
+                                    window: int = 0, sinks: int = 0) -> int:
+    return int(load_library().gdr_attn_decode_workspace_bytes(_DTYPES[dtype], B, Hq, Hkv, d, page_size, max_pages,
+                                                              int(window), int(sinks)))
+
+
+def gdr_attn_decode(q, k, v, k_pages, v_pages, page_table, lengths, o, window: int = 0, sinks: int = 0,
+                    scale: Optional[float] = None, workspace=None, stream=None) -> None:
+    """One decode step of attention over a paged cache: the new token's k, v
+    [B,Hkv,d] are written at position lengths[b] of each sequence and its q
+    [B,Hq,d] attends from there, the mask as in :func:`gdr_attn_prefill`.
+
+    k_pages, v_pages [num_pages,Hkv,page_size,d] are updated in place
+    (page_size a power of two); page_table [B,max_pages] and lengths [B] are
+    int32 device tensors (lengths are not advanced).  workspace: a device
+    tensor of at least gdr_attn_decode_workspace_bytes bytes, or None to have
+    one allocated for this call.
+    """
+    if q.dim() != 3 or k.dim() != 3 or k.shape[0] != q.shape[0]:
+        raise ValueError("q must be [B,Hq,d], k and v [B,Hkv,d]")
+    Hq, Hkv, d = _attn_checks(q, k, v, o, (k_pages, v_pages))
+    B = q.shape[0]
+    page, num_pages, max_pages = _page_checks(k_pages, v_pages, page_table, Hkv, d, B)
+    _int32("lengths", lengths, (B,))
+    _same_device(q, k, v, k_pages, v_pages, page_table, lengths, o, workspace)
+    if workspace is None:
+        workspace = _workspace(gdr_attn_decode_workspace_bytes(q.dtype, B, Hq, Hkv, d, page, max_pages, window, sinks),
+                               q.device, stream)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    lib = load_library()
+    _attn_call(q.device, stream, lambda st: lib.gdr_attn_decode(
+        _DTYPES[q.dtype], B, Hq, Hkv, d, page, num_pages, max_pages, int(window), int(sinks), _scale(scale, d), _ptr(q),
+        _ptr(k), _ptr(v), _ptr(k_pages), _ptr(v_pages), _ptr(page_table), _ptr(lengths), _ptr(o), _ptr(workspace),
+        ws_bytes, st))
+
+
+def gdr_attn_append(k, v, cu_seqlens, lengths, k_pages, v_pages, page_table, stream=None) -> None:
+    """Writes packed keys and values k, v [total,Hkv,d] to the pages of N
+    sequences: token i of sequence n (cu_seqlens [N+1], int32) goes to
+    position lengths[n] + i.  Pages, page_table [N,max_pages] and lengths [N]
+    as in :func:`gdr_attn_decode`; lengths are not advanced."""
+    if k.dim() != 3:
+        raise ValueError("k and v must be [total,Hkv,d]")
+    _, Hkv, d = _attn_checks(k, k, v, k, (k_pages, v_pages))
+    N = lengths.numel()
+    _int32("lengths", lengths, (N,))
+    _int32("cu_seqlens", cu_seqlens, (N + 1,))
+    page, num_pages, max_pages = _page_checks(k_pages, v_pages, page_table, Hkv, d, N)
+    _same_device(k, v, cu_seqlens, lengths, k_pages, v_pages, page_table)
+    lib = load_library()
+    _attn_call(k.device, stream, lambda st: lib.gdr_attn_append(
+        _DTYPES[k.dtype], N, k.shape[0], Hkv, d, page, num_pages, max_pages, _ptr(k), _ptr(v), _ptr(cu_seqlens),
+        _ptr(lengths), _ptr(k_pages), _ptr(v_pages), _ptr(page_table), st))

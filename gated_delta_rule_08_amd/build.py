@@ -19,7 +19,7 @@ LIB = os.path.join(PKG, "libgdr.so")
 ARCH = os.environ.get("GDR_OFFLOAD_ARCH", "gfx950")
 
 SOURCES = ["gdr_api.hip", "decode.hip", "prefill_f32.hip", "prefill_bf16.hip", "backward.hip",
-           "noalloc.hip"]
+           "noalloc.hip", "attn_api.hip", "attn_prefill.hip", "attn_backward.hip", "attn_decode.hip"]
 
 HIPFLAGS = [
     "-O3", "-std=c++17", "-fPIC", "--offload-arch=" + ARCH,

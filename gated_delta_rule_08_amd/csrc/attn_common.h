@@ -1,0 +1,270 @@
+// Device code shared by the attention kernels (prefill, backward, paged decode).
+//
+// Every product is a matrix-core tile whose operand fragment is 8 consecutive
+// elements of the contracted axis per lane.  For bf16 that is one
+// instruction (32x32x16 or 16x16x32); for fp32 the same fragment goes through
+// eight fp32 instructions (32x32x2 or 16x16x4), each taking element i of
+// every lane: the contracted axis is only summed over, so the two operands
+// agreeing on its order is all that is needed, and one kernel body serves
+// both types.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "gdr_internal.h"
+
+namespace gdr {
+namespace attn {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2v __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x4v __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8v __attribute__((ext_vector_type(8)));
+typedef short s16x4v __attribute__((ext_vector_type(4)));
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+template <typename T> struct Frag;
+template <> struct Frag<bf16_t> { typedef bf16x8v type; };
+template <> struct Frag<float> { typedef f32x8 type; };
+template <typename T> using frag_t = typename Frag<T>::type;
+
+__device__ __forceinline__ f32x16 zero16() {
+    return f32x16{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+}
+
+// D[row][col] += sum over 16 elements of A[row][.] B[col][.].  A: row = lane
+// % 32; B: col = lane % 32; lane / 32 picks the half of the contracted axis.
+// D: col = lane % 32, register r is row (r / 4) * 8 + (lane / 32) * 4 + r % 4.
+__device__ __forceinline__ f32x16 mma32(const bf16x8v& a, const bf16x8v& b, const f32x16& c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mma32(const f32x8& a, const f32x8& b, f32x16 c) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[i], b[i], c, 0, 0, 0);
+    return c;
+}
+__device__ __forceinline__ constexpr int row32(int r, int h) { return (r >> 2) * 8 + h * 4 + (r & 3); }
+
+// D[row][col] += sum over 32 elements (8 per quarter lane / 16).  A: row =
+// lane % 16; B: col = lane % 16.  D: col = lane % 16, register r is row
+// (lane / 16) * 4 + r.
+__device__ __forceinline__ f32x4 mma16(const bf16x8v& a, const bf16x8v& b, const f32x4& c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mma16(const f32x8& a, const f32x8& b, f32x4 c) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i], b[i], c, 0, 0, 0);
+    return c;
+}
+
+template <typename T> __device__ __forceinline__ frag_t<T> zero_frag();
+template <> __device__ __forceinline__ bf16x8v zero_frag<bf16_t>() {
+    return __builtin_bit_cast(bf16x8v, make_uint4(0u, 0u, 0u, 0u));
+}
+template <> __device__ __forceinline__ f32x8 zero_frag<float>() {
+    return f32x8{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+}
+
+// 8 consecutive elements from global memory (16-byte aligned).
+__device__ __forceinline__ bf16x8v load8(const bf16_t* p) {
+    return __builtin_bit_cast(bf16x8v, *reinterpret_cast<const uint4*>(p));
+}
+__device__ __forceinline__ f32x8 load8(const float* p) {
+    const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// fp32 values as an operand fragment (bf16: rounded to nearest even; a
+// probability or a score gradient then carries a relative error of at most
+// 2^-9, the size of the rounding of the inputs and of the output).
+template <typename T> __device__ __forceinline__ frag_t<T> pack8(const float (&x)[8]);
+template <> __device__ __forceinline__ bf16x8v pack8<bf16_t>(const float (&x)[8]) {
+    bf16x8v r;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = static_cast<__bf16>(x[i]);
+    return r;
+}
+template <> __device__ __forceinline__ f32x8 pack8<float>(const float (&x)[8]) {
+    f32x8 r;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = x[i];
+    return r;
+}
+
+template <typename T> __device__ __forceinline__ void store4(T* p, float a, float b, float c, float d);
+template <> __device__ __forceinline__ void store4<float>(float* p, float a, float b, float c, float d) {
+    *reinterpret_cast<f32x4*>(p) = f32x4{a, b, c, d};
+}
+template <> __device__ __forceinline__ void store4<bf16_t>(bf16_t* p, float a, float b, float c, float d) {
+    const bf16x4v r = {static_cast<__bf16>(a), static_cast<__bf16>(b), static_cast<__bf16>(c),
+                       static_cast<__bf16>(d)};
+    *reinterpret_cast<uint2*>(p) = __builtin_bit_cast(uint2, r);
+}
+
+__device__ __forceinline__ float ex2(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ float lg2(float x) { return __builtin_amdgcn_logf(x); }
+
+// x of the lane 32 away.
+__device__ __forceinline__ float other_half(float x) { return __shfl_xor(x, 32); }
+
+// ---------------------------------------------------------------- LDS tiles
+//
+// A tile holds rows of D elements in 16-byte units; unit u of row r sits at
+// unit position u ^ swz(r).  Two reads have to be free of bank conflicts:
+//  - row fragments: 32 lanes read the same unit of 32 rows, the upper 32
+//    lanes the next unit; lanes 8b.. and 8(b ^ 7).. share a cycle;
+//  - transposing reads (bf16): 4 lane groups of 16 read 8-byte pieces of 4
+//    rows each, 64 bytes wide.
+// Rows 0..3 therefore differ in the 64-byte block (bits 2..3 of the unit for
+// 256-byte rows, bit 2 for pairs of 128-byte rows) and rows 4..15 in the unit
+// inside it.  swz depends on row % 16 only and a row's units are a power of
+// two, so an address is (lane's base) ^ constant + constant: a lane keeps one
+// base per kind of read.
+template <typename T, int D> struct Tile {
+    static constexpr int kRow = D * static_cast<int>(sizeof(T));  // bytes
+    static constexpr int kUnits = kRow / 16;
+    __device__ __forceinline__ static constexpr int swz(int row) {
+        return kUnits == 8 ? (((row >> 1) & 1) << 2) | ((row >> 2) & 3) : ((row & 3) << 2) | ((row >> 2) & 3);
+    }
+    // byte offset of unit 0 of row r; unit u is at this ^ (u << 4)
+    __device__ __forceinline__ static int at(int row) { return row * kRow + (swz(row) << 4); }
+};
+
+// Row fragment: the 8 elements 8g .. 8g+7 of a row, base = Tile::at(row) (+ a
+// multiple of 2^k >= a row: the tile's place in LDS), imm = a constant number of 16-row steps in bytes.
+template <typename T, int D> struct RowRead;
+template <int D> struct RowRead<bf16_t, D> {
+    __device__ __forceinline__ static int base(int row, int h) { return Tile<bf16_t, D>::at(row) ^ (h << 4); }
+    // element group 2 e + h
+    __device__ __forceinline__ static bf16x8v get(const unsigned char* lds, int base, int e, int imm) {
+        return __builtin_bit_cast(bf16x8v, *reinterpret_cast<const uint4*>(lds + (base ^ (e << 5)) + imm));
+    }
+};
+template <int D> struct RowRead<float, D> {
+    __device__ __forceinline__ static int base(int row, int h) { return Tile<float, D>::at(row) ^ (h << 5); }
+    __device__ __forceinline__ static f32x8 get(const unsigned char* lds, int base, int e, int imm) {
+        const f32x4 a = *reinterpret_cast<const f32x4*>(lds + (base ^ (e << 6)) + imm);
+        const f32x4 b = *reinterpret_cast<const f32x4*>(lds + (base ^ (e << 6) ^ 16) + imm);
+        return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+};
+
+// Column fragment: lane (c = lane % 32, h = lane / 32) gets column 32 t + c of
+// the 8 rows {4h..4h+3, 8+4h..8+4h+3} of 16-row step x: the order in which the
+// registers of an accumulator tile hold its rows, so that those registers are
+// the other operand as they stand.
+//
+// bf16: transposing reads.  The 16 lanes of a group address 4 rows (lr / 4) at
+// 4 column quads (lr % 4); lane lr receives column lr of the 4 rows.
+template <typename T, int D> struct ColRead;
+template <int D> struct ColRead<bf16_t, D> {
+    using L = Tile<bf16_t, D>;
+    __device__ __forceinline__ static int base(int lane) {
+        const int h = lane >> 5, g = (lane >> 4) & 1, lr = lane & 15;
+        return (L::at(4 * h + (lr >> 2)) ^ ((2 * g + ((lr >> 1) & 1)) << 4)) + 8 * (lr & 1);
+    }
+    __device__ __forceinline__ static bf16x8v get(const unsigned char* lds, int base, int t, int x) {
+        typedef __attribute__((address_space(3))) s16x4v lds_s16x4;
+        const unsigned char* lo = lds + (base ^ (t << 6)) + 16 * x * L::kRow;
+        const unsigned char* hi = lds + (base ^ (t << 6) ^ 32) + (16 * x + 8) * L::kRow;
+        const s16x4v a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lo));
+        const s16x4v b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(hi));
+        return __builtin_shufflevector(__builtin_bit_cast(bf16x4v, a), __builtin_bit_cast(bf16x4v, b), 0, 1, 2, 3,
+                                       4, 5, 6, 7);
+    }
+};
+template <int D> struct ColRead<float, D> {
+    using L = Tile<float, D>;
+    __device__ __forceinline__ static int base(int lane) {
+        const int h = lane >> 5, c = lane & 31;
+        return (L::at(4 * h) ^ ((c >> 2) << 4)) + 4 * (c & 3);
+    }
+    __device__ __forceinline__ static f32x8 get(const unsigned char* lds, int base, int t, int x) {
+        f32x8 r;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)  // row 8 (i / 4) + 4 h + i % 4
+            r[i] = *reinterpret_cast<const float*>(lds + (base ^ (t << 7) ^ ((i & 3) << 6) ^ ((i >> 2) << 5)) +
+                                                   (16 * x + 8 * (i >> 2) + (i & 3)) * L::kRow);
+        return r;
+    }
+};
+
+// Copies rows row0 .. row0 + ROWS - 1 (clamped to last_row; rows `stride`
+// elements apart from `base`) into an LDS tile, straight from global memory:
+// one instruction of a wave fills 1024 consecutive bytes of the tile, each
+// lane fetching the unit that belongs at its place.  The caller waits for
+// the copies (vmcnt) and passes a barrier before reading them.
+template <typename T, int D, int ROWS, int WAVES>
+__device__ __forceinline__ void copy_tile(unsigned char* tile, const T* base, size_t stride, int row0,
+                                          int last_row, int wave, int lane) {
+    using L = Tile<T, D>;
+    constexpr int kPer = 1024 / L::kRow > 0 ? 1024 / L::kRow : 1;  // rows of one instruction
+    static_assert(1024 % L::kRow == 0, "an instruction fills whole rows");
+    constexpr int kInstr = ROWS / kPer;
+    static_assert(kInstr % WAVES == 0, "every wave issues the same number of copies");
+#pragma unroll
+    for (int j = 0; j < kInstr / WAVES; ++j) {
+        const int jj = wave + j * WAVES;
+        const int r = jj * kPer + lane / L::kUnits;
+        const int u = (lane % L::kUnits) ^ L::swz(r);  // the unit that belongs there
+        const int row = min(row0 + r, last_row);
+        const T* src = base + static_cast<size_t>(row) * stride + u * (16 / sizeof(T));
+        __builtin_amdgcn_global_load_lds(
+            reinterpret_cast<const uint32_t __attribute__((address_space(1)))*>(
+                reinterpret_cast<uintptr_t>(src)),
+            (__attribute__((address_space(3))) uint32_t*)(tile + jj * 1024), 16, 0, 0);
+    }
+}
+
+// The same for rows of packed query heads: row = query * G + head, at base +
+// (query * Hq + head) * D.
+template <typename T, int D, int ROWS, int WAVES>
+__device__ __forceinline__ void copy_rows(unsigned char* tile, const T* base, int Hq, int G, int row0,
+                                          int last_row, int wave, int lane) {
+    using L = Tile<T, D>;
+    constexpr int kPer = 1024 / L::kRow, kInstr = ROWS / kPer;
+    static_assert(1024 % L::kRow == 0 && kInstr % WAVES == 0, "whole rows, the same number for every wave");
+#pragma unroll
+    for (int j = 0; j < kInstr / WAVES; ++j) {
+        const int jj = wave + j * WAVES;
+        const int r = jj * kPer + lane / L::kUnits;
+        const int u = (lane % L::kUnits) ^ L::swz(r);
+        const int row = min(row0 + r, last_row), i = row / G;
+        const T* src = base + (static_cast<size_t>(i) * Hq + (row - i * G)) * D + u * (16 / sizeof(T));
+        __builtin_amdgcn_global_load_lds(
+            reinterpret_cast<const uint32_t __attribute__((address_space(1)))*>(reinterpret_cast<uintptr_t>(src)),
+            (__attribute__((address_space(3))) uint32_t*)(tile + jj * 1024), 16, 0, 0);
+    }
+}
+// One word per lane of a wave into 256 consecutive bytes of LDS.
+__device__ __forceinline__ void copy_words(unsigned char* lds, const float* src) {
+    __builtin_amdgcn_global_load_lds(
+        reinterpret_cast<const uint32_t __attribute__((address_space(1)))*>(reinterpret_cast<uintptr_t>(src)),
+        (__attribute__((address_space(3))) uint32_t*)(lds), 4, 0, 0);
+}
+
+// Keys and queries of one sequence.  Query i is at position i + off; key j is
+// visible to position p if j <= p and (window == 0 or j > p - window or j <
+// sinks).  window is at most the number of keys, so p + window cannot wrap.
+struct Mask {
+    int window, sinks;
+    __device__ __forceinline__ bool sees(int p, int j) const {
+        return j <= p && (window == 0 || j > p - window || j < sinks);
+    }
+    // every key of [j0, j1] is visible from every position of [p0, p1]
+    __device__ __forceinline__ bool all(int p0, int p1, int j0, int j1) const {
+        return j1 <= p0 && (window == 0 || j0 > p1 - window || j1 < sinks);
+    }
+    // no key of [j0, j1] is visible from any position of [p0, p1]
+    __device__ __forceinline__ bool none(int p0, int p1, int j0, int j1) const {
+        return j0 > p1 || (window != 0 && j1 <= p0 - window && j0 >= sinks);
+    }
+};
+
+}  // namespace attn
+}  // namespace gdr

@@ -1,0 +1,312 @@
+// Windowed attention of a prompt: Tq queries, the last Tq of Tk positions,
+// grouped query heads, full causal or sliding window with sink tokens.
+//
+//   s_ij = scale q_i . k_j,   o_i = sum_j p_ij v_j / l_i,   p_ij = 2^(c s_ij - c m_i),
+//
+// one pass over the visible keys with the running maximum m and sum l of the
+// softmax (fp32; c = scale log2 e, the maximum taken before scaling).
+//
+// The query heads of one key head are packed into the rows of a tile: row =
+// query * G + head of the group.  A workgroup's rows then span few positions
+// (few keys outside the mask) and share every key and value tile.  A wave
+// holds 32 rows and forms S^T = K Q^T with 32x32 products: a lane owns one
+// row (column of S^T) and 16 keys of each tile, so the softmax is in-lane
+// apart from one exchange with the lane 32 away, its statistics are one
+// register each, and the exponentials are the operand of O^T += V^T P^T as
+// they stand (the contracted order is that of the accumulator registers, see
+// ColRead).  O stays in registers.
+#include "attn_common.h"
+
+namespace gdr {
+namespace attn {
+namespace {
+
+// Copies issued before this point have landed and every wave has read what it
+// needed: LDS may be read and the other buffer refilled.
+__device__ __forceinline__ void tile_barrier() {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+constexpr int kWaves = 4;
+constexpr int kRows = 32 * kWaves;  // query rows of a workgroup
+
+struct PrefillArgs {
+    int B, Tq, Tk, Hq, Hkv, G;  // packed: B sequences, Tq = longest, Tk unused
+    int window, sinks;
+    float scale;
+    int tiles;  // row tiles of a (sequence, key head)
+    const int *cu_q, *cu_k;
+    int total_q, total_k;
+};
+
+template <typename T, int D> struct PrefillCfg {
+    static constexpr int BN = sizeof(T) == 2 ? 64 : 32;  // keys of a tile
+    static constexpr int kTileBytes = BN * D * static_cast<int>(sizeof(T));
+    static constexpr int kLds = 4 * kTileBytes;  // K and V, two buffers
+};
+
+// The rows of one wave key by key, hidden keys left out: what a wave does when
+// a non-finite value meets its sums.  A lane holds half of its row's channels.
+template <typename T, int D>
+__device__ __noinline__ void exact_rows(Mask mask, int pos, bool live, int wp0, int wp1, float c, bool neg,
+                                        const T* q, const T* k, const T* v, size_t stride, T* o, float* lse,
+                                        int h2) {
+    constexpr int N = D / 2;
+    float acc[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) acc[e] = 0.f;
+    q += N * h2;
+    k += N * h2;
+    v += N * h2;
+    const float cs = neg ? -c : c;
+    float m = -INFINITY, l = 0.f;
+    const int w_lo = mask.window ? max(0, wp0 - mask.window + 1) : 0;
+#pragma unroll 1
+    for (int j = 0; j <= wp1; ++j) {
+        if (j == min(mask.sinks, w_lo)) j = w_lo;  // between the sinks and the window
+        float s = 0.f;
+#pragma unroll 1
+        for (int e = 0; e < N; e += 4)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                s = fmaf(Elem<T>::load(q + e + x), Elem<T>::load(k + static_cast<size_t>(j) * stride + e + x), s);
+        s = (s + other_half(s)) * cs;
+        if (!mask.sees(pos, j)) continue;
+        const float mx = s > m || s != s ? s : m, mc = mx == -INFINITY ? 0.f : mx;
+        const float alpha = m == -INFINITY ? 0.f : ex2(m - mc), p = ex2(s - mc);
+        m = mx;
+        l = l * alpha + p;
+#pragma unroll
+        for (int e = 0; e < N; ++e) acc[e] = fmaf(p, Elem<T>::load(v + static_cast<size_t>(j) * stride + e), acc[e] * alpha);
+    }
+    if (!live) return;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+    for (int e = 0; e < N; ++e) Elem<T>::store(o + N * h2 + e, acc[e] * inv);
+    if (lse && h2 == 0) *lse = l == 0.f ? -INFINITY : (m + lg2(l)) * kLn2;
+}
+
+template <typename T, int D>
+__global__ __launch_bounds__(64 * kWaves, 2) void prefill_kernel(PrefillArgs a, const T* __restrict__ q,
+                                                                 const T* __restrict__ k,
+                                                                 const T* __restrict__ v, T* __restrict__ o,
+                                                                 float* __restrict__ lse) {
+    using C = PrefillCfg<T, D>;
+    constexpr int BN = C::BN, NS = BN / 32, KS = D / 16, DT = D / 32;
+    extern __shared__ unsigned char smem[];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int h2 = lane >> 5;
+    // Workgroups go round the 8 XCDs: consecutive row tiles of a key head stay
+    // on one XCD, whose L2 then holds that head's keys and values.  The rows
+    // with the most visible keys (the last) start first.
+    const int heads = a.B * a.Hkv, bid = blockIdx.x;
+    int head, tile;
+    if (heads % 8 == 0) {
+        head = (bid / 8 / a.tiles) * 8 + (bid & 7);
+        tile = a.tiles - 1 - (bid / 8) % a.tiles;
+    } else {
+        head = bid % heads;
+        tile = a.tiles - 1 - bid / heads;
+    }
+    const int b = head / a.Hkv, hk = head - b * a.Hkv;
+    int Tq = a.Tq, Tk = a.Tk;
+    size_t q0 = static_cast<size_t>(b) * a.Tq, k0 = static_cast<size_t>(b) * a.Tk;
+    if (a.cu_q) {
+        const int qa = a.cu_q[b], qe = a.cu_q[b + 1], ka = a.cu_k[b], ke = a.cu_k[b + 1];
+        if (qa < 0 || qe < qa || qe > a.total_q || qe - qa > a.Tq || ka < 0 || ke < ka || ke > a.total_k) return;
+        Tq = qe - qa;
+        Tk = ke - ka;
+        q0 = qa;
+        k0 = ka;
+    }
+    const int G = a.G, nrows = Tq * G, row0 = tile * kRows;
+    if (row0 >= nrows) return;
+    const int off = Tk - Tq;
+    const Mask mask{a.window, a.sinks};
+
+    // this wave's and this lane's rows (a wave or lane past the end repeats
+    // the last row and stores nothing)
+    const int wr0 = min(row0 + 32 * wave, nrows - 1), wr1 = min(row0 + 32 * wave + 31, nrows - 1);
+    const bool live = row0 + 32 * wave + (lane & 31) < nrows;
+    const bool wave_live = row0 + 32 * wave < nrows;
+    const int row = min(row0 + 32 * wave + (lane & 31), nrows - 1);
+    const int qi = row / G, g = row - qi * G, pos = qi + off;
+    const int wp0 = __builtin_amdgcn_readfirstlane(wr0 / G + off);
+    const int wp1 = __builtin_amdgcn_readfirstlane(wr1 / G + off);
+    const size_t qrow = (q0 + qi) * a.Hq + static_cast<size_t>(hk) * G + g;
+
+    // key tiles of the workgroup's rows: the sinks before the window, then the window
+    const int p0 = row0 / G + off, p1 = min(row0 + kRows - 1, nrows - 1) / G + off;
+    const int win = a.window;
+    const int w_lo = win ? max(0, p0 - win + 1) : 0;
+    const int t_lo = w_lo / BN, t_hi = p1 < 0 ? -1 : p1 / BN;  // p1 <= Tk - 1
+    const int t_sink = win ? min((a.sinks + BN - 1) / BN, t_lo) : 0;
+    const int n = t_hi < t_lo ? 0 : t_sink + t_hi - t_lo + 1;
+
+    // Q^T as the B operand.  A negative scale flips the sign of q (exact), so
+    // that the largest raw score is the largest scaled one.
+    frag_t<T> qf[KS];
+    {
+        const T* qp = q + qrow * D + 8 * h2;
+        const bool neg = a.scale < 0.f;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            qf[s] = load8(qp + 16 * s);
+            if (neg) qf[s] = -qf[s];
+        }
+    }
+    // a scale of 0 as one that no score survives: c -inf of a hidden key stays -inf
+    const float c = fmaxf(fabsf(a.scale) * kLog2e, 1e-37f);
+
+    f32x16 acc[DT];
+#pragma unroll
+    for (int t = 0; t < DT; ++t) acc[t] = zero16();
+    float m = -INFINITY, l = 0.f;
+
+    const size_t kstride = static_cast<size_t>(a.Hkv) * D;
+    const T* kbase = k + (k0 * a.Hkv + hk) * D;
+    const T* vbase = v + (k0 * a.Hkv + hk) * D;
+    auto tile_of = [&](int i) { return i < t_sink ? i : i - t_sink + t_lo; };
+    auto fetch = [&](int i) {
+        unsigned char* buf = smem + (i & 1) * 2 * C::kTileBytes;
+        const int j0 = tile_of(i) * BN;
+        copy_tile<T, D, BN, kWaves>(buf, kbase, kstride, j0, Tk - 1, wave, lane);
+        copy_tile<T, D, BN, kWaves>(buf + C::kTileBytes, vbase, kstride, j0, Tk - 1, wave, lane);
+    };
+    const int kb0 = RowRead<T, D>::base(lane & 31, h2), vb0 = ColRead<T, D>::base(lane) + C::kTileBytes;
+    if (n > 0) fetch(0);
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+        tile_barrier();
+        if (i + 1 < n) fetch(i + 1);
+        const int buf = (i & 1) * 2 * C::kTileBytes, kb = kb0 + buf, vb = vb0 + buf;
+        const int j0 = tile_of(i) * BN;
+        if (!wave_live || mask.none(wp0, wp1, j0, j0 + BN - 1)) continue;
+
+        f32x16 s[NS];
+#pragma unroll
+        for (int u = 0; u < NS; ++u) {
+            s[u] = zero16();
+#pragma unroll
+            for (int e = 0; e < KS; ++e)
+                s[u] = mma32(RowRead<T, D>::get(smem, kb, e, 32 * u * Tile<T, D>::kRow), qf[e], s[u]);
+        }
+        if (!mask.all(wp0, wp1, j0, j0 + BN - 1)) {
+#pragma unroll
+            for (int u = 0; u < NS; ++u)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    if (!mask.sees(pos, j0 + 32 * u + row32(r, h2))) s[u][r] = -INFINITY;
+        }
+        float mx = s[0][0];
+#pragma unroll
+        for (int u = 0; u < NS; ++u)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[u][r]);
+        mx = fmaxf(m, fmaxf(mx, other_half(mx)));
+        // a row that has seen no key yet keeps m = -inf and weights 0
+        const float mc = mx == -INFINITY ? 0.f : mx * c;
+        if (__any(mx > m)) {
+            const float alpha = m == -INFINITY ? 0.f : ex2(m * c - mc);
+            l *= alpha;
+#pragma unroll
+            for (int t = 0; t < DT; ++t) acc[t] *= alpha;
+            m = mx;
+        }
+        frag_t<T> pf[2 * NS];
+        float ls = 0.f;
+#pragma unroll
+        for (int u = 0; u < NS; ++u) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                s[u][r] = ex2(fmaf(s[u][r], c, -mc));
+                ls += s[u][r];
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                float w[8];
+#pragma unroll
+                for (int y = 0; y < 8; ++y) w[y] = s[u][8 * x + y];
+                pf[2 * u + x] = pack8<T>(w);
+            }
+        }
+        l += ls;
+#pragma unroll
+        for (int t = 0; t < DT; ++t)
+#pragma unroll
+            for (int x = 0; x < 2 * NS; ++x) acc[t] = mma32(ColRead<T, D>::get(smem, vb, t, x), pf[x], acc[t]);
+    }
+
+    l += other_half(l);
+
+    // A hidden key has weight 0, but 0 times an infinity or NaN in its value
+    // row is NaN: a wave whose sums hold a NaN forms its rows again from the
+    // visible keys alone.
+    bool bad = l != l;
+#pragma unroll
+    for (int t = 0; t < DT; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) bad |= acc[t][r] != acc[t][r];
+    if (__any(bad && live)) {
+        exact_rows<T, D>(mask, pos, live, wp0, wp1, c, a.scale < 0.f, q + qrow * D, kbase, vbase, kstride, o + qrow * D,
+                         lse ? lse + qrow : nullptr, h2);
+        return;
+    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;  // no visible key: zeros
+    if (live) {
+        T* op = o + qrow * D;
+#pragma unroll
+        for (int t = 0; t < DT; ++t)
+#pragma unroll
+            for (int r = 0; r < 16; r += 4)
+                store4<T>(op + 32 * t + row32(r, h2), acc[t][r] * inv, acc[t][r + 1] * inv,
+                          acc[t][r + 2] * inv, acc[t][r + 3] * inv);
+        if (lse && h2 == 0) lse[qrow] = l > 0.f ? (m * c + lg2(l)) * kLn2 : -INFINITY;
+    }
+}
+
+template <typename T, int D>
+hipError_t launch(const PrefillArgs& a, const void* q, const void* k, const void* v, void* o, float* lse,
+                  hipStream_t st) {
+    using C = PrefillCfg<T, D>;
+    const unsigned long long blocks = static_cast<unsigned long long>(a.B) * a.Hkv * a.tiles;
+    if (!grid_fits(blocks, 64 * kWaves)) return hipErrorInvalidConfiguration;
+    auto* f = prefill_kernel<T, D>;
+    if (C::kLds > 64 * 1024) {
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(f),
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize, C::kLds);
+        if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL(f, dim3(static_cast<unsigned>(blocks)), dim3(64 * kWaves), C::kLds, st, a,
+                       static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v),
+                       static_cast<T*>(o), lse);
+    return hipGetLastError();
+}
+
+}  // namespace
+}  // namespace attn
+
+hipError_t launch_attn_prefill(int dtype, int B, int Tq, int Tk, int Hq, int Hkv, int d, int window, int sinks,
+                               float scale, const void* q, const void* k, const void* v, void* o, float* lse,
+                               hipStream_t st, const AttnPacked& pk) {
+    attn::PrefillArgs a{};
+    a.B = B;
+    a.Tq = Tq;
+    a.Tk = Tk;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.G = Hq / Hkv;
+    a.window = window;
+    a.sinks = sinks;
+    a.scale = scale;
+    a.tiles = static_cast<int>((static_cast<long long>(Tq) * a.G + attn::kRows - 1) / attn::kRows);
+    a.cu_q = pk.cu_q;
+    a.cu_k = pk.cu_k;
+    a.total_q = pk.total_q;
+    a.total_k = pk.total_k;
+    if (dtype == GDR_DTYPE_F32)
+        return d == 64 ? attn::launch<float, 64>(a, q, k, v, o, lse, st) : attn::launch<float, 128>(a, q, k, v, o, lse, st);
+    return d == 64 ? attn::launch<bf16_t, 64>(a, q, k, v, o, lse, st) : attn::launch<bf16_t, 128>(a, q, k, v, o, lse, st);
+}
+
+}  // namespace gdr

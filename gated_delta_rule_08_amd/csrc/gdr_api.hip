@@ -159,7 +159,8 @@ const char* gdr_status_string(int status) {
         case GDR_ERR_NULL_PTR: return "GDR_ERR_NULL_PTR: a required pointer is NULL";
         case GDR_ERR_BAD_SHAPE: return "GDR_ERR_BAD_SHAPE: a size is negative or too large";
         case GDR_ERR_UNSUPPORTED:
-            return "GDR_ERR_UNSUPPORTED: dk and dv must be 16, 32, 64 or 128 and chunk must be 64";
+            return "GDR_ERR_UNSUPPORTED: dk and dv must be 16, 32, 64 or 128 and chunk must be 64 (attention: d "
+                   "64 or 128, page size a power of two)";
         case GDR_ERR_MISALIGNED:
             return "GDR_ERR_MISALIGNED: tensors need 16-byte alignment (beta and GDN alpha 4-byte)";
         case GDR_ERR_WORKSPACE: return "GDR_ERR_WORKSPACE: workspace missing or too small";

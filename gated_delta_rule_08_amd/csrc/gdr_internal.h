@@ -123,6 +123,36 @@ hipError_t launch_backward(int kda, int dtype, int B, int T, int H, int dk, int 
                            const float* d_state_out, void* dq, void* dkk, void* dvv, float* dalpha,
                            float* dbeta, float* d_state_in, float* ws, size_t ws_floats, hipStream_t s);
 
+// Attention (attn_*.hip): windowed prefill and its backward, the paged decode
+// step and the append to the pages.  window is 0 (full causal) or at most the
+// number of keys, sinks at most the number of keys.
+//  Packed sequences (device pointers; null for the uniform layout): sequence b
+//  holds queries cu_q[b] .. cu_q[b+1]-1 and keys cu_k[b] .. cu_k[b+1]-1; one
+//  whose offsets are out of range is skipped.
+struct AttnPacked {
+    const int* cu_q = nullptr;
+    const int* cu_k = nullptr;
+    int total_q = 0, total_k = 0;
+};
+hipError_t launch_attn_prefill(int dtype, int B, int Tq, int Tk, int Hq, int Hkv, int d, int window, int sinks,
+                               float scale, const void* q, const void* k, const void* v, void* o, float* lse,
+                               hipStream_t s, const AttnPacked& pk = AttnPacked());
+
+size_t attn_backward_workspace_floats(int B, int Tq, int Tk, int Hq, int Hkv, int d, int window, int sinks);
+hipError_t launch_attn_backward(int dtype, int B, int Tq, int Tk, int Hq, int Hkv, int d, int window, int sinks,
+                                float scale, const void* q, const void* k, const void* v, const void* o,
+                                const float* lse, const void* go, void* gq, void* gk, void* gv, float* ws,
+                                hipStream_t s);
+size_t attn_decode_workspace_floats(int B, int Hq, int Hkv, int d, int page_size, int max_pages, int window,
+                                    int sinks);
+hipError_t launch_attn_decode(int dtype, int B, int Hq, int Hkv, int d, int page_size, int num_pages, int max_pages,
+                              int window, int sinks, float scale, const void* q, const void* k, const void* v,
+                              void* k_pages, void* v_pages, const int* table, const int* lengths, void* o, float* ws,
+                              hipStream_t s);
+hipError_t launch_attn_append(int dtype, int N, int total, int Hkv, int d, int page_size, int num_pages,
+                              int max_pages, const void* k, const void* v, const int* cu, const int* lengths,
+                              void* k_pages, void* v_pages, const int* table, hipStream_t s);
+
 // state_out <- state_in (or zeros when state_in is NULL), n floats.
 hipError_t launch_state_copy(const float* state_in, float* state_out, size_t n, hipStream_t s);
 

@@ -29,8 +29,8 @@
  *  - q, k, v, o share one element type, selected by `dtype`: GDR_DTYPE_F32
  *    (IEEE fp32) or GDR_DTYPE_BF16 (bfloat16, outputs rounded to nearest
  *    even).  alpha, beta and the state are always fp32.
- *  - Supported head sizes: dk, dv in {16, 32, 64, 128}.  The chunk size of
- *    the prefill is 64.
+ *  - Supported head sizes: dk, dv in {16, 32, 64, 128} (attention: below).  The
+ *    chunk size of the prefill is 64.
  *  - Alignment: q, k, v, o, the state buffers and KDA alpha must be 16-byte
  *    aligned; beta and GDN alpha 4-byte aligned.
  *  - `stream` is a hipStream_t (NULL = the default stream).  All work is
@@ -66,7 +66,8 @@ enum {
     GDR_ERR_NULL_PTR = -1,    /* a required pointer is NULL                 */
     GDR_ERR_BAD_SHAPE = -2,   /* a size is negative or overflows (also: a
                                  launch would exceed 2^32 work-items)       */
-    GDR_ERR_UNSUPPORTED = -3, /* dk, dv or chunk outside the supported set  */
+    GDR_ERR_UNSUPPORTED = -3, /* dk, dv, d, chunk or page size outside the
+                                 supported set                              */
     GDR_ERR_MISALIGNED = -4,  /* a pointer violates the alignment rule      */
     GDR_ERR_WORKSPACE = -5,   /* workspace missing or too small             */
     GDR_ERR_BAD_ENUM = -6,    /* gate, dtype or flags not known             */
@@ -373,6 +374,146 @@ size_t gdr_chunk_backward_workspace_bytes(int gate, int dtype, int B, int T, int
  * the same as in one pass. */
 size_t gdr_chunk_backward_workspace_bytes_ranged(int gate, int dtype, int B, int T, int H, int dk,
                                                  int dv, int chunk, int range_chunks);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Attention: the two other token mixers a layer can be switched to (§2.A lists
+ * full attention, FA, and sliding-window attention, SWA, beside KDA and GDN),
+ * over the whole prompt, backwards, and token by token over a paged cache.
+ *
+ * Mask, the same everywhere: the query at position p sees key j if
+ *     j <= p  and  (window == 0  or  j > p - window  or  j < sinks),
+ * i.e. full causal attention with window 0, else the last `window` positions
+ * (its own included) and the first `sinks` keys.  For a query row i:
+ *     s_ij = scale q_i . k_j over the visible keys, o_i = softmax(s_i) v.
+ * A query that sees no key gets o = 0 and lse = -inf.  A hidden key has no
+ * influence whatever its values (infinities and NaN included).
+ *
+ * Query heads: Hq a multiple of Hkv; query head h reads key head
+ * h / (Hq / Hkv).  d in {64, 128} for keys and values alike.  With dtype BF16
+ * the products run on bf16 matrix cores with fp32 accumulation and the
+ * softmax weights (backward: and the score gradients) enter the second
+ * product rounded to bf16; statistics and sums are fp32.  With dtype F32 every
+ * operation is fp32.  Every sum runs in a fixed order: repeated calls give
+ * identical results.  Tensors as above: dense, row-major, 16-byte aligned
+ * (int arrays and lse 4-byte), no output overlapping an input.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * Attention of Tq queries, the last Tq of Tk positions (query i is at position
+ * i + Tk - Tq), for B sequences: a whole prompt (Tq == Tk) or its next part on
+ * the keys so far (Tq < Tk).  With Tq > Tk the first Tq - Tk queries see
+ * nothing.
+ *
+ *   q, o   [B, Tq, Hq, d]    k, v  [B, Tk, Hkv, d]   dtype
+ *   lse    [B, Tq, Hq] fp32, or NULL: log of the sum of exp(s_ij), what the
+ *          backward needs
+ *
+ * No workspace.  Returns a GDR_* status.
+ */
+int gdr_attn_prefill(int dtype, int B, int Tq, int Tk, int Hq, int Hkv, int d, int window, int sinks,
+                     float scale, const void* q, const void* k, const void* v, void* o, float* lse,
+                     void* stream);
+
+/*
+ * gdr_attn_prefill of N packed sequences of different lengths.
+ *
+ *   q, o   [total_q, Hq, d]  k, v  [total_k, Hkv, d]   dtype
+ *   lse    [total_q, Hq] fp32, or NULL
+ *   cu_q, cu_k  [N + 1] int32, DEVICE: sequence n has queries cu_q[n] ..
+ *          cu_q[n+1]-1, the last of its keys cu_k[n] .. cu_k[n+1]-1
+ *   max_q  an upper bound of every sequence's queries (sizes the launch)
+ *
+ * The offsets are device data the host does not read: a sequence whose offsets
+ * are out of order, beyond total_q or total_k, or with more than max_q
+ * queries is skipped (nothing of it is written), and rows of no sequence are
+ * left as they were.  Returns a GDR_* status.
+ */
+int gdr_attn_prefill_varlen(int dtype, int N, int total_q, int total_k, int max_q, int Hq, int Hkv, int d,
+                            int window, int sinks, float scale, const void* q, const void* k, const void* v,
+                            const int* cu_q, const int* cu_k, void* o, float* lse, void* stream);
+
+/*
+ * Backward pass of gdr_attn_prefill: gradients of L = sum(grad_o * o), with o
+ * and lse as the forward wrote them for the same arguments.
+ *
+ *   q, o, grad_o, grad_q [B, Tq, Hq, d];  k, v, grad_k, grad_v [B, Tk, Hkv, d]
+ *   lse [B, Tq, Hq] fp32
+ *   workspace  at least gdr_attn_backward_workspace_bytes(...) bytes
+ *
+ * grad_k and grad_v sum over the query heads of a key head.  A query that sees
+ * no key has a zero gradient, and so has a key that no query sees.  Returns a
+ * GDR_* status.
+ */
+int gdr_attn_backward(int dtype, int B, int Tq, int Tk, int Hq, int Hkv, int d, int window, int sinks,
+                      float scale, const void* q, const void* k, const void* v, const void* o,
+                      const float* lse, const void* grad_o, void* grad_q, void* grad_k, void* grad_v,
+                      void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace gdr_attn_backward needs (0 when the arguments are
+ * invalid or nothing has to be computed). */
+size_t gdr_attn_backward_workspace_bytes(int dtype, int B, int Tq, int Tk, int Hq, int Hkv, int d,
+                                         int window, int sinks);
+
+/*
+ * The paged key-value cache of the decode step: a pool of num_pages pages of
+ * page_size positions (a power of two up to 65536), each holding every key
+ * head's keys or values,
+ *
+ *   k_pages, v_pages [num_pages, Hkv, page_size, d]   dtype
+ *   page_table       [B, max_pages] int32, DEVICE: position p of sequence b is
+ *                    slot p % page_size of page page_table[b, p / page_size];
+ *                    entries past the sequence are not read
+ *   lengths          [B] int32, DEVICE: positions the cache holds before the
+ *                    call; the caller advances them
+ *
+ * num_pages * Hkv * page_size must stay below 2^31 (rows of a page tensor).
+ */
+
+/*
+ * One decode step of attention for B sequences: the new token's key and value
+ * are written at position lengths[b] and its query attends from there.
+ *
+ *   q, o   [B, Hq, d]    k, v  [B, Hkv, d]   dtype (the new token)
+ *   workspace  at least gdr_attn_decode_workspace_bytes(...) bytes (NULL if
+ *              that is 0): the partial results of long sequences, which are cut
+ *              into parts and joined
+ *
+ * The table and the lengths are device data the host does not read: a sequence
+ * whose length is negative or leaves no room in its table row, or whose new
+ * position has a page outside [0, num_pages), is skipped (o and the pages stay
+ * as they were); other visible positions of a page outside the pool are hidden.
+ * The page of the new position must not be shared with another sequence of
+ * the call; full pages may be.  Returns a GDR_* status.
+ */
+int gdr_attn_decode(int dtype, int B, int Hq, int Hkv, int d, int page_size, int num_pages, int max_pages,
+                    int window, int sinks, float scale, const void* q, const void* k, const void* v,
+                    void* k_pages, void* v_pages, const int* page_table, const int* lengths, void* o,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace gdr_attn_decode needs (0 when the arguments are invalid
+ * or none is needed). */
+size_t gdr_attn_decode_workspace_bytes(int dtype, int B, int Hq, int Hkv, int d, int page_size, int max_pages,
+                                       int window, int sinks);
+
+/*
+ * Writes the keys and values of N packed sequences (a batch of prompts, or
+ * their next parts) to their pages: token i of sequence n goes to position
+ * lengths[n] + i.
+ *
+ *   k, v        [total, Hkv, d]   dtype
+ *   cu_seqlens  [N + 1] int32, DEVICE: non-decreasing token offsets; tokens of
+ *               no sequence are ignored
+ *   lengths, page_table, pages as above (N sequences)
+ *
+ * A token whose position is negative, beyond the table row or on a page
+ * outside [0, num_pages) is not written.  Two tokens with the same place race.
+ * Returns a GDR_* status.
+ */
+int gdr_attn_append(int dtype, int N, int total, int Hkv, int d, int page_size, int num_pages, int max_pages,
+                    const void* k, const void* v, const int* cu_seqlens, const int* lengths, void* k_pages,
+                    void* v_pages, const int* page_table, void* stream);
 
 /* Static, NUL-terminated description of a status code (never NULL). */
 const char* gdr_status_string(int status);
