@@ -25,12 +25,12 @@ int common_checks(int dtype, int Hq, int Hkv, int d, int window, int sinks) {
     return GDR_OK;
 }
 
-// Token and row counts stay in an int with room for a tile past the end, and
-// no tensor passes 2^40 elements.
+// Rows of one sequence (tokens x heads) stay below 2^29 and heads at 2^15, so
+// that offsets inside a tile and row numbers fit 32 bits; no tensor passes
+// 2^40 elements.
 bool sizes_ok(long long B, long long T, long long H, long long d) {
     const long long lim = 1LL << 40;
-    if (T > INT_MAX - 4096 || B * H > INT_MAX / 8) return false;
-    if (H > 0 && T > (INT_MAX - 4096) / H) return false;
+    if (T >= (1 << 29) || H > (1 << 15) || T * H >= (1 << 29) || B * H > INT_MAX / 8) return false;
     if (T * H > 0 && B > lim / (T * H * d)) return false;
     return true;
 }

@@ -31,14 +31,14 @@ constexpr int kRows = 32 * kWaves;  // rows of a dq workgroup
 constexpr int kSegRows = 512;       // rows of one sink segment
 
 struct BwdArgs {
-    int B, Tq, Tk, Hq, Hkv, G;
+    int B, Tq, Tk, Hq, Hkv;
+    FastDiv G;
     int window, sinks;
     float scale;
     int rows, pitch;          // rows of a (sequence, key head); pitch of the row statistics
     int key_blocks, row_tiles;
     int sink_tiles, segs;     // 32-key tiles that hold sinks, segments of each (at most)
-    float* lse2;              // [B Hkv, pitch]: lse log2 e
-    float* delta;             // [B Hkv, pitch]
+    float* stats;             // [B Hkv, 2, pitch]: lse log2 e, then delta
     float* part;              // [B Hkv, sink_tiles, 1 + segs, 2, 32, d]
 };
 
@@ -46,9 +46,9 @@ struct BwdArgs {
 // no window, causally: [lo, hi).
 __device__ __forceinline__ void rows_of(const BwdArgs& a, int j0, int j1, int& lo, int& hi) {
     const int off = a.Tk - a.Tq;
-    lo = max(0, j0 - off) * a.G;
+    lo = max(0, j0 - off) * a.G.d;
     const int last = a.window ? min(a.Tq - 1, j1 + a.window - 1 - off) : a.Tq - 1;
-    hi = max(lo, (last + 1) * a.G);
+    hi = max(lo, (last + 1) * a.G.d);
 }
 
 // Row statistics in row order: lse in base 2 and delta, 16 lanes per row.
@@ -71,29 +71,29 @@ __global__ __launch_bounds__(256) void stats_kernel(BwdArgs a, const T* __restri
     if (l16) return;
     const size_t tok = i / a.Hq;
     const int head = static_cast<int>(i - tok * a.Hq), b = static_cast<int>(tok / a.Tq);
-    const size_t at = (static_cast<size_t>(b) * a.Hkv + head / a.G) * a.pitch +
-                      (tok - static_cast<size_t>(b) * a.Tq) * a.G + head % a.G;
-    a.lse2[at] = lse[i] * kLog2e;
-    a.delta[at] = s;
+    const size_t at = (static_cast<size_t>(b) * a.Hkv + a.G(head)) * 2 * a.pitch +
+                      (tok - static_cast<size_t>(b) * a.Tq) * a.G.d + (head - a.G(head) * a.G.d);
+    a.stats[at] = lse[i] * kLog2e;
+    a.stats[at + a.pitch] = s;
 }
 
 // What a wave does when a non-finite value met its sums (a hidden pair has
 // weight 0, and 0 times an infinity or NaN is NaN): its keys' gradients row by
 // row, hidden pairs left out.  A lane holds half of its key's channels.
 template <typename T, int D>
-__device__ __noinline__ void exact_keys(const BwdArgs& a, int b, int hk, int key, int off, int lo, int hi, const T* q,
+__device__ __forceinline__ void exact_keys(const BwdArgs& a, int b, int hk, int key, int off, int lo, int hi, const T* q,
                                         const T* k, const T* v, const T* go, float* dk, float* dv, int h2) {
     constexpr int N = D / 2;
     const Mask mask{a.window, a.sinks};
     const size_t krow = ((static_cast<size_t>(b) * a.Tk + min(key, a.Tk - 1)) * a.Hkv + hk) * D;
     const float c = a.scale * kLog2e;
-    const size_t stat = (static_cast<size_t>(b) * a.Hkv + hk) * a.pitch;
+    const float* stat = a.stats + (static_cast<size_t>(b) * a.Hkv + hk) * 2 * a.pitch;
 #pragma unroll 1
     for (int e = 0; e < N; ++e) dk[e] = dv[e] = 0.f;
 #pragma unroll 1
     for (int r = lo; r < hi; ++r) {
-        const int i = r / a.G;
-        const size_t qrow = ((static_cast<size_t>(b) * a.Tq + i) * a.Hq + hk * a.G + (r - i * a.G)) * D;
+        const int i = a.G(r);
+        const size_t qrow = ((static_cast<size_t>(b) * a.Tq + i) * a.Hq + hk * a.G.d + (r - i * a.G.d)) * D;
         float s = 0.f, dp = 0.f;
 #pragma unroll 1
         for (int e = N * h2; e < N * h2 + N; ++e) {
@@ -103,7 +103,7 @@ __device__ __noinline__ void exact_keys(const BwdArgs& a, int b, int hk, int key
         s += other_half(s);
         dp += other_half(dp);
         if (!mask.sees(i + off, key)) continue;
-        const float p = ex2(fmaf(s, c, -a.lse2[stat + r])), ds = p * (dp - a.delta[stat + r]);
+        const float p = ex2(fmaf(s, c, -stat[r])), ds = p * (dp - stat[a.pitch + r]);
 #pragma unroll 1
         for (int e = 0; e < N; ++e) {
             dk[e] = fmaf(ds, Elem<T>::load(q + qrow + N * h2 + e), dk[e]);
@@ -116,19 +116,21 @@ template <typename T, int D, int WAVES> struct DkdvCfg {
     static constexpr int BM = 32;  // rows of a step
     static constexpr int kTile = BM * D * static_cast<int>(sizeof(T));
     static constexpr int kBuf = 2 * kTile;    // Q and dO (addresses are xor-ed: a power of two)
-    static constexpr int kStat = 2 * kBuf;    // then lse2 and delta, 256 bytes for each buffer
-    static constexpr int kLds = 2 * kBuf + 512;
+    static constexpr int kStat = 2 * kBuf;    // then lse2 and delta of each buffer, 32 rows by 32 rows
+    static constexpr int kStatBuf = 8 * BM;
+    static constexpr int kLds = kStat + 2 * kStatBuf;
 };
 
 // WAVES = 4: 128 keys of one key head, every row that sees them through the
 // window.  WAVES = 1 (sinks): 32 sink keys, one segment of the rows past it.
 template <typename T, int D, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, 1) void dkdv_kernel(BwdArgs a, const T* __restrict__ q,
+__global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && WAVES == 4 ? 2 : 1) void dkdv_kernel(BwdArgs a, const T* __restrict__ q,
                                                              const T* __restrict__ k, const T* __restrict__ v,
                                                              const T* __restrict__ go, T* __restrict__ gk,
                                                              T* __restrict__ gv) {
     using C = DkdvCfg<T, D, WAVES>;
-    constexpr int KS = D / 16, DT = D / 32, BM = C::BM;
+    using L = Tile<T, D>;
+    constexpr int KS = D / 16, DT = D / 32, BM = C::BM, NM = BM / 32;
     constexpr bool kSeg = WAVES == 1;
     extern __shared__ unsigned char smem[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h2 = lane >> 5;
@@ -161,6 +163,9 @@ __global__ __launch_bounds__(64 * WAVES, 1) void dkdv_kernel(BwdArgs a, const T*
     }
     if (kSeg && lo >= hi) return;
     const bool wave_live = j0 < a.Tk;
+    // this lane's key is visible to rows [key_lo, key_hi) of [lo, hi)
+    const int key_lo = min(a.Tq, max(0, key - off)) * a.G.d;
+    const int key_hi = a.window == 0 || key < a.sinks ? hi : min(hi, min(a.Tq, max(0, key + a.window - off)) * a.G.d);
 
     const size_t kstride = static_cast<size_t>(a.Hkv) * D;
     const size_t k0 = (static_cast<size_t>(b) * a.Tk * a.Hkv + hk) * D;
@@ -177,17 +182,20 @@ __global__ __launch_bounds__(64 * WAVES, 1) void dkdv_kernel(BwdArgs a, const T*
 #pragma unroll
     for (int t = 0; t < DT; ++t) dk[t] = dv[t] = zero16();
     const float c = a.scale * kLog2e;
-    const size_t stat = static_cast<size_t>(head) * a.pitch;
-    const size_t q0 = (static_cast<size_t>(b) * a.Tq * a.Hq + static_cast<size_t>(hk) * a.G) * D;
+    const float* stat = a.stats + static_cast<size_t>(head) * 2 * a.pitch;
+    const size_t q0 = (static_cast<size_t>(b) * a.Tq * a.Hq + static_cast<size_t>(hk) * a.G.d) * D;
 
     auto fetch = [&](int i) {
         unsigned char* buf = smem + (i & 1) * C::kBuf;
-        const int r0 = lo + BM * i;
-        copy_rows<T, D, BM, WAVES>(buf, q + q0, a.Hq, a.G, r0, a.rows - 1, wave, lane);
-        copy_rows<T, D, BM, WAVES>(buf + C::kTile, go + q0, a.Hq, a.G, r0, a.rows - 1, wave, lane);
-        if (wave == 0) {  // lanes 0..31: lse2, 32..63: delta
-            const float* src = (h2 ? a.delta : a.lse2) + stat + min(r0 + (lane & 31), a.rows - 1);
-            copy_words(smem + C::kStat + (i & 1) * 256, src);
+        const int r0 = lo + BM * i, i0 = a.G(r0);
+        const size_t base = q0 + static_cast<size_t>(i0) * a.Hq * D;
+        copy_rows<T, D, BM, WAVES>(buf, q + base, buf + C::kTile, go + base, wave, lane, [&](int r) {
+            const int row = min(r0 + r, a.rows - 1), y = a.G(row);
+            return ((y - i0) * a.Hq + (row - y * a.G.d)) * D;
+        });
+        if (wave < NM) {  // lanes 0..31: lse2, 32..63: delta
+            const int r = min(32 * wave + (lane & 31), a.rows - 1 - r0);
+            copy_words(smem + C::kStat + (i & 1) * C::kStatBuf + 256 * wave, stat + r0, 4u * (h2 * a.pitch + r));
         }
     };
     const int n = (hi - lo + BM - 1) / BM;
@@ -199,50 +207,69 @@ __global__ __launch_bounds__(64 * WAVES, 1) void dkdv_kernel(BwdArgs a, const T*
         if (i + 1 < n) fetch(i + 1);
         const int buf = (i & 1) * C::kBuf, rb = rb0 + buf, cb = cb0 + buf;
         const int r0 = lo + BM * i;
-        const int p0 = r0 / a.G + off, p1 = min(r0 + BM - 1, hi - 1) / a.G + off;
+        const int p0 = a.G(r0) + off, p1 = a.G(min(r0 + BM - 1, hi - 1)) + off;
         if (!wave_live || mask.none(p0, p1, j0, j1)) continue;
-        f32x16 s = zero16(), dp = zero16();
+        const float* st = reinterpret_cast<const float*>(smem + C::kStat + (i & 1) * C::kStatBuf) + 4 * h2;
+        const bool whole = mask.all(p0, p1, j0, j0 + 31) && r0 + BM <= hi;
 #pragma unroll
-        for (int e = 0; e < KS; ++e) s = mma32(RowRead<T, D>::get(smem, rb, e, 0), kf[e], s);
+        for (int w = 0; w < NM; ++w) {
+            // P: registers of S as they stand are the B operand of dV
+            f32x16 s = zero16();
 #pragma unroll
-        for (int e = 0; e < KS; ++e) dp = mma32(RowRead<T, D>::get(smem, rb, e, C::kTile), vf[e], dp);
-        const float* st = reinterpret_cast<const float*>(smem + C::kStat + (i & 1) * 256) + 4 * h2;
-#pragma unroll
-        for (int r = 0; r < 16; r += 4) {
-            const f32x4 ls = *reinterpret_cast<const f32x4*>(st + 2 * r);
-            const f32x4 de = *reinterpret_cast<const f32x4*>(st + 32 + 2 * r);
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                s[r + y] = ex2(fmaf(s[r + y], c, -ls[y]));
-                dp[r + y] = s[r + y] * (dp[r + y] - de[y]);
+            for (int e = 0; e < KS; ++e) {
+                s = mma32(RowRead<T, D>::get(smem, rb, e, 32 * w * L::kRow), kf[e], s);
+                if (e % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // at most four fragments ahead: no spills
             }
+#pragma unroll
+            for (int r = 0; r < 16; r += 4) {
+                const f32x4 ls = *reinterpret_cast<const f32x4*>(st + 64 * w + 2 * r);
+#pragma unroll
+                for (int y = 0; y < 4; ++y) s[r + y] = ex2(fmaf(s[r + y], c, -ls[y]));
+            }
+            if (!whole) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int row = r0 + 32 * w + row32(r, h2);
+                    if (row < key_lo || row >= key_hi) s[r] = 0.f;
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            {
+                frag_t<T> pf[2] = {pack_regs<T>(s, 0), pack_regs<T>(s, 1)};
+#pragma unroll
+                for (int t = 0; t < DT; ++t)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+                        dv[t] = mma32(ColRead<T, D>::get(smem, cb + C::kTile, t, 2 * w + u), pf[u], dv[t]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            f32x16 dp = zero16();
+            const int rb2 = again(rb), cb2 = again(cb);
+#pragma unroll
+            for (int e = 0; e < KS; ++e) {
+                dp = mma32(RowRead<T, D>::get(smem, rb2, e, C::kTile + 32 * w * L::kRow), vf[e], dp);
+                if (e % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+            }
+#pragma unroll
+            for (int r = 0; r < 16; r += 4) {
+                const f32x4 de = *reinterpret_cast<const f32x4*>(st + 64 * w + 32 + 2 * r);
+#pragma unroll
+                for (int y = 0; y < 4; ++y) dp[r + y] = s[r + y] * (dp[r + y] - de[y]);
+            }
+            if (!whole) {  // a hidden pair's weight is 0, its dP may be anything
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    if (s[r] == 0.f) dp[r] = 0.f;
+            }
+            {
+                frag_t<T> df[2] = {pack_regs<T>(dp, 0), pack_regs<T>(dp, 1)};
+#pragma unroll
+                for (int t = 0; t < DT; ++t)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) dk[t] = mma32(ColRead<T, D>::get(smem, cb2, t, 2 * w + u), df[u], dk[t]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
         }
-        if (!(mask.all(p0, p1, j0, j0 + 31) && r0 + BM <= hi)) {
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int row = r0 + row32(r, h2);
-                if (row >= hi || !mask.sees(row / a.G + off, key)) s[r] = dp[r] = 0.f;
-            }
-        }
-        frag_t<T> pf[2], df[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            float w[8], z[8];
-#pragma unroll
-            for (int y = 0; y < 8; ++y) {
-                w[y] = s[8 * u + y];
-                z[y] = dp[8 * u + y];
-            }
-            pf[u] = pack8<T>(w);
-            df[u] = pack8<T>(z);
-        }
-#pragma unroll
-        for (int t = 0; t < DT; ++t)
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                dv[t] = mma32(ColRead<T, D>::get(smem, cb + C::kTile, t, u), pf[u], dv[t]);
-                dk[t] = mma32(ColRead<T, D>::get(smem, cb, t, u), df[u], dk[t]);
-            }
     }
     if (!wave_live) return;
 
@@ -288,7 +315,7 @@ __global__ __launch_bounds__(64 * WAVES, 1) void dkdv_kernel(BwdArgs a, const T*
         }
 }
 
-// Adds the parts of one sink tile in order: one workgroup per (head, tile).
+// Adds the parts of one sink tile in order, four elements a thread.
 template <typename T, int D>
 __global__ __launch_bounds__(256) void sink_join_kernel(BwdArgs a, T* __restrict__ gk, T* __restrict__ gv) {
     const int head = blockIdx.x / a.sink_tiles, tile = blockIdx.x % a.sink_tiles;
@@ -298,20 +325,18 @@ __global__ __launch_bounds__(256) void sink_join_kernel(BwdArgs a, T* __restrict
     rows_of(a, m0, min(m0 + kKeys, a.Tk) - 1, lo, end);
     const int parts = 1 + (a.rows > end ? (a.rows - end - 1) / kSegRows + 1 : 0);
     const float* part = a.part + (static_cast<size_t>(head) * a.sink_tiles + tile) * (1 + a.segs) * 64 * D;
-    for (int i = threadIdx.x; i < 64 * D / 4; i += 256) {
-        f32x4 s = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-        for (int p = 0; p < parts; ++p) s += *reinterpret_cast<const f32x4*>(part + static_cast<size_t>(p) * 64 * D + 4 * i);
-        const int row = i / (D / 4), ch = 4 * (i % (D / 4)), key = 32 * tile + (row & 31);
-        if (key >= a.Tk) continue;
-        T* dst = (row >= 32 ? gv : gk) + ((static_cast<size_t>(b) * a.Tk + key) * a.Hkv + hk) * D + ch;
-        store4<T>(dst, s[0], s[1], s[2], s[3]);
-    }
+    const int i = blockIdx.y * 256 + threadIdx.x, row = i / (D / 4), ch = 4 * (i % (D / 4)), key = 32 * tile + (row & 31);
+    if (key >= a.Tk) return;
+    f32x4 s = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+    for (int p = 0; p < parts; ++p) s += *reinterpret_cast<const f32x4*>(part + static_cast<size_t>(p) * 64 * D + 4 * i);
+    T* dst = (row >= 32 ? gv : gk) + ((static_cast<size_t>(b) * a.Tk + key) * a.Hkv + hk) * D + ch;
+    store4<T>(dst, s[0], s[1], s[2], s[3]);
 }
 
 // As exact_keys, for one wave's rows of dQ.
 template <typename T, int D>
-__device__ __noinline__ void exact_dq(const BwdArgs& a, Mask mask, int pos, bool live, int wp1, float lse2, float delta,
+__device__ __forceinline__ void exact_dq(const BwdArgs& a, Mask mask, int pos, bool live, int wp1, float lse2, float delta,
                                       const T* q, const T* go, const T* k, const T* v, size_t stride, T* gq, int h2) {
     constexpr int N = D / 2;
     const float c = a.scale * kLog2e;
@@ -345,7 +370,7 @@ template <typename T, int D> struct DqCfg {
 };
 
 template <typename T, int D>
-__global__ __launch_bounds__(64 * kWaves, 1) void dq_kernel(BwdArgs a, const T* __restrict__ q, const T* __restrict__ k,
+__global__ __launch_bounds__(64 * kWaves, sizeof(T) == 2 ? 2 : 1) void dq_kernel(BwdArgs a, const T* __restrict__ q, const T* __restrict__ k,
                                                             const T* __restrict__ v, const T* __restrict__ go,
                                                             T* __restrict__ gq) {
     using C = DqCfg<T, D>;
@@ -367,11 +392,11 @@ __global__ __launch_bounds__(64 * kWaves, 1) void dq_kernel(BwdArgs a, const T* 
     const int wr0 = min(row0 + 32 * wave, a.rows - 1), wr1 = min(row0 + 32 * wave + 31, a.rows - 1);
     const bool live = row0 + 32 * wave + (lane & 31) < a.rows, wave_live = row0 + 32 * wave < a.rows;
     const int row = min(row0 + 32 * wave + (lane & 31), a.rows - 1);
-    const int qi = row / a.G, pos = qi + off;
-    const int wp0 = __builtin_amdgcn_readfirstlane(wr0 / a.G + off);
-    const int wp1 = __builtin_amdgcn_readfirstlane(wr1 / a.G + off);
-    const size_t qrow = (static_cast<size_t>(b) * a.Tq + qi) * a.Hq + static_cast<size_t>(hk) * a.G + (row - qi * a.G);
-    const int p0 = row0 / a.G + off, p1 = min(row0 + kRows - 1, a.rows - 1) / a.G + off;
+    const int qi = a.G(row), pos = qi + off;
+    const int wp0 = __builtin_amdgcn_readfirstlane(a.G(wr0) + off);
+    const int wp1 = __builtin_amdgcn_readfirstlane(a.G(wr1) + off);
+    const size_t qrow = (static_cast<size_t>(b) * a.Tq + qi) * a.Hq + static_cast<size_t>(hk) * a.G.d + (row - qi * a.G.d);
+    const int p0 = a.G(row0) + off, p1 = a.G(min(row0 + kRows - 1, a.rows - 1)) + off;
     const int w_lo = a.window ? max(0, p0 - a.window + 1) : 0;
     const int t_lo = w_lo / BN, t_hi = p1 < 0 ? -1 : p1 / BN;
     const int t_sink = a.window ? min((a.sinks + BN - 1) / BN, t_lo) : 0;
@@ -383,8 +408,8 @@ __global__ __launch_bounds__(64 * kWaves, 1) void dq_kernel(BwdArgs a, const T* 
         qf[s] = load8(q + qrow * D + 8 * h2 + 16 * s);
         gf[s] = load8(go + qrow * D + 8 * h2 + 16 * s);
     }
-    const float lse2 = a.lse2[static_cast<size_t>(head) * a.pitch + row];
-    const float delta = a.delta[static_cast<size_t>(head) * a.pitch + row];
+    const float lse2 = a.stats[static_cast<size_t>(head) * 2 * a.pitch + row];
+    const float delta = a.stats[(static_cast<size_t>(head) * 2 + 1) * a.pitch + row];
     const float c = a.scale * kLog2e;
     f32x16 dq[DT];
 #pragma unroll
@@ -396,8 +421,8 @@ __global__ __launch_bounds__(64 * kWaves, 1) void dq_kernel(BwdArgs a, const T* 
     auto fetch = [&](int i) {
         unsigned char* buf = smem + (i & 1) * 2 * C::kTile;
         const int j0 = tile_of(i) * BN;
-        copy_tile<T, D, BN, kWaves>(buf, kbase, kstride, j0, a.Tk - 1, wave, lane);
-        copy_tile<T, D, BN, kWaves>(buf + C::kTile, vbase, kstride, j0, a.Tk - 1, wave, lane);
+        copy_rows<T, D, BN, kWaves>(buf, kbase + j0 * kstride, buf + C::kTile, vbase + j0 * kstride, wave, lane,
+                                    [&](int r) { return min(r, a.Tk - 1 - j0) * a.Hkv * D; });
     };
     const int rb0 = RowRead<T, D>::base(lane & 31, h2), cb0 = ColRead<T, D>::base(lane);
     if (n > 0) fetch(0);
@@ -460,11 +485,11 @@ BwdArgs make_args(int B, int Tq, int Tk, int Hq, int Hkv, int window, int sinks,
     a.Tk = Tk;
     a.Hq = Hq;
     a.Hkv = Hkv;
-    a.G = Hq / Hkv;
+    a.G = FastDiv(Hq / Hkv);
     a.window = window;
     a.sinks = sinks;
     a.scale = scale;
-    a.rows = Tq * a.G;
+    a.rows = Tq * a.G.d;
     a.pitch = (a.rows + 3) / 4 * 4;
     a.key_blocks = (Tk + kKeys - 1) / kKeys;
     a.row_tiles = (a.rows + kRows - 1) / kRows;
@@ -488,7 +513,7 @@ hipError_t launch(const BwdArgs& a, const void* q_, const void* k_, const void* 
     const unsigned long long kv_blocks = heads * a.key_blocks, q_blocks = heads * a.row_tiles;
     const unsigned long long seg_blocks = heads * a.sink_tiles * a.segs, join_blocks = heads * a.sink_tiles;
     if (!grid_fits(stat_blocks, 256) || !grid_fits(kv_blocks, 64 * kWaves) || !grid_fits(q_blocks, 64 * kWaves) ||
-        !grid_fits(seg_blocks, 64) || !grid_fits(join_blocks, 256))
+        !grid_fits(seg_blocks, 64) || !grid_fits(join_blocks * (D / 16), 256))
         return hipErrorInvalidConfiguration;
     using CK = DkdvCfg<T, D, kWaves>;
     using CQ = DqCfg<T, D>;
@@ -505,7 +530,7 @@ hipError_t launch(const BwdArgs& a, const void* q_, const void* k_, const void* 
         if (seg_blocks)
             hipLaunchKernelGGL((dkdv_kernel<T, D, 1>), dim3(static_cast<unsigned>(seg_blocks)), dim3(64), CK::kLds, st, a,
                                q, k, v, go, static_cast<T*>(gk), static_cast<T*>(gv));
-        hipLaunchKernelGGL((sink_join_kernel<T, D>), dim3(static_cast<unsigned>(join_blocks)), dim3(256), 0, st, a,
+        hipLaunchKernelGGL((sink_join_kernel<T, D>), dim3(static_cast<unsigned>(join_blocks), 64 * D / 4 / 256), dim3(256), 0, st, a,
                            static_cast<T*>(gk), static_cast<T*>(gv));
     }
     if (q_blocks)
@@ -529,9 +554,8 @@ hipError_t launch_attn_backward(int dtype, int B, int Tq, int Tk, int Hq, int Hk
                                 hipStream_t st) {
     attn::BwdArgs a = attn::make_args(B, Tq, Tk, Hq, Hkv, window, sinks, scale);
     const size_t heads = static_cast<size_t>(B) * Hkv;
-    a.lse2 = ws;
-    a.delta = ws + heads * a.pitch;
-    a.part = a.delta + heads * a.pitch;
+    a.stats = ws;
+    a.part = ws + heads * 2 * a.pitch;
     auto* f = dtype == GDR_DTYPE_F32 ? (d == 64 ? attn::launch<float, 64> : attn::launch<float, 128>)
                                      : (d == 64 ? attn::launch<bf16_t, 64> : attn::launch<bf16_t, 128>);
     return f(a, q, k, v, o, lse, go, gq, gk, gv, st);

@@ -96,6 +96,14 @@ template <> __device__ __forceinline__ f32x8 pack8<float>(const float (&x)[8]) {
     return r;
 }
 
+// Registers 8u .. 8u+7 of an accumulator tile as an operand fragment.
+template <typename T> __device__ __forceinline__ frag_t<T> pack_regs(const f32x16& s, int u) {
+    float x[8];
+#pragma unroll
+    for (int y = 0; y < 8; ++y) x[y] = s[8 * u + y];
+    return pack8<T>(x);
+}
+
 template <typename T> __device__ __forceinline__ void store4(T* p, float a, float b, float c, float d);
 template <> __device__ __forceinline__ void store4<float>(float* p, float a, float b, float c, float d) {
     *reinterpret_cast<f32x4*>(p) = f32x4{a, b, c, d};
@@ -109,8 +117,32 @@ template <> __device__ __forceinline__ void store4<bf16_t>(bf16_t* p, float a, f
 __device__ __forceinline__ float ex2(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ float lg2(float x) { return __builtin_amdgcn_logf(x); }
 
+// n / d for 0 <= n < 2^31 by one multiplication: with 2^s >= d the smallest
+// such power and m = ceil(2^(31+s) / d), n m / 2^(31+s) exceeds n / d by less
+// than n / 2^31 / d < 1 / d, so its floor is exact.
+struct FastDiv {
+    uint32_t mul, shift;
+    int d;
+    __host__ FastDiv(int div = 1) : d(div) {
+        int s = 0;
+        while ((1ll << s) < div) ++s;
+        mul = static_cast<uint32_t>(((1ull << (31 + s)) + div - 1) / div);
+        shift = 31 + s;
+    }
+    __device__ __forceinline__ int operator()(int n) const {
+        return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(n)) * mul) >> shift);
+    }
+};
+
 // x of the lane 32 away.
 __device__ __forceinline__ float other_half(float x) { return __shfl_xor(x, 32); }
+
+// x as a value the compiler knows nothing about: addresses formed from it are
+// formed again instead of being kept in registers from their last use.
+__device__ __forceinline__ int again(int x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
 
 // ---------------------------------------------------------------- LDS tiles
 //
@@ -194,55 +226,38 @@ template <int D> struct ColRead<float, D> {
     }
 };
 
-// Copies rows row0 .. row0 + ROWS - 1 (clamped to last_row; rows `stride`
-// elements apart from `base`) into an LDS tile, straight from global memory:
-// one instruction of a wave fills 1024 consecutive bytes of the tile, each
-// lane fetching the unit that belongs at its place.  The caller waits for
-// the copies (vmcnt) and passes a barrier before reading them.
-template <typename T, int D, int ROWS, int WAVES>
-__device__ __forceinline__ void copy_tile(unsigned char* tile, const T* base, size_t stride, int row0,
-                                          int last_row, int wave, int lane) {
-    using L = Tile<T, D>;
-    constexpr int kPer = 1024 / L::kRow > 0 ? 1024 / L::kRow : 1;  // rows of one instruction
-    static_assert(1024 % L::kRow == 0, "an instruction fills whole rows");
-    constexpr int kInstr = ROWS / kPer;
-    static_assert(kInstr % WAVES == 0, "every wave issues the same number of copies");
-#pragma unroll
-    for (int j = 0; j < kInstr / WAVES; ++j) {
-        const int jj = wave + j * WAVES;
-        const int r = jj * kPer + lane / L::kUnits;
-        const int u = (lane % L::kUnits) ^ L::swz(r);  // the unit that belongs there
-        const int row = min(row0 + r, last_row);
-        const T* src = base + static_cast<size_t>(row) * stride + u * (16 / sizeof(T));
-        __builtin_amdgcn_global_load_lds(
-            reinterpret_cast<const uint32_t __attribute__((address_space(1)))*>(
-                reinterpret_cast<uintptr_t>(src)),
-            (__attribute__((address_space(3))) uint32_t*)(tile + jj * 1024), 16, 0, 0);
-    }
+// One instruction of a wave: 1024 bytes from `base` + the lanes' offsets into
+// 1024 consecutive bytes of LDS, lane by lane.
+__device__ __forceinline__ void copy_1k(unsigned char* lds, const void* base, uint32_t off) {
+    const auto* src = static_cast<const unsigned char*>(base) + off;
+    __builtin_amdgcn_global_load_lds(
+        reinterpret_cast<const uint32_t __attribute__((address_space(1)))*>(reinterpret_cast<uintptr_t>(src)),
+        (__attribute__((address_space(3))) uint32_t*)(lds), 16, 0, 0);
 }
 
-// The same for rows of packed query heads: row = query * G + head, at base +
-// (query * Hq + head) * D.
-template <typename T, int D, int ROWS, int WAVES>
-__device__ __forceinline__ void copy_rows(unsigned char* tile, const T* base, int Hq, int G, int row0,
-                                          int last_row, int wave, int lane) {
+// Copies ROWS rows of two tensors of one layout into two LDS tiles, straight
+// from global memory: an instruction fills 1024 / row bytes rows, each lane
+// fetching the unit that belongs at its place.  offset(r) is the element
+// offset of row r of the tile from the (wave-uniform) bases.  The caller waits
+// for the copies (vmcnt) and passes a barrier before reading them.
+template <typename T, int D, int ROWS, int WAVES, typename OffsetFn>
+__device__ __forceinline__ void copy_rows(unsigned char* tile_a, const T* a, unsigned char* tile_b, const T* b,
+                                          int wave, int lane, OffsetFn offset) {
     using L = Tile<T, D>;
     constexpr int kPer = 1024 / L::kRow, kInstr = ROWS / kPer;
     static_assert(1024 % L::kRow == 0 && kInstr % WAVES == 0, "whole rows, the same number for every wave");
 #pragma unroll
     for (int j = 0; j < kInstr / WAVES; ++j) {
-        const int jj = wave + j * WAVES;
-        const int r = jj * kPer + lane / L::kUnits;
-        const int u = (lane % L::kUnits) ^ L::swz(r);
-        const int row = min(row0 + r, last_row), i = row / G;
-        const T* src = base + (static_cast<size_t>(i) * Hq + (row - i * G)) * D + u * (16 / sizeof(T));
-        __builtin_amdgcn_global_load_lds(
-            reinterpret_cast<const uint32_t __attribute__((address_space(1)))*>(reinterpret_cast<uintptr_t>(src)),
-            (__attribute__((address_space(3))) uint32_t*)(tile + jj * 1024), 16, 0, 0);
+        const int jj = wave + j * WAVES, r = jj * kPer + lane / L::kUnits;
+        const uint32_t u = (lane % L::kUnits) ^ L::swz(r);  // the unit that belongs there
+        const uint32_t off = static_cast<uint32_t>(offset(r)) * sizeof(T) + u * 16;
+        copy_1k(tile_a + jj * 1024, a, off);
+        copy_1k(tile_b + jj * 1024, b, off);
     }
 }
-// One word per lane of a wave into 256 consecutive bytes of LDS.
-__device__ __forceinline__ void copy_words(unsigned char* lds, const float* src) {
+// One word per lane, into 256 consecutive bytes.
+__device__ __forceinline__ void copy_words(unsigned char* lds, const float* base, uint32_t off) {
+    const auto* src = reinterpret_cast<const unsigned char*>(base) + off;
     __builtin_amdgcn_global_load_lds(
         reinterpret_cast<const uint32_t __attribute__((address_space(1)))*>(reinterpret_cast<uintptr_t>(src)),
         (__attribute__((address_space(3))) uint32_t*)(lds), 4, 0, 0);

@@ -31,7 +31,8 @@ constexpr int kWaves = 4;
 constexpr int kRows = 32 * kWaves;  // query rows of a workgroup
 
 struct PrefillArgs {
-    int B, Tq, Tk, Hq, Hkv, G;  // packed: B sequences, Tq = longest, Tk unused
+    int B, Tq, Tk, Hq, Hkv;  // packed: B sequences, Tq = longest, Tk unused
+    FastDiv G;
     int window, sinks;
     float scale;
     int tiles;  // row tiles of a (sequence, key head)
@@ -48,7 +49,7 @@ template <typename T, int D> struct PrefillCfg {
 // The rows of one wave key by key, hidden keys left out: what a wave does when
 // a non-finite value meets its sums.  A lane holds half of its row's channels.
 template <typename T, int D>
-__device__ __noinline__ void exact_rows(Mask mask, int pos, bool live, int wp0, int wp1, float c, bool neg,
+__device__ __forceinline__ void exact_rows(Mask mask, int pos, bool live, int wp0, int wp1, float c, bool neg,
                                         const T* q, const T* k, const T* v, size_t stride, T* o, float* lse,
                                         int h2) {
     constexpr int N = D / 2;
@@ -119,7 +120,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prefill_kernel(PrefillArgs a, 
         q0 = qa;
         k0 = ka;
     }
-    const int G = a.G, nrows = Tq * G, row0 = tile * kRows;
+    const FastDiv G = a.G;
+    const int nrows = Tq * G.d, row0 = tile * kRows;
     if (row0 >= nrows) return;
     const int off = Tk - Tq;
     const Mask mask{a.window, a.sinks};
@@ -130,13 +132,13 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prefill_kernel(PrefillArgs a, 
     const bool live = row0 + 32 * wave + (lane & 31) < nrows;
     const bool wave_live = row0 + 32 * wave < nrows;
     const int row = min(row0 + 32 * wave + (lane & 31), nrows - 1);
-    const int qi = row / G, g = row - qi * G, pos = qi + off;
-    const int wp0 = __builtin_amdgcn_readfirstlane(wr0 / G + off);
-    const int wp1 = __builtin_amdgcn_readfirstlane(wr1 / G + off);
-    const size_t qrow = (q0 + qi) * a.Hq + static_cast<size_t>(hk) * G + g;
+    const int qi = G(row), g = row - qi * G.d, pos = qi + off;
+    const int wp0 = __builtin_amdgcn_readfirstlane(G(wr0) + off);
+    const int wp1 = __builtin_amdgcn_readfirstlane(G(wr1) + off);
+    const size_t qrow = (q0 + qi) * a.Hq + static_cast<size_t>(hk) * G.d + g;
 
     // key tiles of the workgroup's rows: the sinks before the window, then the window
-    const int p0 = row0 / G + off, p1 = min(row0 + kRows - 1, nrows - 1) / G + off;
+    const int p0 = G(row0) + off, p1 = G(min(row0 + kRows - 1, nrows - 1)) + off;
     const int win = a.window;
     const int w_lo = win ? max(0, p0 - win + 1) : 0;
     const int t_lo = w_lo / BN, t_hi = p1 < 0 ? -1 : p1 / BN;  // p1 <= Tk - 1
@@ -170,8 +172,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prefill_kernel(PrefillArgs a, 
     auto fetch = [&](int i) {
         unsigned char* buf = smem + (i & 1) * 2 * C::kTileBytes;
         const int j0 = tile_of(i) * BN;
-        copy_tile<T, D, BN, kWaves>(buf, kbase, kstride, j0, Tk - 1, wave, lane);
-        copy_tile<T, D, BN, kWaves>(buf + C::kTileBytes, vbase, kstride, j0, Tk - 1, wave, lane);
+        copy_rows<T, D, BN, kWaves>(buf, kbase + j0 * kstride, buf + C::kTileBytes, vbase + j0 * kstride, wave, lane,
+                                    [&](int r) { return min(r, Tk - 1 - j0) * a.Hkv * D; });
     };
     const int kb0 = RowRead<T, D>::base(lane & 31, h2), vb0 = ColRead<T, D>::base(lane) + C::kTileBytes;
     if (n > 0) fetch(0);
@@ -295,11 +297,11 @@ hipError_t launch_attn_prefill(int dtype, int B, int Tq, int Tk, int Hq, int Hkv
     a.Tk = Tk;
     a.Hq = Hq;
     a.Hkv = Hkv;
-    a.G = Hq / Hkv;
+    a.G = attn::FastDiv(Hq / Hkv);
     a.window = window;
     a.sinks = sinks;
     a.scale = scale;
-    a.tiles = static_cast<int>((static_cast<long long>(Tq) * a.G + attn::kRows - 1) / attn::kRows);
+    a.tiles = static_cast<int>((static_cast<long long>(Tq) * a.G.d + attn::kRows - 1) / attn::kRows);
     a.cu_q = pk.cu_q;
     a.cu_k = pk.cu_k;
     a.total_q = pk.total_q;

@@ -396,7 +396,8 @@ size_t gdr_chunk_backward_workspace_bytes_ranged(int gate, int dtype, int B, int
  * product rounded to bf16; statistics and sums are fp32.  With dtype F32 every
  * operation is fp32.  Every sum runs in a fixed order: repeated calls give
  * identical results.  Tensors as above: dense, row-major, 16-byte aligned
- * (int arrays and lse 4-byte), no output overlapping an input.
+ * (int arrays and lse 4-byte), no output overlapping an input; at most 2^15
+ * heads, and fewer than 2^29 rows (positions x heads) in one sequence.
  * ---------------------------------------------------------------------------
  */
 
