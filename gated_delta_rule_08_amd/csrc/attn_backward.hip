@@ -12,9 +12,14 @@
 // per wave and walks the keys, as the forward does.  Every sum has a fixed
 // order.
 //
+// The first of them, dq_kernel, also forms delta and writes the row statistics
+// the second one reads.
+//
 // Sink keys are seen by every later row, a list far longer than any other
 // key's: those rows are cut into segments of their own (one wave each), whose
-// fp32 partial sums a last kernel adds in order.
+// fp32 partial sums a last kernel adds in order.  Small problems, whose keys
+// alone would leave compute units without work, cut every key's rows in the
+// same way, and the rows of dq_kernel give each wave a quarter of the keys.
 #include "attn_common.h"
 
 namespace gdr {
@@ -28,7 +33,6 @@ __device__ __forceinline__ void tile_barrier() {
 constexpr int kWaves = 4;
 constexpr int kKeys = 32 * kWaves;  // keys of a dkdv workgroup
 constexpr int kRows = 32 * kWaves;  // rows of a dq workgroup
-constexpr int kSegRows = 512;       // rows of one sink segment
 
 struct BwdArgs {
     int B, Tq, Tk, Hq, Hkv;
@@ -37,9 +41,13 @@ struct BwdArgs {
     float scale;
     int rows, pitch;          // rows of a (sequence, key head); pitch of the row statistics
     int key_blocks, row_tiles;
-    int sink_tiles, segs;     // 32-key tiles that hold sinks, segments of each (at most)
+    bool split;               // dq: 32 rows per workgroup, a quarter of the keys per wave
+    int slices;               // parts of every key's rows (small problems; else 1)
+    int sink_tiles, segs;     // 32-key tiles that hold sinks, segments of each (at most; 0 with slices > 1)
+    int seg_rows;
+    int part_tiles, slots;    // key tiles whose gradients come in parts, parts of each (at most)
     float* stats;             // [B Hkv, 2, pitch]: lse log2 e, then delta
-    float* part;              // [B Hkv, sink_tiles, 1 + segs, 2, 32, d]
+    float* part;              // [B Hkv, part_tiles, slots, 2, 32, d]
 };
 
 // Rows (query * G + head) that see keys [j0, j1] through the window or, with
@@ -49,32 +57,7 @@ __device__ __forceinline__ void rows_of(const BwdArgs& a, int j0, int j1, int& l
     lo = max(0, j0 - off) * a.G.d;
     const int last = a.window ? min(a.Tq - 1, j1 + a.window - 1 - off) : a.Tq - 1;
     hi = max(lo, (last + 1) * a.G.d);
-}
-
-// Row statistics in row order: lse in base 2 and delta, 16 lanes per row.
-template <typename T, int D>
-__global__ __launch_bounds__(256) void stats_kernel(BwdArgs a, const T* __restrict__ o, const T* __restrict__ go,
-                                                    const float* __restrict__ lse) {
-    const size_t n = static_cast<size_t>(a.B) * a.Tq * a.Hq;
-    const size_t i = (static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x) >> 4;
-    if (i >= n) return;
-    const int l16 = threadIdx.x & 15;
-    constexpr int N = D / 16;
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < N; e += 4)
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-            s = fmaf(Elem<T>::load(o + i * D + N * l16 + e + x), Elem<T>::load(go + i * D + N * l16 + e + x), s);
-#pragma unroll
-    for (int x = 1; x < 16; x <<= 1) s += __shfl_xor(s, x);
-    if (l16) return;
-    const size_t tok = i / a.Hq;
-    const int head = static_cast<int>(i - tok * a.Hq), b = static_cast<int>(tok / a.Tq);
-    const size_t at = (static_cast<size_t>(b) * a.Hkv + a.G(head)) * 2 * a.pitch +
-                      (tok - static_cast<size_t>(b) * a.Tq) * a.G.d + (head - a.G(head) * a.G.d);
-    a.stats[at] = lse[i] * kLog2e;
-    a.stats[at + a.pitch] = s;
+    if (a.slices > 1 && a.window && j0 < a.sinks) hi = a.rows;  // no segments: the sinks' rows are sliced with the rest
 }
 
 // What a wave does when a non-finite value met its sums (a hidden pair has
@@ -134,7 +117,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && WAVES == 4 ? 2 : 1) v
     constexpr bool kSeg = WAVES == 1;
     extern __shared__ unsigned char smem[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h2 = lane >> 5;
-    const int per = kSeg ? a.sink_tiles * a.segs : a.key_blocks;
+    const int per = kSeg ? a.sink_tiles * a.segs : a.key_blocks * a.slices;
     const int heads = a.B * a.Hkv;
     int bid = blockIdx.x, head, x;
     if (heads % 8 == 0) {  // one head's blocks on one XCD
@@ -145,21 +128,22 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && WAVES == 4 ? 2 : 1) v
         x = bid / heads;
     }
     const int b = head / a.Hkv, hk = head - b * a.Hkv;
-    const int seg = kSeg ? x % a.segs : 0;
-    const int tile = kSeg ? x / a.segs : x * WAVES + wave;  // 32-key tile of this wave
+    const int cuts = kSeg ? a.segs : a.slices, y = x / cuts, cut = x - y * cuts;
+    const int tile = kSeg ? y : y * WAVES + wave;  // 32-key tile of this wave
     const int j0 = 32 * tile, j1 = min(j0 + 31, a.Tk - 1), key = j0 + (lane & 31);
     const int off = a.Tk - a.Tq;
     const Mask mask{a.window, a.sinks};
 
     int lo, hi;
-    if (kSeg) {
-        const int m0 = j0 / kKeys * kKeys;  // the main workgroup's keys: its rows end at hi
-        int end;
-        rows_of(a, m0, min(m0 + kKeys, a.Tk) - 1, lo, end);
-        lo = end + seg * kSegRows;
-        hi = min(a.rows, lo + kSegRows);
-    } else {
-        rows_of(a, x * kKeys, min(x * kKeys + kKeys, a.Tk) - 1, lo, hi);
+    const int m0 = kSeg ? j0 / kKeys * kKeys : y * kKeys;  // the keys of a main workgroup
+    rows_of(a, m0, min(m0 + kKeys, a.Tk) - 1, lo, hi);
+    if (kSeg) {  // past what the main workgroup takes
+        lo = hi + cut * a.seg_rows;
+        hi = min(a.rows, lo + a.seg_rows);
+    } else if (a.slices > 1) {
+        const int len = ((hi - lo + a.slices - 1) / a.slices + 31) / 32 * 32;
+        lo = min(hi, lo + cut * len);
+        hi = min(hi, lo + len);
     }
     if (kSeg && lo >= hi) return;
     const bool wave_live = j0 < a.Tk;
@@ -273,10 +257,10 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && WAVES == 4 ? 2 : 1) v
     }
     if (!wave_live) return;
 
-    // the keys' gradients, or this part of a sink tile's
+    // the keys' gradients, or this part of them
     float* part = nullptr;
-    if (tile < a.sink_tiles)
-        part = a.part + ((static_cast<size_t>(head) * a.sink_tiles + tile) * (1 + a.segs) + (kSeg ? 1 + seg : 0)) * 64 * D;
+    if (tile < a.part_tiles)
+        part = a.part + ((static_cast<size_t>(head) * a.part_tiles + tile) * a.slots + (kSeg ? 1 + cut : cut)) * 64 * D;
     bool bad = false;
 #pragma unroll
     for (int t = 0; t < DT; ++t)
@@ -315,16 +299,16 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && WAVES == 4 ? 2 : 1) v
         }
 }
 
-// Adds the parts of one sink tile in order, four elements a thread.
+// Adds the parts of one key tile in order, four elements a thread.
 template <typename T, int D>
-__global__ __launch_bounds__(256) void sink_join_kernel(BwdArgs a, T* __restrict__ gk, T* __restrict__ gv) {
-    const int head = blockIdx.x / a.sink_tiles, tile = blockIdx.x % a.sink_tiles;
+__global__ __launch_bounds__(256) void join_kernel(BwdArgs a, T* __restrict__ gk, T* __restrict__ gv) {
+    const int head = blockIdx.x / a.part_tiles, tile = blockIdx.x % a.part_tiles;
     const int b = head / a.Hkv, hk = head - b * a.Hkv;
     const int m0 = 32 * tile / kKeys * kKeys;
-    int lo, end;
+    int lo, end, parts = a.slices;
     rows_of(a, m0, min(m0 + kKeys, a.Tk) - 1, lo, end);
-    const int parts = 1 + (a.rows > end ? (a.rows - end - 1) / kSegRows + 1 : 0);
-    const float* part = a.part + (static_cast<size_t>(head) * a.sink_tiles + tile) * (1 + a.segs) * 64 * D;
+    if (a.segs && a.rows > end) parts += (a.rows - end - 1) / a.seg_rows + 1;
+    const float* part = a.part + (static_cast<size_t>(head) * a.part_tiles + tile) * a.slots * 64 * D;
     const int i = blockIdx.y * 256 + threadIdx.x, row = i / (D / 4), ch = 4 * (i % (D / 4)), key = 32 * tile + (row & 31);
     if (key >= a.Tk) return;
     f32x4 s = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -363,18 +347,21 @@ __device__ __forceinline__ void exact_dq(const BwdArgs& a, Mask mask, int pos, b
     for (int e = 0; e < N; ++e) Elem<T>::store(gq + N * h2 + e, dq[e] * a.scale);
 }
 
-template <typename T, int D> struct DqCfg {
-    static constexpr int BN = 32;
+template <typename T, int D, bool SPLIT> struct DqCfg {
+    static constexpr int BN = SPLIT ? 32 * kWaves : 32;  // keys of a step
     static constexpr int kTile = BN * D * static_cast<int>(sizeof(T));
-    static constexpr int kLds = 4 * kTile;
+    static constexpr int kBufs = 4 * kTile <= 128 * 1024 ? 2 : 1;
+    static constexpr int kLds = 2 * kBufs * kTile;
 };
 
-template <typename T, int D>
-__global__ __launch_bounds__(64 * kWaves, sizeof(T) == 2 ? 2 : 1) void dq_kernel(BwdArgs a, const T* __restrict__ q, const T* __restrict__ k,
-                                                            const T* __restrict__ v, const T* __restrict__ go,
-                                                            T* __restrict__ gq) {
-    using C = DqCfg<T, D>;
-    constexpr int BN = C::BN, KS = D / 16, DT = D / 32;
+// 32 rows per wave, or with SPLIT 32 rows per workgroup, each wave a quarter
+// of the keys.
+template <typename T, int D, bool SPLIT>
+__global__ __launch_bounds__(64 * kWaves, sizeof(T) == 2 ? 2 : 1) void dq_kernel(
+    BwdArgs a, const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v, const T* __restrict__ o,
+    const T* __restrict__ go, const float* __restrict__ lse, T* __restrict__ gq) {
+    using C = DqCfg<T, D, SPLIT>;
+    constexpr int BN = C::BN, KS = D / 16, DT = D / 32, kGroup = SPLIT ? 32 : kRows;
     extern __shared__ unsigned char smem[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h2 = lane >> 5;
     const int heads = a.B * a.Hkv, bid = blockIdx.x;
@@ -387,52 +374,65 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(T) == 2 ? 2 : 1) void dq_kernel
         tile = a.row_tiles - 1 - bid / heads;
     }
     const int b = head / a.Hkv, hk = head - b * a.Hkv;
-    const int off = a.Tk - a.Tq, row0 = tile * kRows;
+    const int off = a.Tk - a.Tq, row0 = tile * kGroup, wrow = row0 + (SPLIT ? 0 : 32 * wave);
     const Mask mask{a.window, a.sinks};
-    const int wr0 = min(row0 + 32 * wave, a.rows - 1), wr1 = min(row0 + 32 * wave + 31, a.rows - 1);
-    const bool live = row0 + 32 * wave + (lane & 31) < a.rows, wave_live = row0 + 32 * wave < a.rows;
-    const int row = min(row0 + 32 * wave + (lane & 31), a.rows - 1);
+    const int wr0 = min(wrow, a.rows - 1), wr1 = min(wrow + 31, a.rows - 1);
+    const bool live = wrow + (lane & 31) < a.rows, wave_live = wrow < a.rows;
+    const int row = min(wrow + (lane & 31), a.rows - 1);
     const int qi = a.G(row), pos = qi + off;
     const int wp0 = __builtin_amdgcn_readfirstlane(a.G(wr0) + off);
     const int wp1 = __builtin_amdgcn_readfirstlane(a.G(wr1) + off);
     const size_t qrow = (static_cast<size_t>(b) * a.Tq + qi) * a.Hq + static_cast<size_t>(hk) * a.G.d + (row - qi * a.G.d);
-    const int p0 = a.G(row0) + off, p1 = a.G(min(row0 + kRows - 1, a.rows - 1)) + off;
+    const int p0 = a.G(row0) + off, p1 = a.G(min(row0 + kGroup - 1, a.rows - 1)) + off;
     const int w_lo = a.window ? max(0, p0 - a.window + 1) : 0;
     const int t_lo = w_lo / BN, t_hi = p1 < 0 ? -1 : p1 / BN;
     const int t_sink = a.window ? min((a.sinks + BN - 1) / BN, t_lo) : 0;
     const int n = t_hi < t_lo ? 0 : t_sink + t_hi - t_lo + 1;
 
-    frag_t<T> qf[KS], gf[KS];
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-        qf[s] = load8(q + qrow * D + 8 * h2 + 16 * s);
-        gf[s] = load8(go + qrow * D + 8 * h2 + 16 * s);
-    }
-    const float lse2 = a.stats[static_cast<size_t>(head) * 2 * a.pitch + row];
-    const float delta = a.stats[(static_cast<size_t>(head) * 2 + 1) * a.pitch + row];
-    const float c = a.scale * kLog2e;
-    f32x16 dq[DT];
-#pragma unroll
-    for (int t = 0; t < DT; ++t) dq[t] = zero16();
     const size_t kstride = static_cast<size_t>(a.Hkv) * D;
     const T* kbase = k + (static_cast<size_t>(b) * a.Tk * a.Hkv + hk) * D;
     const T* vbase = v + (static_cast<size_t>(b) * a.Tk * a.Hkv + hk) * D;
     auto tile_of = [&](int i) { return i < t_sink ? i : i - t_sink + t_lo; };
     auto fetch = [&](int i) {
-        unsigned char* buf = smem + (i & 1) * 2 * C::kTile;
+        unsigned char* buf = smem + (i & (C::kBufs - 1)) * 2 * C::kTile;
         const int j0 = tile_of(i) * BN;
         copy_rows<T, D, BN, kWaves>(buf, kbase + j0 * kstride, buf + C::kTile, vbase + j0 * kstride, wave, lane,
                                     [&](int r) { return min(r, a.Tk - 1 - j0) * a.Hkv * D; });
     };
-    const int rb0 = RowRead<T, D>::base(lane & 31, h2), cb0 = ColRead<T, D>::base(lane);
-    if (n > 0) fetch(0);
+    if (C::kBufs == 2 && n > 0) fetch(0);
+
+    frag_t<T> qf[KS], gf[KS];
+    float delta = 0.f;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+        qf[s] = load8(q + qrow * D + 8 * h2 + 16 * s);
+        gf[s] = load8(go + qrow * D + 8 * h2 + 16 * s);
+        const frag_t<T> of = load8(o + qrow * D + 8 * h2 + 16 * s);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) delta = fmaf(static_cast<float>(of[x]), static_cast<float>(gf[s][x]), delta);
+    }
+    delta += other_half(delta);
+    const float lse2 = lse[qrow] * kLog2e;
+    if (live && (!SPLIT || wave == 0))
+        a.stats[(static_cast<size_t>(head) * 2 + h2) * a.pitch + row] = h2 ? delta : lse2;
+    const float c = a.scale * kLog2e;
+    f32x16 dq[DT];
+#pragma unroll
+    for (int t = 0; t < DT; ++t) dq[t] = zero16();
+    const int sub = SPLIT ? 32 * wave : 0;  // this wave's keys of a step
+    const int rb0 = RowRead<T, D>::base(lane & 31, h2) + sub * Tile<T, D>::kRow;
+    const int cb0 = ColRead<T, D>::base(lane) + sub * Tile<T, D>::kRow;
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
+        if (C::kBufs == 1) {
+            if (i > 0) tile_barrier();
+            fetch(i);
+        }
         tile_barrier();
-        if (i + 1 < n) fetch(i + 1);
-        const int buf = (i & 1) * 2 * C::kTile, rb = rb0 + buf, cb = cb0 + buf;
-        const int j0 = tile_of(i) * BN;
-        if (!wave_live || mask.none(wp0, wp1, j0, j0 + BN - 1)) continue;
+        if (C::kBufs == 2 && i + 1 < n) fetch(i + 1);
+        const int buf = (i & (C::kBufs - 1)) * 2 * C::kTile, rb = rb0 + buf, cb = cb0 + buf;
+        const int j0 = tile_of(i) * BN + sub;
+        if (!wave_live || mask.none(wp0, wp1, j0, j0 + 31)) continue;
         f32x16 s = zero16(), dp = zero16();
 #pragma unroll
         for (int e = 0; e < KS; ++e) s = mma32(RowRead<T, D>::get(smem, rb, e, 0), qf[e], s);
@@ -440,23 +440,35 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(T) == 2 ? 2 : 1) void dq_kernel
         for (int e = 0; e < KS; ++e) dp = mma32(RowRead<T, D>::get(smem, rb, e, C::kTile), gf[e], dp);
 #pragma unroll
         for (int r = 0; r < 16; ++r) dp[r] = ex2(fmaf(s[r], c, -lse2)) * (dp[r] - delta);
-        if (!mask.all(wp0, wp1, j0, j0 + BN - 1)) {
+        if (!mask.all(wp0, wp1, j0, j0 + 31)) {
 #pragma unroll
             for (int r = 0; r < 16; ++r)
                 if (!mask.sees(pos, j0 + row32(r, h2))) dp[r] = 0.f;
         }
-        frag_t<T> df[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            float z[8];
-#pragma unroll
-            for (int y = 0; y < 8; ++y) z[y] = dp[8 * u + y];
-            df[u] = pack8<T>(z);
-        }
+        const frag_t<T> df[2] = {pack_regs<T>(dp, 0), pack_regs<T>(dp, 1)};
 #pragma unroll
         for (int t = 0; t < DT; ++t)
 #pragma unroll
             for (int u = 0; u < 2; ++u) dq[t] = mma32(ColRead<T, D>::get(smem, cb, t, u), df[u], dq[t]);
+    }
+    if constexpr (SPLIT) {  // the waves' sums, added in wave order by the first
+        static_assert(C::kLds >= (kWaves - 1) * 64 * DT * 64, "LDS holds the other waves' sums");
+        tile_barrier();
+        float* box = reinterpret_cast<float*>(smem);
+        if (wave > 0) {
+#pragma unroll
+            for (int t = 0; t < DT; ++t)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) box[(((wave - 1) * DT + t) * 16 + r) * 64 + lane] = dq[t][r];
+        }
+        tile_barrier();
+        if (wave > 0) return;
+#pragma unroll
+        for (int w = 0; w < kWaves - 1; ++w)
+#pragma unroll
+            for (int t = 0; t < DT; ++t)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) dq[t][r] += box[((w * DT + t) * 16 + r) * 64 + lane];
     }
     bool bad = false;
 #pragma unroll
@@ -492,9 +504,25 @@ BwdArgs make_args(int B, int Tq, int Tk, int Hq, int Hkv, int window, int sinks,
     a.rows = Tq * a.G.d;
     a.pitch = (a.rows + 3) / 4 * 4;
     a.key_blocks = (Tk + kKeys - 1) / kKeys;
-    a.row_tiles = (a.rows + kRows - 1) / kRows;
-    a.sink_tiles = window && Tq > 0 ? (sinks + 31) / 32 : 0;
-    a.segs = a.sink_tiles ? (a.rows + kSegRows - 1) / kSegRows : 0;
+    const long long heads = static_cast<long long>(B) * Hkv, groups = heads * a.key_blocks;
+    a.split = heads * ((a.rows + kRows - 1) / kRows) < 256;  // fewer workgroups than CUs
+    a.row_tiles = a.split ? (a.rows + 31) / 32 : (a.rows + kRows - 1) / kRows;
+    // Below one workgroup per CU the rows are sliced, to two per CU and no
+    // slice under 64 rows.
+    a.slices = 1;
+    if (groups > 0 && groups < 256) {
+        const long long want = (512 + groups - 1) / groups, most = (a.rows + 63) / 64;
+        a.slices = static_cast<int>(want < most ? want : most > 0 ? most : 1);
+    }
+    // Sink segments: about one wave per SIMD, no segment under 128 rows.
+    if (a.slices == 1 && window && Tq > 0) a.sink_tiles = (sinks + 31) / 32;
+    if (a.sink_tiles) {
+        const long long even = heads * a.sink_tiles * a.rows / 1024;
+        a.seg_rows = static_cast<int>(even < 128 ? 128 : even > a.rows ? a.rows : (even + 31) / 32 * 32);
+        a.segs = (a.rows + a.seg_rows - 1) / a.seg_rows;
+    }
+    a.part_tiles = a.slices > 1 ? (Tk + 31) / 32 : a.sink_tiles;
+    a.slots = a.slices + a.segs;
     return a;
 }
 
@@ -509,33 +537,30 @@ hipError_t launch(const BwdArgs& a, const void* q_, const void* k_, const void* 
     const T *q = static_cast<const T*>(q_), *k = static_cast<const T*>(k_), *v = static_cast<const T*>(v_),
             *o = static_cast<const T*>(o_), *go = static_cast<const T*>(go_);
     const unsigned long long heads = static_cast<unsigned long long>(a.B) * a.Hkv;
-    const unsigned long long stat_blocks = (static_cast<unsigned long long>(a.B) * a.Tq * a.Hq + 15) / 16;
-    const unsigned long long kv_blocks = heads * a.key_blocks, q_blocks = heads * a.row_tiles;
-    const unsigned long long seg_blocks = heads * a.sink_tiles * a.segs, join_blocks = heads * a.sink_tiles;
-    if (!grid_fits(stat_blocks, 256) || !grid_fits(kv_blocks, 64 * kWaves) || !grid_fits(q_blocks, 64 * kWaves) ||
+    const unsigned long long kv_blocks = heads * a.key_blocks * a.slices, q_blocks = heads * a.row_tiles;
+    const unsigned long long seg_blocks = heads * a.sink_tiles * a.segs, join_blocks = heads * a.part_tiles;
+    if (!grid_fits(kv_blocks, 64 * kWaves) || !grid_fits(q_blocks, 64 * kWaves) ||
         !grid_fits(seg_blocks, 64) || !grid_fits(join_blocks * (D / 16), 256))
         return hipErrorInvalidConfiguration;
     using CK = DkdvCfg<T, D, kWaves>;
-    using CQ = DqCfg<T, D>;
+    auto* dq = a.split ? dq_kernel<T, D, true> : dq_kernel<T, D, false>;
+    const int dq_lds = a.split ? DqCfg<T, D, true>::kLds : DqCfg<T, D, false>::kLds;
     hipError_t e;
     if ((e = allow_lds(dkdv_kernel<T, D, kWaves>, CK::kLds)) != hipSuccess) return e;
     if ((e = allow_lds(dkdv_kernel<T, D, 1>, CK::kLds)) != hipSuccess) return e;
-    if ((e = allow_lds(dq_kernel<T, D>, CQ::kLds)) != hipSuccess) return e;
-    if (stat_blocks)
-        hipLaunchKernelGGL((stats_kernel<T, D>), dim3(static_cast<unsigned>(stat_blocks)), dim3(256), 0, st, a, o, go, lse);
+    if ((e = allow_lds(dq, dq_lds)) != hipSuccess) return e;
+    if (q_blocks)
+        hipLaunchKernelGGL(dq, dim3(static_cast<unsigned>(q_blocks)), dim3(64 * kWaves), dq_lds, st, a, q, k, v, o, go, lse,
+                           static_cast<T*>(gq));
     if (kv_blocks)
         hipLaunchKernelGGL((dkdv_kernel<T, D, kWaves>), dim3(static_cast<unsigned>(kv_blocks)), dim3(64 * kWaves),
                            CK::kLds, st, a, q, k, v, go, static_cast<T*>(gk), static_cast<T*>(gv));
-    if (join_blocks) {
-        if (seg_blocks)
-            hipLaunchKernelGGL((dkdv_kernel<T, D, 1>), dim3(static_cast<unsigned>(seg_blocks)), dim3(64), CK::kLds, st, a,
-                               q, k, v, go, static_cast<T*>(gk), static_cast<T*>(gv));
-        hipLaunchKernelGGL((sink_join_kernel<T, D>), dim3(static_cast<unsigned>(join_blocks), 64 * D / 4 / 256), dim3(256), 0, st, a,
-                           static_cast<T*>(gk), static_cast<T*>(gv));
-    }
-    if (q_blocks)
-        hipLaunchKernelGGL((dq_kernel<T, D>), dim3(static_cast<unsigned>(q_blocks)), dim3(64 * kWaves), CQ::kLds, st, a,
-                           q, k, v, go, static_cast<T*>(gq));
+    if (seg_blocks)
+        hipLaunchKernelGGL((dkdv_kernel<T, D, 1>), dim3(static_cast<unsigned>(seg_blocks)), dim3(64), CK::kLds, st, a, q, k,
+                           v, go, static_cast<T*>(gk), static_cast<T*>(gv));
+    if (join_blocks)
+        hipLaunchKernelGGL((join_kernel<T, D>), dim3(static_cast<unsigned>(join_blocks), 64 * D / 4 / 256), dim3(256), 0,
+                           st, a, static_cast<T*>(gk), static_cast<T*>(gv));
     return hipGetLastError();
 }
 
@@ -545,7 +570,7 @@ hipError_t launch(const BwdArgs& a, const void* q_, const void* k_, const void* 
 size_t attn_backward_workspace_floats(int B, int Tq, int Tk, int Hq, int Hkv, int d, int window, int sinks) {
     const attn::BwdArgs a = attn::make_args(B, Tq, Tk, Hq, Hkv, window, sinks, 1.f);
     const size_t heads = static_cast<size_t>(B) * Hkv;
-    return heads * (2 * static_cast<size_t>(a.pitch) + static_cast<size_t>(a.sink_tiles) * (1 + a.segs) * 64 * d);
+    return heads * (2 * static_cast<size_t>(a.pitch) + static_cast<size_t>(a.part_tiles) * a.slots * 64 * d);
 }
 
 hipError_t launch_attn_backward(int dtype, int B, int Tq, int Tk, int Hq, int Hkv, int d, int window, int sinks,

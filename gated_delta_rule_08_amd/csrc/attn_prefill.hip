@@ -40,10 +40,12 @@ struct PrefillArgs {
     int total_q, total_k;
 };
 
-template <typename T, int D> struct PrefillCfg {
-    static constexpr int BN = sizeof(T) == 2 ? 64 : 32;  // keys of a tile
+template <typename T, int D, bool SPLIT> struct PrefillCfg {
+    static constexpr int NS = sizeof(T) == 2 && !SPLIT ? 2 : 1;  // 32-key tiles of a wave's step
+    static constexpr int BN = 32 * NS * (SPLIT ? kWaves : 1);    // keys of a workgroup's step
     static constexpr int kTileBytes = BN * D * static_cast<int>(sizeof(T));
-    static constexpr int kLds = 4 * kTileBytes;  // K and V, two buffers
+    static constexpr int kBufs = 4 * kTileBytes <= 128 * 1024 ? 2 : 1;
+    static constexpr int kLds = 2 * kBufs * kTileBytes;  // K and V
 };
 
 // The rows of one wave key by key, hidden keys left out: what a wave does when
@@ -87,13 +89,15 @@ __device__ __forceinline__ void exact_rows(Mask mask, int pos, bool live, int wp
     if (lse && h2 == 0) *lse = l == 0.f ? -INFINITY : (m + lg2(l)) * kLn2;
 }
 
-template <typename T, int D>
+// 32 rows per wave, or with SPLIT 32 rows per workgroup, each wave taking a
+// quarter of the keys and the four joined at the end.
+template <typename T, int D, bool SPLIT>
 __global__ __launch_bounds__(64 * kWaves, 2) void prefill_kernel(PrefillArgs a, const T* __restrict__ q,
                                                                  const T* __restrict__ k,
                                                                  const T* __restrict__ v, T* __restrict__ o,
                                                                  float* __restrict__ lse) {
-    using C = PrefillCfg<T, D>;
-    constexpr int BN = C::BN, NS = BN / 32, KS = D / 16, DT = D / 32;
+    using C = PrefillCfg<T, D, SPLIT>;
+    constexpr int BN = C::BN, NS = C::NS, KS = D / 16, DT = D / 32, kGroup = SPLIT ? 32 : kRows;
     extern __shared__ unsigned char smem[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int h2 = lane >> 5;
@@ -121,29 +125,41 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prefill_kernel(PrefillArgs a, 
         k0 = ka;
     }
     const FastDiv G = a.G;
-    const int nrows = Tq * G.d, row0 = tile * kRows;
+    const int nrows = Tq * G.d, row0 = tile * kGroup;
     if (row0 >= nrows) return;
     const int off = Tk - Tq;
     const Mask mask{a.window, a.sinks};
 
     // this wave's and this lane's rows (a wave or lane past the end repeats
     // the last row and stores nothing)
-    const int wr0 = min(row0 + 32 * wave, nrows - 1), wr1 = min(row0 + 32 * wave + 31, nrows - 1);
-    const bool live = row0 + 32 * wave + (lane & 31) < nrows;
-    const bool wave_live = row0 + 32 * wave < nrows;
-    const int row = min(row0 + 32 * wave + (lane & 31), nrows - 1);
+    const int wrow = row0 + (SPLIT ? 0 : 32 * wave);
+    const int wr0 = min(wrow, nrows - 1), wr1 = min(wrow + 31, nrows - 1);
+    const bool live = wrow + (lane & 31) < nrows, wave_live = wrow < nrows;
+    const int row = min(wrow + (lane & 31), nrows - 1);
     const int qi = G(row), g = row - qi * G.d, pos = qi + off;
     const int wp0 = __builtin_amdgcn_readfirstlane(G(wr0) + off);
     const int wp1 = __builtin_amdgcn_readfirstlane(G(wr1) + off);
     const size_t qrow = (q0 + qi) * a.Hq + static_cast<size_t>(hk) * G.d + g;
 
     // key tiles of the workgroup's rows: the sinks before the window, then the window
-    const int p0 = G(row0) + off, p1 = G(min(row0 + kRows - 1, nrows - 1)) + off;
+    const int p0 = G(row0) + off, p1 = G(min(row0 + kGroup - 1, nrows - 1)) + off;
     const int win = a.window;
     const int w_lo = win ? max(0, p0 - win + 1) : 0;
     const int t_lo = w_lo / BN, t_hi = p1 < 0 ? -1 : p1 / BN;  // p1 <= Tk - 1
     const int t_sink = win ? min((a.sinks + BN - 1) / BN, t_lo) : 0;
     const int n = t_hi < t_lo ? 0 : t_sink + t_hi - t_lo + 1;
+
+    const size_t kstride = static_cast<size_t>(a.Hkv) * D;
+    const T* kbase = k + (k0 * a.Hkv + hk) * D;
+    const T* vbase = v + (k0 * a.Hkv + hk) * D;
+    auto tile_of = [&](int i) { return i < t_sink ? i : i - t_sink + t_lo; };
+    auto fetch = [&](int i) {
+        unsigned char* buf = smem + (i & (C::kBufs - 1)) * 2 * C::kTileBytes;
+        const int j0 = tile_of(i) * BN;
+        copy_rows<T, D, BN, kWaves>(buf, kbase + j0 * kstride, buf + C::kTileBytes, vbase + j0 * kstride, wave, lane,
+                                    [&](int r) { return min(r, Tk - 1 - j0) * a.Hkv * D; });
+    };
+    if (C::kBufs == 2 && n > 0) fetch(0);
 
     // Q^T as the B operand.  A negative scale flips the sign of q (exact), so
     // that the largest raw score is the largest scaled one.
@@ -165,25 +181,20 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prefill_kernel(PrefillArgs a, 
     for (int t = 0; t < DT; ++t) acc[t] = zero16();
     float m = -INFINITY, l = 0.f;
 
-    const size_t kstride = static_cast<size_t>(a.Hkv) * D;
-    const T* kbase = k + (k0 * a.Hkv + hk) * D;
-    const T* vbase = v + (k0 * a.Hkv + hk) * D;
-    auto tile_of = [&](int i) { return i < t_sink ? i : i - t_sink + t_lo; };
-    auto fetch = [&](int i) {
-        unsigned char* buf = smem + (i & 1) * 2 * C::kTileBytes;
-        const int j0 = tile_of(i) * BN;
-        copy_rows<T, D, BN, kWaves>(buf, kbase + j0 * kstride, buf + C::kTileBytes, vbase + j0 * kstride, wave, lane,
-                                    [&](int r) { return min(r, Tk - 1 - j0) * a.Hkv * D; });
-    };
-    const int kb0 = RowRead<T, D>::base(lane & 31, h2), vb0 = ColRead<T, D>::base(lane) + C::kTileBytes;
-    if (n > 0) fetch(0);
+    const int sub = SPLIT ? 32 * wave : 0;  // this wave's keys of a step
+    const int kb0 = RowRead<T, D>::base(lane & 31, h2) + sub * Tile<T, D>::kRow;
+    const int vb0 = ColRead<T, D>::base(lane) + sub * Tile<T, D>::kRow + C::kTileBytes;
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
+        if (C::kBufs == 1) {
+            if (i > 0) tile_barrier();
+            fetch(i);
+        }
         tile_barrier();
-        if (i + 1 < n) fetch(i + 1);
-        const int buf = (i & 1) * 2 * C::kTileBytes, kb = kb0 + buf, vb = vb0 + buf;
-        const int j0 = tile_of(i) * BN;
-        if (!wave_live || mask.none(wp0, wp1, j0, j0 + BN - 1)) continue;
+        if (C::kBufs == 2 && i + 1 < n) fetch(i + 1);
+        const int buf = (i & (C::kBufs - 1)) * 2 * C::kTileBytes, kb = kb0 + buf, vb = vb0 + buf;
+        const int j0 = tile_of(i) * BN + sub;
+        if (!wave_live || mask.none(wp0, wp1, j0, j0 + 32 * NS - 1)) continue;
 
         f32x16 s[NS];
 #pragma unroll
@@ -193,7 +204,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prefill_kernel(PrefillArgs a, 
             for (int e = 0; e < KS; ++e)
                 s[u] = mma32(RowRead<T, D>::get(smem, kb, e, 32 * u * Tile<T, D>::kRow), qf[e], s[u]);
         }
-        if (!mask.all(wp0, wp1, j0, j0 + BN - 1)) {
+        if (!mask.all(wp0, wp1, j0, j0 + 32 * NS - 1)) {
 #pragma unroll
             for (int u = 0; u < NS; ++u)
 #pragma unroll
@@ -225,12 +236,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prefill_kernel(PrefillArgs a, 
                 ls += s[u][r];
             }
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                float w[8];
-#pragma unroll
-                for (int y = 0; y < 8; ++y) w[y] = s[u][8 * x + y];
-                pf[2 * u + x] = pack8<T>(w);
-            }
+            for (int x = 0; x < 2; ++x) pf[2 * u + x] = pack_regs<T>(s[u], x);
         }
         l += ls;
 #pragma unroll
@@ -240,6 +246,35 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prefill_kernel(PrefillArgs a, 
     }
 
     l += other_half(l);
+    if constexpr (SPLIT) {  // the waves' parts, joined by the first in wave order
+        constexpr int kBox = (DT * 16 + 2) * 64;  // floats of one wave
+        static_assert(C::kLds >= (kWaves - 1) * kBox * 4, "LDS holds the other waves' parts");
+        float* box = reinterpret_cast<float*>(smem) + lane;
+        tile_barrier();
+        if (wave > 0) {
+            float* mine = box + (wave - 1) * kBox;
+            mine[0] = m;
+            mine[64] = l;
+#pragma unroll
+            for (int t = 0; t < DT; ++t)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) mine[(t * 16 + r + 2) * 64] = acc[t][r];
+        }
+        tile_barrier();
+        if (wave > 0) return;
+#pragma unroll 1
+        for (int w = 0; w < kWaves - 1; ++w) {
+            const float* its = box + w * kBox;
+            const float m1 = its[0], mx = fmaxf(m, m1), mc = mx == -INFINITY ? 0.f : mx * c;
+            const float a0 = m == -INFINITY ? 0.f : ex2(m * c - mc), a1 = m1 == -INFINITY ? 0.f : ex2(m1 * c - mc);
+            m = mx;
+            l = l * a0 + its[64] * a1;
+#pragma unroll
+            for (int t = 0; t < DT; ++t)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) acc[t][r] = fmaf(its[(t * 16 + r + 2) * 64], a1, acc[t][r] * a0);
+        }
+    }
 
     // A hidden key has weight 0, but 0 times an infinity or NaN in its value
     // row is NaN: a wave whose sums hold a NaN forms its rows again from the
@@ -267,13 +302,13 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prefill_kernel(PrefillArgs a, 
     }
 }
 
-template <typename T, int D>
-hipError_t launch(const PrefillArgs& a, const void* q, const void* k, const void* v, void* o, float* lse,
-                  hipStream_t st) {
-    using C = PrefillCfg<T, D>;
+template <typename T, int D, bool SPLIT>
+hipError_t launch_tiles(const PrefillArgs& a, const void* q, const void* k, const void* v, void* o, float* lse,
+                        hipStream_t st) {
+    using C = PrefillCfg<T, D, SPLIT>;
     const unsigned long long blocks = static_cast<unsigned long long>(a.B) * a.Hkv * a.tiles;
     if (!grid_fits(blocks, 64 * kWaves)) return hipErrorInvalidConfiguration;
-    auto* f = prefill_kernel<T, D>;
+    auto* f = prefill_kernel<T, D, SPLIT>;
     if (C::kLds > 64 * 1024) {
         const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(f),
                                                  hipFuncAttributeMaxDynamicSharedMemorySize, C::kLds);
@@ -283,6 +318,17 @@ hipError_t launch(const PrefillArgs& a, const void* q, const void* k, const void
                        static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v),
                        static_cast<T*>(o), lse);
     return hipGetLastError();
+}
+
+// Fewer 128-row workgroups than CUs: 32-row workgroups instead, each wave a
+// quarter of the keys.
+template <typename T, int D>
+hipError_t launch(PrefillArgs a, const void* q, const void* k, const void* v, void* o, float* lse, hipStream_t st) {
+    const long long rows = static_cast<long long>(a.Tq) * a.G.d, heads = static_cast<long long>(a.B) * a.Hkv;
+    a.tiles = static_cast<int>((rows + kRows - 1) / kRows);
+    if (heads * a.tiles >= 256) return launch_tiles<T, D, false>(a, q, k, v, o, lse, st);
+    a.tiles = static_cast<int>((rows + 31) / 32);
+    return launch_tiles<T, D, true>(a, q, k, v, o, lse, st);
 }
 
 }  // namespace
@@ -301,7 +347,6 @@ hipError_t launch_attn_prefill(int dtype, int B, int Tq, int Tk, int Hq, int Hkv
     a.window = window;
     a.sinks = sinks;
     a.scale = scale;
-    a.tiles = static_cast<int>((static_cast<long long>(Tq) * a.G.d + attn::kRows - 1) / attn::kRows);
     a.cu_q = pk.cu_q;
     a.cu_k = pk.cu_k;
     a.total_q = pk.total_q;
