@@ -477,35 +477,80 @@ def gdr_chunk_backward(gate: str, q, k, v, alpha, beta, state_in, grad_o, grad_s
 
 
 
-def _attn_checks(q, k, v, o, extra=()):
-    """Shapes and types common to the attention calls; returns Hq, Hkv, d."""
-    if q.dim() < 2 or k.dim() != q.dim() or k.shape != v.shape or o.shape != q.shape or k.shape[-1] != q.shape[-1]:
-        raise ValueError("q, k, v, o shapes disagree")
-    if any(t.dtype != q.dtype for t in (k, v, o, *extra)) or q.dtype not in _DTYPES:
+# The attention calls are short (a decode step of a small batch takes a few
+# microseconds on the GPU), so their checks keep to what a call costs: integer
+# device numbers, plain integers as pointers, the raw stream handle.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _attn_device(*ts) -> int:
+    """The device number all of the tensors (None ones apart) are on."""
+    dev = None
+    for t in ts:
+        if t is not None:
+            n = t.get_device()
+            if n != dev:
+                if n < 0:
+                    raise ValueError("all tensors must be on the GPU")
+                if dev is not None:
+                    raise ValueError("all tensors must be on one device")
+                dev = n
+            if not t.is_contiguous():
+                raise ValueError("all tensors must be contiguous")
+    return dev
+
+
+def _attn_launch(dev: int, stream, fn, *args) -> None:
+    """fn(*args, stream) with `dev` current: a launch belongs to the tensors'
+    device, whichever device is current, and by default to its current stream."""
+    if stream is None:
+        stream = _raw_stream(dev)
+    elif isinstance(stream, torch.cuda.Stream):
+        stream = stream.cuda_stream
+    if dev == torch.cuda.current_device():
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, stream)
+    if status:
+        _check(status)
+
+
+def _attn_types(q, *ts) -> int:
+    """The dtype code of q, which every other tensor shares."""
+    dtype = q.dtype
+    for t in ts:
+        if t.dtype != dtype:
+            raise ValueError("q, k, v, o (pages, gradients) must share dtype fp32 or bf16")
+    code = _DTYPES.get(dtype)
+    if code is None:
         raise ValueError("q, k, v, o (pages, gradients) must share dtype fp32 or bf16")
-    Hq, Hkv = q.shape[-2], k.shape[-2]
-    if (Hkv == 0 and Hq) or (Hkv and Hq % Hkv):
+    return code
+
+
+def _attn_heads(Hq: int, Hkv: int) -> None:
+    if Hq % Hkv if Hkv else Hq:
         raise ValueError("the query heads must be a multiple of the key heads")
-    return Hq, Hkv, q.shape[-1]
 
 
-def _int32(name, t, shape):
-    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape):
+def _attn_int(x: int) -> int:
+    """A window or sink count as a C int: anything larger hides nothing either."""
+    return x if x < 0x7fffffff else 0x7fffffff
+
+
+def _int32(name, t, shape) -> None:
+    if t.dtype != torch.int32 or t.shape != shape:
         raise ValueError("%s must be int32 %s" % (name, list(shape)))
 
 
-def _attn_call(dev, stream, call):
-    """Runs call(stream pointer) with `dev` current: a launch belongs to
-    the tensors' device, whichever device is current."""
-    if dev.index == torch.cuda.current_device():
-        _check(call(_stream(stream)))
-        return
-    with torch.cuda.device(dev):
-        _check(call(_stream(stream)))
-
-
-def _scale(scale, d):
-    return float(d) ** -0.5 if scale is None else float(scale)
+def _attn_workspace(workspace, need: int, dev: int, stream):
+    """(pointer, bytes, tensor) of the caller's workspace or of one made for this call."""
+    if workspace is None:
+        if not need:
+            return None, 0, None
+        workspace = _workspace(need, torch.device("cuda", dev), stream)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
 def gdr_attn_prefill(q, k, v, o, lse=None, window: int = 0, sinks: int = 0, scale: Optional[float] = None,
@@ -518,17 +563,20 @@ def gdr_attn_prefill(q, k, v, o, lse=None, window: int = 0, sinks: int = 0, scal
     positions.  ``lse`` (optional, fp32 [B,Tq,Hq]) receives the log-sum-exp
     that :func:`gdr_attn_backward` needs.  ``scale`` defaults to d ** -0.5.
     """
-    if q.dim() != 4 or k.dim() != 4 or k.shape[0] != q.shape[0]:
+    if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q must be [B,Tq,Hq,d], k and v [B,Tk,Hkv,d]")
-    Hq, Hkv, d = _attn_checks(q, k, v, o)
-    B, Tq, Tk = q.shape[0], q.shape[1], k.shape[1]
-    if lse is not None and (lse.shape != q.shape[:3] or lse.dtype != torch.float32):
+    B, Tq, Hq, d = shape = q.shape
+    _, Tk, Hkv, _ = k.shape
+    if k.shape != (B, Tk, Hkv, d) or v.shape != (B, Tk, Hkv, d) or o.shape != shape:
+        raise ValueError("q, k, v, o shapes disagree")
+    _attn_heads(Hq, Hkv)
+    code = _attn_types(q, k, v, o)
+    if lse is not None and (lse.shape != shape[:3] or lse.dtype != torch.float32):
         raise ValueError("lse must be fp32 [B,Tq,Hq]")
-    _same_device(q, k, v, o, lse)
-    lib = load_library()
-    _attn_call(q.device, stream, lambda st: lib.gdr_attn_prefill(
-        _DTYPES[q.dtype], B, Tq, Tk, Hq, Hkv, d, int(window), int(sinks), _scale(scale, d), _ptr(q), _ptr(k), _ptr(v),
-        _ptr(o), _ptr(lse), st))
+    dev = _attn_device(q, k, v, o, lse)
+    _attn_launch(dev, stream, load_library().gdr_attn_prefill, code, B, Tq, Tk, Hq, Hkv, d, _attn_int(window), _attn_int(sinks),
+                 d ** -0.5 if scale is None else scale, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+                 None if lse is None else lse.data_ptr())
 
 
 def gdr_attn_prefill_varlen(q, k, v, cu_q, cu_k, o, lse=None, max_seqlen_q: Optional[int] = None, window: int = 0,
@@ -537,30 +585,34 @@ def gdr_attn_prefill_varlen(q, k, v, cu_q, cu_k, o, lse=None, max_seqlen_q: Opti
     [total_k,Hkv,d], lse [total_q,Hq]; cu_q and cu_k [N+1] are int32 device
     offsets.  max_seqlen_q bounds every sequence's queries; if None it is read
     from cu_q (one device-to-host copy)."""
-    if q.dim() != 3:
+    if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q must be [total_q,Hq,d], k and v [total_k,Hkv,d]")
-    Hq, Hkv, d = _attn_checks(q, k, v, o)
+    total_q, Hq, d = shape = q.shape
+    total_k, Hkv, _ = k.shape
+    if k.shape != (total_k, Hkv, d) or v.shape != (total_k, Hkv, d) or o.shape != shape:
+        raise ValueError("q, k, v, o shapes disagree")
+    _attn_heads(Hq, Hkv)
+    code = _attn_types(q, k, v, o)
     N = cu_q.numel() - 1
     if N < 0:
         raise ValueError("cu_q must be [N+1]")
     _int32("cu_q", cu_q, (N + 1,))
     _int32("cu_k", cu_k, (N + 1,))
-    if lse is not None and (lse.shape != q.shape[:2] or lse.dtype != torch.float32):
+    if lse is not None and (lse.shape != shape[:2] or lse.dtype != torch.float32):
         raise ValueError("lse must be fp32 [total_q,Hq]")
-    _same_device(q, k, v, cu_q, cu_k, o, lse)
+    dev = _attn_device(q, k, v, cu_q, cu_k, o, lse)
     if max_seqlen_q is None:
         cu = cu_q.cpu()
-        max_seqlen_q = int((cu[1:] - cu[:-1]).max()) if N > 0 else 0
-    lib = load_library()
-    _attn_call(q.device, stream, lambda st: lib.gdr_attn_prefill_varlen(
-        _DTYPES[q.dtype], N, q.shape[0], k.shape[0], int(max_seqlen_q), Hq, Hkv, d, int(window), int(sinks),
-        _scale(scale, d), _ptr(q), _ptr(k), _ptr(v), _ptr(cu_q), _ptr(cu_k), _ptr(o), _ptr(lse), st))
+        max_seqlen_q = int((cu[1:] - cu[:-1]).max().clamp(min=0)) if N > 0 else 0
+    _attn_launch(dev, stream, load_library().gdr_attn_prefill_varlen, code, N, total_q, total_k, max_seqlen_q, Hq, Hkv, d,
+                 _attn_int(window), _attn_int(sinks), d ** -0.5 if scale is None else scale, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                 cu_q.data_ptr(), cu_k.data_ptr(), o.data_ptr(), None if lse is None else lse.data_ptr())
 
 
 def gdr_attn_backward_workspace_bytes(dtype, B: int, Tq: int, Tk: int, Hq: int, Hkv: int, d: int, window: int = 0,
                                       sinks: int = 0) -> int:
-    return int(load_library().gdr_attn_backward_workspace_bytes(_DTYPES[dtype], B, Tq, Tk, Hq, Hkv, d, int(window),
-                                                                int(sinks)))
+    return int(load_library().gdr_attn_backward_workspace_bytes(_DTYPES[dtype], B, Tq, Tk, Hq, Hkv, d,
+                                                                _attn_int(window), _attn_int(sinks)))
 
 
 def gdr_attn_backward(q, k, v, o, lse, grad_o, grad_q, grad_k, grad_v, window: int = 0, sinks: int = 0,
@@ -570,38 +622,41 @@ def gdr_attn_backward(q, k, v, o, lse, grad_o, grad_q, grad_k, grad_v, window: i
     what the forward wrote for the same q, k, v, window, sinks and scale.
     workspace: a device tensor of at least gdr_attn_backward_workspace_bytes
     bytes, or None to have one allocated for this call."""
-    if q.dim() != 4 or k.dim() != 4 or k.shape[0] != q.shape[0]:
+    if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q must be [B,Tq,Hq,d], k and v [B,Tk,Hkv,d]")
-    Hq, Hkv, d = _attn_checks(q, k, v, o, (grad_o, grad_q, grad_k, grad_v))
-    B, Tq, Tk = q.shape[0], q.shape[1], k.shape[1]
-    if grad_o.shape != q.shape or grad_q.shape != q.shape or grad_k.shape != k.shape or grad_v.shape != k.shape:
+    B, Tq, Hq, d = shape = q.shape
+    _, Tk, Hkv, _ = kshape = k.shape
+    if kshape != (B, Tk, Hkv, d) or v.shape != kshape or o.shape != shape:
+        raise ValueError("q, k, v, o shapes disagree")
+    if grad_o.shape != shape or grad_q.shape != shape or grad_k.shape != kshape or grad_v.shape != kshape:
         raise ValueError("gradient shapes must match the inputs")
-    if lse.shape != q.shape[:3] or lse.dtype != torch.float32:
+    _attn_heads(Hq, Hkv)
+    code = _attn_types(q, k, v, o, grad_o, grad_q, grad_k, grad_v)
+    if lse.shape != shape[:3] or lse.dtype != torch.float32:
         raise ValueError("lse must be fp32 [B,Tq,Hq]")
-    _same_device(q, k, v, o, lse, grad_o, grad_q, grad_k, grad_v, workspace)
-    if workspace is None:
-        workspace = _workspace(gdr_attn_backward_workspace_bytes(q.dtype, B, Tq, Tk, Hq, Hkv, d, window, sinks),
-                               q.device, stream)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    lib = load_library()
-    _attn_call(q.device, stream, lambda st: lib.gdr_attn_backward(
-        _DTYPES[q.dtype], B, Tq, Tk, Hq, Hkv, d, int(window), int(sinks), _scale(scale, d), _ptr(q), _ptr(k), _ptr(v),
-        _ptr(o), _ptr(lse), _ptr(grad_o), _ptr(grad_q), _ptr(grad_k), _ptr(grad_v), _ptr(workspace), ws_bytes, st))
+    dev = _attn_device(q, k, v, o, lse, grad_o, grad_q, grad_k, grad_v, workspace)
+    need = 0 if workspace is not None else gdr_attn_backward_workspace_bytes(q.dtype, B, Tq, Tk, Hq, Hkv, d, window, sinks)
+    ws, ws_bytes, workspace = _attn_workspace(workspace, need, dev, stream)
+    _attn_launch(dev, stream, load_library().gdr_attn_backward, code, B, Tq, Tk, Hq, Hkv, d, _attn_int(window), _attn_int(sinks),
+                 d ** -0.5 if scale is None else scale, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+                 lse.data_ptr(), grad_o.data_ptr(), grad_q.data_ptr(), grad_k.data_ptr(), grad_v.data_ptr(), ws, ws_bytes)
 
 
 def _page_checks(k_pages, v_pages, page_table, Hkv, d, N):
-    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.shape[1] != Hkv or k_pages.shape[3] != d:
+    if k_pages.dim() != 4 or page_table.dim() != 2:
+        raise ValueError("k_pages and v_pages must be [num_pages,Hkv,page_size,d], page_table [sequences,max_pages]")
+    num_pages, _, page, _ = shape = k_pages.shape
+    if shape != (num_pages, Hkv, page, d) or v_pages.shape != shape:
         raise ValueError("k_pages and v_pages must be [num_pages,Hkv,page_size,d]")
-    if page_table.dim() != 2:
-        raise ValueError("page_table must be int32 [sequences,max_pages]")
-    _int32("page_table", page_table, (N, page_table.shape[1]))
-    return k_pages.shape[2], k_pages.shape[0], page_table.shape[1]
+    max_pages = page_table.shape[1]
+    _int32("page_table", page_table, (N, max_pages))
+    return page, num_pages, max_pages
 
 
 def gdr_attn_decode_workspace_bytes(dtype, B: int, Hq: int, Hkv: int, d: int, page_size: int, max_pages: int,
                                     window: int = 0, sinks: int = 0) -> int:
     return int(load_library().gdr_attn_decode_workspace_bytes(_DTYPES[dtype], B, Hq, Hkv, d, page_size, max_pages,
-                                                              int(window), int(sinks)))
+                                                              _attn_int(window), _attn_int(sinks)))
 
 
 def gdr_attn_decode(q, k, v, k_pages, v_pages, page_table, lengths, o, window: int = 0, sinks: int = 0,
@@ -616,22 +671,23 @@ def gdr_attn_decode(q, k, v, k_pages, v_pages, page_table, lengths, o, window: i
     tensor of at least gdr_attn_decode_workspace_bytes bytes, or None to have
     one allocated for this call.
     """
-    if q.dim() != 3 or k.dim() != 3 or k.shape[0] != q.shape[0]:
+    if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q must be [B,Hq,d], k and v [B,Hkv,d]")
-    Hq, Hkv, d = _attn_checks(q, k, v, o, (k_pages, v_pages))
-    B = q.shape[0]
+    B, Hq, d = shape = q.shape
+    Hkv = k.shape[1]
+    if k.shape != (B, Hkv, d) or v.shape != (B, Hkv, d) or o.shape != shape:
+        raise ValueError("q, k, v, o shapes disagree")
+    _attn_heads(Hq, Hkv)
+    code = _attn_types(q, k, v, o, k_pages, v_pages)
     page, num_pages, max_pages = _page_checks(k_pages, v_pages, page_table, Hkv, d, B)
     _int32("lengths", lengths, (B,))
-    _same_device(q, k, v, k_pages, v_pages, page_table, lengths, o, workspace)
-    if workspace is None:
-        workspace = _workspace(gdr_attn_decode_workspace_bytes(q.dtype, B, Hq, Hkv, d, page, max_pages, window, sinks),
-                               q.device, stream)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    lib = load_library()
-    _attn_call(q.device, stream, lambda st: lib.gdr_attn_decode(
-        _DTYPES[q.dtype], B, Hq, Hkv, d, page, num_pages, max_pages, int(window), int(sinks), _scale(scale, d), _ptr(q),
-        _ptr(k), _ptr(v), _ptr(k_pages), _ptr(v_pages), _ptr(page_table), _ptr(lengths), _ptr(o), _ptr(workspace),
-        ws_bytes, st))
+    dev = _attn_device(q, k, v, k_pages, v_pages, page_table, lengths, o, workspace)
+    need = 0 if workspace is not None else gdr_attn_decode_workspace_bytes(q.dtype, B, Hq, Hkv, d, page, max_pages, window,
+                                                                           sinks)
+    ws, ws_bytes, workspace = _attn_workspace(workspace, need, dev, stream)
+    _attn_launch(dev, stream, load_library().gdr_attn_decode, code, B, Hq, Hkv, d, page, num_pages, max_pages, _attn_int(window), _attn_int(sinks),
+                 d ** -0.5 if scale is None else scale, q.data_ptr(), k.data_ptr(), v.data_ptr(), k_pages.data_ptr(),
+                 v_pages.data_ptr(), page_table.data_ptr(), lengths.data_ptr(), o.data_ptr(), ws, ws_bytes)
 
 
 def gdr_attn_append(k, v, cu_seqlens, lengths, k_pages, v_pages, page_table, stream=None) -> None:
@@ -641,13 +697,15 @@ def gdr_attn_append(k, v, cu_seqlens, lengths, k_pages, v_pages, page_table, str
     as in :func:`gdr_attn_decode`; lengths are not advanced."""
     if k.dim() != 3:
         raise ValueError("k and v must be [total,Hkv,d]")
-    _, Hkv, d = _attn_checks(k, k, v, k, (k_pages, v_pages))
+    total, Hkv, d = shape = k.shape
+    if v.shape != shape:
+        raise ValueError("k and v shapes disagree")
+    code = _attn_types(k, v, k_pages, v_pages)
     N = lengths.numel()
     _int32("lengths", lengths, (N,))
     _int32("cu_seqlens", cu_seqlens, (N + 1,))
     page, num_pages, max_pages = _page_checks(k_pages, v_pages, page_table, Hkv, d, N)
-    _same_device(k, v, cu_seqlens, lengths, k_pages, v_pages, page_table)
-    lib = load_library()
-    _attn_call(k.device, stream, lambda st: lib.gdr_attn_append(
-        _DTYPES[k.dtype], N, k.shape[0], Hkv, d, page, num_pages, max_pages, _ptr(k), _ptr(v), _ptr(cu_seqlens),
-        _ptr(lengths), _ptr(k_pages), _ptr(v_pages), _ptr(page_table), st))
+    dev = _attn_device(k, v, cu_seqlens, lengths, k_pages, v_pages, page_table)
+    _attn_launch(dev, stream, load_library().gdr_attn_append, code, N, total, Hkv, d, page, num_pages, max_pages,
+                 k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), lengths.data_ptr(), k_pages.data_ptr(),
+                 v_pages.data_ptr(), page_table.data_ptr())

@@ -105,6 +105,17 @@ template <int D> struct ColRead16<float, D> {
     }
 };
 
+// 16-byte loads of the pages: read once, so they need not stay in the caches.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ u32x4 stream16(const void* p) {
+    return __builtin_nontemporal_load(static_cast<const u32x4*>(p));
+}
+__device__ __forceinline__ bf16x8v stream8(const bf16_t* p) { return __builtin_bit_cast(bf16x8v, stream16(p)); }
+__device__ __forceinline__ f32x8 stream8(const float* p) {
+    const f32x4 a = __builtin_bit_cast(f32x4, stream16(p)), b = __builtin_bit_cast(f32x4, stream16(p + 4));
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
 template <typename T, int D>
 __global__ __launch_bounds__(64 * kWaves) void decode_kernel(
     DecodeArgs a, const T* __restrict__ q, const T* __restrict__ knew, const T* __restrict__ vnew, T* k_pages,
@@ -167,21 +178,20 @@ __global__ __launch_bounds__(64 * kWaves) void decode_kernel(
         return ((page * a.Hkv + hk) << a.page_shift) + (key & slot_mask);
     };
     frag_t<T> kf[2][KS];
-    uint4 vr[kVLoads];
+    u32x4 vr[kVLoads];
     auto fetch = [&](int rid) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const int r = __shfl(rid, 16 * u + c16);
             const T* p = (r == kNew ? knew + new_row * D : k_pages + static_cast<size_t>(r) * D) + 8 * h4;
 #pragma unroll
-            for (int s = 0; s < KS; ++s) kf[u][s] = r == kNone ? zero_frag<T>() : load8(p + 32 * s);
+            for (int s = 0; s < KS; ++s) kf[u][s] = r == kNone ? zero_frag<T>() : stream8(p + 32 * s);
         }
 #pragma unroll
         for (int j = 0; j < kVLoads; ++j) {
             const int r = __shfl(rid, kPer * j + lane / L::kUnits);
             const T* p = r == kNew ? vnew + new_row * D : v_pages + static_cast<size_t>(r) * D;
-            vr[j] = r == kNone ? make_uint4(0u, 0u, 0u, 0u)
-                               : reinterpret_cast<const uint4*>(p)[lane % L::kUnits];
+            vr[j] = r == kNone ? u32x4{0u, 0u, 0u, 0u} : stream16(p + (lane % L::kUnits) * (16 / sizeof(T)));
         }
     };
 
@@ -208,7 +218,7 @@ __global__ __launch_bounds__(64 * kWaves) void decode_kernel(
         }
 #pragma unroll
         for (int j = 0; j < kVLoads; ++j)
-            *reinterpret_cast<uint4*>(tile + (L::at(kPer * j + lane / L::kUnits) ^ ((lane % L::kUnits) << 4))) = vr[j];
+            *reinterpret_cast<u32x4*>(tile + (L::at(kPer * j + lane / L::kUnits) ^ ((lane % L::kUnits) << 4))) = vr[j];
         rid = next;
         if (at + kGrain < last) fetch(rid);
 
@@ -294,16 +304,18 @@ __global__ __launch_bounds__(64 * kWaves) void decode_kernel(
     }
 }
 
-// Joins a sequence's parts, one wave per query head: lane s holds part s's
-// weight 2^(m_s - max m), the channels run over the lanes.
+// Joins a sequence's parts, one workgroup per query head: every wave forms the
+// parts' weights 2^(m_s - max m) (lane s holds part s) and adds a quarter of
+// the parts, the channels over its lanes; the four sums are added in order.
 template <typename T, int D>
 __global__ __launch_bounds__(256) void join_kernel(DecodeArgs a, const int* __restrict__ table,
                                                    const int* __restrict__ lengths,
                                                    const float* __restrict__ part_o,
                                                    const float* __restrict__ part_ml, T* __restrict__ o) {
-    const int lane = threadIdx.x & 63;
-    const size_t row = static_cast<size_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-    if (row >= static_cast<size_t>(a.B) * a.Hq) return;
+    constexpr int N = D / 64, W = 4;
+    __shared__ float sums[W - 1][D];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const size_t row = blockIdx.x;
     const Span sp = span_of(a, static_cast<int>(row / a.Hq), table, lengths);
     if (sp.pos < 0 || sp.parts == 1) return;
     const size_t prow = row * a.splits;
@@ -312,27 +324,40 @@ __global__ __launch_bounds__(256) void join_kernel(DecodeArgs a, const int* __re
         m = part_ml[(prow + lane) * 2];
         l = part_ml[(prow + lane) * 2 + 1];
     }
+    const float* p = part_o + prow * D + N * lane;
+    float x[kMaxSplits / W][N];
+#pragma unroll
+    for (int i = 0; i < kMaxSplits / W; ++i)  // all loads before the first use
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            x[i][e] = W * i + wave < sp.parts ? p[static_cast<size_t>(W * i + wave) * D + e] : 0.f;
     float M = m;
 #pragma unroll
-    for (int x = 1; x < 64; x <<= 1) M = fmaxf(M, __shfl_xor(M, x));
+    for (int s = 1; s < 64; s <<= 1) M = fmaxf(M, __shfl_xor(M, s));
     const float w = m == -INFINITY ? 0.f : ex2(m - M);
     float total = l * w;
 #pragma unroll
-    for (int x = 1; x < 64; x <<= 1) total += __shfl_xor(total, x);
-    constexpr int N = D / 64;
-    float acc[N];
+    for (int s = 1; s < 64; s <<= 1) total += __shfl_xor(total, s);
+    float acc[N] = {};
 #pragma unroll
-    for (int e = 0; e < N; ++e) acc[e] = 0.f;
-    const float* p = part_o + prow * D + N * lane;
-#pragma unroll 1
-    for (int s = 0; s < sp.parts; ++s) {
-        const float ws = __shfl(w, s);
+    for (int i = 0; i < kMaxSplits / W; ++i) {
+        const float ws = __shfl(w, W * i + wave);
 #pragma unroll
-        for (int e = 0; e < N; ++e) acc[e] = fmaf(ws, p[static_cast<size_t>(s) * D + e], acc[e]);
+        for (int e = 0; e < N; ++e) acc[e] = fmaf(ws, x[i][e], acc[e]);
     }
+    if (wave > 0) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) sums[wave - 1][N * lane + e] = acc[e];
+    }
+    __syncthreads();
+    if (wave > 0) return;
     const float inv = total == 0.f ? 0.f : 1.f / total;
 #pragma unroll
-    for (int e = 0; e < N; ++e) Elem<T>::store(o + row * D + N * lane + e, acc[e] * inv);
+    for (int e = 0; e < N; ++e) {
+#pragma unroll
+        for (int s = 0; s < W - 1; ++s) acc[e] += sums[s][N * lane + e];
+        Elem<T>::store(o + row * D + N * lane + e, acc[e] * inv);
+    }
 }
 
 template <typename T, int D>
@@ -341,7 +366,7 @@ hipError_t launch_decode_t(const DecodeArgs& a, const void* q, const void* k, co
     using C = DecodeCfg<T, D>;
     const unsigned long long blocks = static_cast<unsigned long long>(a.B) * a.Hkv * a.head_tiles * a.splits;
     const unsigned long long rows = static_cast<unsigned long long>(a.B) * a.Hq;
-    if (!grid_fits(blocks, 64 * kWaves) || !grid_fits((rows + 3) / 4, 256)) return hipErrorInvalidConfiguration;
+    if (!grid_fits(blocks, 64 * kWaves) || !grid_fits(rows, 256)) return hipErrorInvalidConfiguration;
     auto* f = decode_kernel<T, D>;
     if (C::kLds > 64 * 1024) {
         const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(f),
@@ -356,7 +381,7 @@ hipError_t launch_decode_t(const DecodeArgs& a, const void* q, const void* k, co
                        part_o, part_ml);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.splits == 1) return e;
-    hipLaunchKernelGGL((join_kernel<T, D>), dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(256), 0, st, a, table,
+    hipLaunchKernelGGL((join_kernel<T, D>), dim3(static_cast<unsigned>(rows)), dim3(256), 0, st, a, table,
                        lengths, part_o, part_ml, static_cast<T*>(o));
     return hipGetLastError();
 }
@@ -400,14 +425,15 @@ int log2_of(int x) {
     return s;
 }
 
-// Parts per sequence and key head: enough workgroups for two rounds of the
-// 1024 that fit the GPU at a time (four per CU), no part below 256 keys of the
-// longest sequence the page table can hold.
+// Parts per sequence and key head: enough workgroups for several rounds of
+// what fits the GPU at a time, no part below 256 keys of the longest sequence
+// the page table can hold; up to 512 keys the second launch costs more than
+// the parts save.
 int decode_splits(int B, int Hkv, int G, int page_size, int max_pages, int window, int sinks) {
     long long keys = static_cast<long long>(max_pages) * page_size;
     if (window && keys > static_cast<long long>(window) + sinks) keys = static_cast<long long>(window) + sinks;
     const long long units = static_cast<long long>(B) * Hkv * ((G + 15) / 16);
-    if (units == 0) return 1;
+    if (units == 0 || keys <= 512) return 1;
     long long s = 2048 / units;
     if (s > (keys + 255) / 256) s = (keys + 255) / 256;
     return static_cast<int>(s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : s);

@@ -88,9 +88,9 @@ def test_backward(lib):
     for kw in (dict(B=0), dict(Hq=0), dict(Hq=0, Hkv=0), dict(Tq=0, Tk=0)):
         assert call(ptrs=[None] * 9, ws=None, n=0, **kw) == OK
     # sinks under a window need room for their partial sums; without a window they hide nothing
-    assert size(1, 1, 4096, 4096, 4, 2, 64, 128, 4) > size(1, 1, 4096, 4096, 4, 2, 64, 128, 0)
-    assert size(1, 1, 4096, 4096, 4, 2, 64, 0, 4) == size(1, 1, 4096, 4096, 4, 2, 64, 0, 0)
-    assert size(1, 1, 4096, 4096, 4, 2, 64, 4096, 4) == size(1, 1, 4096, 4096, 4, 2, 64, 0, 0)
+    assert size(1, 1, 65536, 65536, 4, 2, 64, 128, 4) > size(1, 1, 65536, 65536, 4, 2, 64, 128, 0)
+    assert size(1, 1, 65536, 65536, 4, 2, 64, 0, 4) == size(1, 1, 65536, 65536, 4, 2, 64, 0, 0)
+    assert size(1, 1, 65536, 65536, 4, 2, 64, 65536, 4) == size(1, 1, 65536, 65536, 4, 2, 64, 0, 0)
     for bad in ((5, 1, 8, 8, 4, 2, 64, 0, 0), (1, -1, 8, 8, 4, 2, 64, 0, 0), (1, 1, 8, 8, 4, 3, 64, 0, 0),
                 (1, 1, 8, 8, 4, 2, 80, 0, 0), (1, 1, BIG, 8, 4, 2, 64, 0, 0), (1, 1, 0, 8, 4, 2, 64, 0, 0)):
         assert size(*bad) == 0, bad
