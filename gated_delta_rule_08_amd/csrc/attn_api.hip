@@ -129,7 +129,7 @@ size_t gdr_attn_decode_workspace_bytes(int dtype, int B, int Hq, int Hkv, int d,
         page_checks(Hkv, page_size, 0, max_pages) != GDR_OK || B == 0 || Hq == 0 || max_pages == 0)
         return 0;
     window = clamp_window(window, max_pages * page_size);
-    return gdr::attn_decode_workspace_floats(B, Hq, Hkv, d, page_size, max_pages, window,
+    return gdr::attn_decode_workspace_floats(Hq, Hkv, d, page_size, max_pages, window,
                                              clamp_sinks(sinks, window, max_pages * page_size)) *
            sizeof(float);
 }

@@ -26,10 +26,6 @@ namespace gdr {
 namespace attn {
 namespace {
 
-__device__ __forceinline__ void tile_barrier() {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-}
-
 constexpr int kWaves = 4;
 constexpr int kKeys = 32 * kWaves;  // keys of a dkdv workgroup
 constexpr int kRows = 32 * kWaves;  // rows of a dq workgroup
@@ -170,7 +166,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && WAVES == 4 ? 2 : 1) v
     const size_t q0 = (static_cast<size_t>(b) * a.Tq * a.Hq + static_cast<size_t>(hk) * a.G.d) * D;
 
     auto fetch = [&](int i) {
-        unsigned char* buf = smem + (i & 1) * C::kBuf;
+        const uint32_t buf = lds_addr(smem) + (i & 1) * C::kBuf;
         const int r0 = lo + BM * i, i0 = a.G(r0);
         const size_t base = q0 + static_cast<size_t>(i0) * a.Hq * D;
         copy_rows<T, D, BM, WAVES>(buf, q + base, buf + C::kTile, go + base, wave, lane, [&](int r) {
@@ -179,7 +175,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && WAVES == 4 ? 2 : 1) v
         });
         if (wave < NM) {  // lanes 0..31: lse2, 32..63: delta
             const int r = min(32 * wave + (lane & 31), a.rows - 1 - r0);
-            copy_words(smem + C::kStat + (i & 1) * C::kStatBuf + 256 * wave, stat + r0, 4u * (h2 * a.pitch + r));
+            copy_words(lds_addr(smem) + C::kStat + (i & 1) * C::kStatBuf + 256 * wave, stat + r0, 4u * (h2 * a.pitch + r));
         }
     };
     const int n = (hi - lo + BM - 1) / BM;
@@ -394,7 +390,7 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(T) == 2 ? 2 : 1) void dq_kernel
     const T* vbase = v + (static_cast<size_t>(b) * a.Tk * a.Hkv + hk) * D;
     auto tile_of = [&](int i) { return i < t_sink ? i : i - t_sink + t_lo; };
     auto fetch = [&](int i) {
-        unsigned char* buf = smem + (i & (C::kBufs - 1)) * 2 * C::kTile;
+        const uint32_t buf = lds_addr(smem) + (i & (C::kBufs - 1)) * 2 * C::kTile;
         const int j0 = tile_of(i) * BN;
         copy_rows<T, D, BN, kWaves>(buf, kbase + j0 * kstride, buf + C::kTile, vbase + j0 * kstride, wave, lane,
                                     [&](int r) { return min(r, a.Tk - 1 - j0) * a.Hkv * D; });

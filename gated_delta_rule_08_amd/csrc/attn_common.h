@@ -226,13 +226,40 @@ template <int D> struct ColRead<float, D> {
     }
 };
 
-// One instruction of a wave: 1024 bytes from `base` + the lanes' offsets into
-// 1024 consecutive bytes of LDS, lane by lane.
-__device__ __forceinline__ void copy_1k(unsigned char* lds, const void* base, uint32_t off) {
-    const auto* src = static_cast<const unsigned char*>(base) + off;
-    __builtin_amdgcn_global_load_lds(
-        reinterpret_cast<const uint32_t __attribute__((address_space(1)))*>(reinterpret_cast<uintptr_t>(src)),
-        (__attribute__((address_space(3))) uint32_t*)(lds), 16, 0, 0);
+// Copies straight from global memory to LDS, one instruction of a wave: lane
+// by lane, 16 bytes each into 1024 consecutive bytes (4 bytes each into 256).
+// They are written as assembly because the compiler would wait for a copy
+// before any later LDS read that it cannot tell apart from it, which is every
+// read of the other buffer: the kernels wait themselves (vmcnt, before the
+// barrier or the read that needs the copy).  They return nothing in registers;
+// M0, the destination, serves no other instruction of these kernels.
+// lds: wave-uniform byte address in LDS (lds_addr).
+__device__ __forceinline__ uint32_t lds_addr(const void* p) {
+    return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const void*)p));
+}
+__device__ __forceinline__ void copy_1k(uint32_t lds, const void* base, uint32_t off) {  // base is wave-uniform
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_words(uint32_t lds, const void* base, uint32_t off) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(off), "s"(base)
+                 : "memory");
+}
+__device__ __forceinline__ void stream_1k(uint32_t lds, const void* p) {  // an address per lane, not to be cached
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off nt" ::"s"(lds), "v"(p) : "memory");
+}
+__device__ __forceinline__ void gather_words(uint32_t lds, const void* p) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(p) : "memory");
+}
+
+// This wave's copies and loads have landed, its LDS accesses are done, and every
+// wave has come this far: buffers filled before may be read, buffers read
+// before may be refilled.
+__device__ __forceinline__ void tile_barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
 }
 
 // Copies ROWS rows of two tensors of one layout into two LDS tiles, straight
@@ -241,8 +268,8 @@ __device__ __forceinline__ void copy_1k(unsigned char* lds, const void* base, ui
 // offset of row r of the tile from the (wave-uniform) bases.  The caller waits
 // for the copies (vmcnt) and passes a barrier before reading them.
 template <typename T, int D, int ROWS, int WAVES, typename OffsetFn>
-__device__ __forceinline__ void copy_rows(unsigned char* tile_a, const T* a, unsigned char* tile_b, const T* b,
-                                          int wave, int lane, OffsetFn offset) {
+__device__ __forceinline__ void copy_rows(uint32_t tile_a, const T* a, uint32_t tile_b, const T* b, int wave, int lane,
+                                          OffsetFn offset) {
     using L = Tile<T, D>;
     constexpr int kPer = 1024 / L::kRow, kInstr = ROWS / kPer;
     static_assert(1024 % L::kRow == 0 && kInstr % WAVES == 0, "whole rows, the same number for every wave");
@@ -255,14 +282,6 @@ __device__ __forceinline__ void copy_rows(unsigned char* tile_a, const T* a, uns
         copy_1k(tile_b + jj * 1024, b, off);
     }
 }
-// One word per lane, into 256 consecutive bytes.
-__device__ __forceinline__ void copy_words(unsigned char* lds, const float* base, uint32_t off) {
-    const auto* src = reinterpret_cast<const unsigned char*>(base) + off;
-    __builtin_amdgcn_global_load_lds(
-        reinterpret_cast<const uint32_t __attribute__((address_space(1)))*>(reinterpret_cast<uintptr_t>(src)),
-        (__attribute__((address_space(3))) uint32_t*)(lds), 4, 0, 0);
-}
-
 // Keys and queries of one sequence.  Query i is at position i + off; key j is
 // visible to position p if j <= p and (window == 0 or j > p - window or j <
 // sinks).  window is at most the number of keys, so p + window cannot wrap.

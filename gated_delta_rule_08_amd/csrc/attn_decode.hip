@@ -6,15 +6,19 @@
 // one contiguous block.  The step reads every visible key and value once and
 // does 4 d flops per query head and key with them: HBM-bound for any group a
 // model uses.  It is therefore built for bytes in flight: each wave streams
-// its own 32 keys per step, K straight into operand registers, V through
-// registers into a wave-private LDS tile (the transposing reads supply the
-// second product's operand), the next step's loads issued as soon as the
-// registers are free; no barrier until the end.  The group's query heads are
+// its own 32 keys per step into LDS tiles of its own, straight from memory, the
+// next step's keys requested as soon as this step's are read, the values
+// likewise; no registers hold them, and no barrier until the end.  The group's query heads are
 // the 16 columns of S^T = K Q^T, so a key read serves every head of its group.
 //
-// The visible keys of a sequence are a list (the sinks, then the window) cut
-// into equal parts, one workgroup each, where B x Hkv alone would not fill the
-// GPU; a second kernel joins the parts' (m, l, O) in order.
+// The visible keys of a sequence are a list (the sinks, then the window) in
+// blocks of 128.  Sequences differ in length, so it is not they that are dealt
+// out but the blocks: the blocks of all (sequence, key head) units in a row are
+// cut into equal shares, one per workgroup, whatever the lengths are.  A
+// workgroup finds its share from the lengths alone (a scan over the batch),
+// writes the units it holds whole, and leaves (m, l, O) of the at most two it
+// shares with others to a second kernel, which joins them in order.  Lengths
+// of at most 512 keys take one workgroup per unit and no join.
 #include "attn_common.h"
 
 namespace gdr {
@@ -23,15 +27,15 @@ namespace {
 
 constexpr int kWaves = 4;
 constexpr int kStep = 32;                // keys of a wave's step
-constexpr int kGrain = kStep * kWaves;   // keys of a workgroup's step
-constexpr int kMaxSplits = 64;
+constexpr int kBlock = kStep * kWaves;   // keys of a workgroup's step
 
 struct DecodeArgs {
     int B, Hq, Hkv, G, head_tiles;
     int page_shift, num_pages, max_pages;
     int window, sinks;
     float scale;
-    int splits;
+    int shares;  // workgroups the blocks are dealt to; 0: one workgroup per unit
+    int heads;   // query heads of a unit: min(16, G)
 };
 
 // What one sequence's step covers, from its device data alone (the same in
@@ -41,8 +45,7 @@ struct Span {
     int w_lo;    // first key of the window
     int sinks;   // keys before it that stay visible
     int count;   // visible keys
-    int chunk;   // keys of one part
-    int parts;   // parts that hold keys
+    int blocks;
 };
 
 __device__ __forceinline__ Span span_of(const DecodeArgs& a, int b, const int* __restrict__ table,
@@ -50,6 +53,7 @@ __device__ __forceinline__ Span span_of(const DecodeArgs& a, int b, const int* _
     Span s;
     const int p = lengths[b];
     s.pos = -1;
+    s.blocks = 0;
     if (p < 0 || (p >> a.page_shift) >= a.max_pages) return s;
     const int page = table[static_cast<size_t>(b) * a.max_pages + (p >> a.page_shift)];
     if (page < 0 || page >= a.num_pages) return s;
@@ -57,17 +61,62 @@ __device__ __forceinline__ Span span_of(const DecodeArgs& a, int b, const int* _
     s.w_lo = a.window ? max(0, p - a.window + 1) : 0;
     s.sinks = min(a.sinks, s.w_lo);
     s.count = s.sinks + (p - s.w_lo) + 1;
-    const int even = (s.count - 1) / a.splits + 1;
-    s.chunk = ((even - 1) / kGrain + 1) * kGrain;
-    s.parts = (s.count - 1) / s.chunk + 1;
+    s.blocks = (s.count - 1) / kBlock + 1;
     return s;
 }
 
+// The blocks of the batch in a row: sequence by sequence, within one unit by
+// unit (key head, 16 query heads), `per` units each.  A wave sums them 64
+// sequences at a time.
+__device__ __forceinline__ int scan64(int x, int lane) {  // inclusive
+#pragma unroll
+    for (int s = 1; s < 64; s <<= 1) {
+        const int y = __shfl_up(x, s);
+        if (lane >= s) x += y;
+    }
+    return x;
+}
+__device__ __forceinline__ long long blocks_before(const DecodeArgs& a, int b, const int* table, const int* lengths,
+                                                   int lane) {  // of one unit per sequence, sequences 0 .. b-1
+    long long sum = 0;
+    for (int at = 0; at < b; at += 64)
+        sum += __shfl(scan64(at + lane < b ? span_of(a, at + lane, table, lengths).blocks : 0, lane), 63);
+    return sum;
+}
+// Shares in use: no share is empty, so a unit's parts are consecutive shares.
+__device__ __forceinline__ int shares_of(const DecodeArgs& a, long long n) {
+    return static_cast<int>(n < a.shares ? n : a.shares);
+}
+// The share that holds block g of n, share w being blocks [w n / W, (w+1) n / W).
+__device__ __forceinline__ int owner(long long g, long long n, int W) {
+    return static_cast<int>(((g + 1) * W - 1) / n);
+}
+
 template <typename T, int D> struct DecodeCfg {
-    static constexpr int kTile = kStep * D * static_cast<int>(sizeof(T));  // a wave's V tile
-    static constexpr int kPitch = D + 4;                                   // floats of a joined row
+    static constexpr int kTile = kStep * D * static_cast<int>(sizeof(T));  // a wave's K or V tile
+    static constexpr int kTable = 512;                                     // and its table entries, two steps
+    static constexpr int kWave = 2 * kTile + kTable;
+    static constexpr int kPitch = D + 4;  // floats of a joined row
     static constexpr int kJoin = kWaves * 16 * (kPitch + 2) * 4;
-    static constexpr int kLds = kWaves * kTile > kJoin ? kWaves * kTile : kJoin;
+    static constexpr int kLds = kWaves * kWave > kJoin ? kWaves * kWave : kJoin;
+};
+
+// Row fragment for 16x16x32 products: lane (c = lane % 16, h = lane / 16) gets
+// elements 32 e + 8 h .. + 7 of row c.
+template <typename T, int D> struct RowRead16;
+template <int D> struct RowRead16<bf16_t, D> {
+    __device__ __forceinline__ static int base(int lane) { return Tile<bf16_t, D>::at(lane & 15) ^ ((lane >> 4) << 4); }
+    __device__ __forceinline__ static bf16x8v get(const unsigned char* lds, int base, int e) {
+        return __builtin_bit_cast(bf16x8v, *reinterpret_cast<const uint4*>(lds + (base ^ (e << 6))));
+    }
+};
+template <int D> struct RowRead16<float, D> {
+    __device__ __forceinline__ static int base(int lane) { return Tile<float, D>::at(lane & 15) ^ ((lane >> 4) << 5); }
+    __device__ __forceinline__ static f32x8 get(const unsigned char* lds, int base, int e) {
+        const f32x4 a = *reinterpret_cast<const f32x4*>(lds + (base ^ (e << 7)));
+        const f32x4 b = *reinterpret_cast<const f32x4*>(lds + (base ^ (e << 7) ^ 16));
+        return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
 };
 
 // Column fragment of a 32-row tile for 16x16x32 products: lane (c = lane % 16,
@@ -105,245 +154,341 @@ template <int D> struct ColRead16<float, D> {
     }
 };
 
-// 16-byte loads of the pages: read once, so they need not stay in the caches.
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-__device__ __forceinline__ u32x4 stream16(const void* p) {
-    return __builtin_nontemporal_load(static_cast<const u32x4*>(p));
+// At most n of this wave's latest loads and copies are still on their way.
+template <int N> __device__ __forceinline__ void wait_loads() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0f70 | (N & 15) | ((N >> 4) << 14));
+    asm volatile("" ::: "memory");
 }
-__device__ __forceinline__ bf16x8v stream8(const bf16_t* p) { return __builtin_bit_cast(bf16x8v, stream16(p)); }
-__device__ __forceinline__ f32x8 stream8(const float* p) {
-    const f32x4 a = __builtin_bit_cast(f32x4, stream16(p)), b = __builtin_bit_cast(f32x4, stream16(p + 4));
-    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+// This wave's LDS reads have returned: what they read may be overwritten.
+__device__ __forceinline__ void wait_lds() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xc07f);
+    asm volatile("" ::: "memory");
 }
 
 template <typename T, int D>
-__global__ __launch_bounds__(64 * kWaves) void decode_kernel(
+__global__ __launch_bounds__(64 * kWaves, sizeof(T) * D <= 256 ? 2 : 1) void decode_kernel(
     DecodeArgs a, const T* __restrict__ q, const T* __restrict__ knew, const T* __restrict__ vnew, T* k_pages,
     T* v_pages, const int* __restrict__ table, const int* __restrict__ lengths, T* __restrict__ o,
     float* __restrict__ part_o, float* __restrict__ part_ml) {
     using C = DecodeCfg<T, D>;
     using L = Tile<T, D>;
     constexpr int KS = D / 32, DT = D / 16;
-    constexpr int kPer = 1024 / L::kRow, kVLoads = kStep / kPer;  // rows of one V load instruction
+    constexpr int kPer = 1024 / L::kRow, kCopies = kStep / kPer;  // rows of one copy, copies of a tile
     constexpr int kNone = -1, kNew = -2;
     extern __shared__ unsigned char smem[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c16 = lane & 15, h4 = lane >> 4;
 
-    int id = blockIdx.x;
-    const int split = id % a.splits;
-    id /= a.splits;
-    const int ht = id % a.head_tiles;
-    id /= a.head_tiles;
-    const int hk = id % a.Hkv, b = id / a.Hkv;
-    const Span sp = span_of(a, b, table, lengths);
-    if (sp.pos < 0 || split >= sp.parts) return;
-
-    const int slot_mask = (1 << a.page_shift) - 1;
-    const int* trow = table + static_cast<size_t>(b) * a.max_pages;
-    const size_t new_row = static_cast<size_t>(b) * a.Hkv + hk;
-    if (split == 0 && ht == 0 && threadIdx.x < 2 * L::kUnits) {  // the new token into its page
-        const bool val = threadIdx.x >= L::kUnits;
-        const int u = threadIdx.x % L::kUnits;
-        const int page = trow[sp.pos >> a.page_shift];
-        const size_t row = ((static_cast<size_t>(page) * a.Hkv + hk) << a.page_shift) + (sp.pos & slot_mask);
-        reinterpret_cast<uint4*>((val ? v_pages : k_pages) + row * D)[u] =
-            reinterpret_cast<const uint4*>((val ? vnew : knew) + new_row * D)[u];
-    }
-
-    const int head0 = hk * a.G + ht * 16, nheads = min(16, a.G - ht * 16);
-    frag_t<T> qf[KS];
-    {
-        const bool neg = a.scale < 0.f;
-        const T* qp = q + (static_cast<size_t>(b) * a.Hq + head0 + min(c16, nheads - 1)) * D + 8 * h4;
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-            qf[s] = load8(qp + 32 * s);
-            if (neg) qf[s] = -qf[s];
-        }
-    }
+    const int slot_mask = (1 << a.page_shift) - 1, per = a.Hkv * a.head_tiles;
     // a scale of 0 as one that no score survives: c -inf of a hidden key stays -inf
     const float c = fmaxf(fabsf(a.scale) * kLog2e, 1e-37f);
+    unsigned char *kt = smem + wave * C::kWave, *vt = kt + C::kTile, *tt = vt + C::kTile;
+    const uint32_t kt_at = lds_addr(kt), vt_at = lds_addr(vt), tt_at = lds_addr(tt);
+    const int kb = RowRead16<T, D>::base(lane), vb = ColRead16<T, D>::base(lane);
 
-    // Cache row of list entry i: the new token's own row is taken from the
-    // call's k and v (its page is being written); entries past the end and
-    // keys of an invalid page are hidden.
-    const int first = split * sp.chunk, last = min(sp.count, first + sp.chunk);
-    auto row_of = [&](int i) {
-        if (i >= last) return kNone;
-        const int key = i < sp.sinks ? i : i - sp.sinks + sp.w_lo;
-        if (key == sp.pos) return kNew;
-        const int page = trow[key >> a.page_shift];
-        if (page < 0 || page >= a.num_pages) return kNone;
-        return ((page * a.Hkv + hk) << a.page_shift) + (key & slot_mask);
-    };
-    frag_t<T> kf[2][KS];
-    u32x4 vr[kVLoads];
-    auto fetch = [&](int rid) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int r = __shfl(rid, 16 * u + c16);
-            const T* p = (r == kNew ? knew + new_row * D : k_pages + static_cast<size_t>(r) * D) + 8 * h4;
-#pragma unroll
-            for (int s = 0; s < KS; ++s) kf[u][s] = r == kNone ? zero_frag<T>() : stream8(p + 32 * s);
+    // this workgroup's blocks: [at_block, at_block + left) of unit `unit` of sequence b and on
+    int b, unit, at_block, left;
+    Span sp;
+    if (a.shares == 0) {
+        b = blockIdx.x / per;
+        unit = blockIdx.x - b * per;
+        sp = span_of(a, b, table, lengths);
+        at_block = 0;
+        left = sp.blocks;
+    } else {
+        const long long n = per * blocks_before(a, a.B, table, lengths, lane);
+        const int W = shares_of(a, n);
+        if (static_cast<int>(blockIdx.x) >= W) return;
+        const long long lo = n * blockIdx.x / W, hi = n * (blockIdx.x + 1) / W;
+        left = __builtin_amdgcn_readfirstlane(static_cast<int>(hi - lo));
+        long long before = 0;  // per unit
+        for (b = 0; b < a.B; b += 64) {
+            const int mine = b + lane < a.B ? span_of(a, b + lane, table, lengths).blocks : 0;
+            const int upto = scan64(mine, lane);
+            const uint64_t past = __ballot((before + upto) * per > lo);
+            if (past) {  // the first sequence that ends after lo
+                const int x = __builtin_ctzll(past);
+                before += __shfl(upto - mine, x);
+                b += x;
+                break;
+            }
+            before += __shfl(upto, 63);
         }
-#pragma unroll
-        for (int j = 0; j < kVLoads; ++j) {
-            const int r = __shfl(rid, kPer * j + lane / L::kUnits);
-            const T* p = r == kNew ? vnew + new_row * D : v_pages + static_cast<size_t>(r) * D;
-            vr[j] = r == kNone ? u32x4{0u, 0u, 0u, 0u} : stream16(p + (lane % L::kUnits) * (16 / sizeof(T)));
-        }
-    };
+        b = __builtin_amdgcn_readfirstlane(b);
+        if (b >= a.B) return;  // not reached unless the lengths change under the call
+        sp = span_of(a, b, table, lengths);
+        const long long in = lo - before * per;
+        unit = __builtin_amdgcn_readfirstlane(static_cast<int>(in / max(1, sp.blocks)));
+        at_block = __builtin_amdgcn_readfirstlane(static_cast<int>(in - static_cast<long long>(unit) * sp.blocks));
+    }
 
-    unsigned char* tile = smem + wave * C::kTile;
-    const int vb = ColRead16<T, D>::base(lane);
-    f32x4 acc[DT];
-#pragma unroll
-    for (int t = 0; t < DT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    float m = -INFINITY, l = 0.f;
-
-    int at = first + wave * kStep;
-    int rid = row_of(at + (lane & 31));
-    if (at < last) fetch(rid);
 #pragma unroll 1
-    for (; at < last; at += kGrain) {
-        const uint32_t shown = static_cast<uint32_t>(__ballot(rid != kNone));
-        const int next = row_of(at + kGrain + (lane & 31));
-        f32x4 s[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            s[u] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int e = 0; e < KS; ++e) s[u] = mma16(kf[u][e], qf[e], s[u]);
+    while (left > 0) {
+        if (unit >= per || sp.blocks == 0) {  // the next sequence that is not skipped
+            if (++b >= a.B) return;
+            unit = 0;
+            sp = span_of(a, b, table, lengths);
+            continue;
         }
-#pragma unroll
-        for (int j = 0; j < kVLoads; ++j)
-            *reinterpret_cast<u32x4*>(tile + (L::at(kPer * j + lane / L::kUnits) ^ ((lane % L::kUnits) << 4))) = vr[j];
-        rid = next;
-        if (at + kGrain < last) fetch(rid);
+        const int take = min(left, sp.blocks - at_block);
+        const int hk = unit / a.head_tiles, ht = unit - hk * a.head_tiles;
+        const int* trow = table + static_cast<size_t>(b) * a.max_pages;
+        const size_t new_row = static_cast<size_t>(b) * a.Hkv + hk;
+        if (at_block == 0 && ht == 0 && threadIdx.x < 2 * L::kUnits) {  // the new token into its page
+            const bool val = threadIdx.x >= L::kUnits;
+            const int u = threadIdx.x % L::kUnits;
+            const int page = trow[sp.pos >> a.page_shift];
+            const size_t row = ((static_cast<size_t>(page) * a.Hkv + hk) << a.page_shift) + (sp.pos & slot_mask);
+            reinterpret_cast<uint4*>((val ? v_pages : k_pages) + row * D)[u] =
+                reinterpret_cast<const uint4*>((val ? vnew : knew) + new_row * D)[u];
+        }
 
-        if (shown != 0xffffffffu) {
+        const int head0 = hk * a.G + ht * 16, nheads = min(16, a.G - ht * 16);
+        frag_t<T> qf[KS];
+        {
+            const bool neg = a.scale < 0.f;
+            const T* qp = q + (static_cast<size_t>(b) * a.Hq + head0 + min(c16, nheads - 1)) * D + 8 * h4;
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    if (!((shown >> (16 * u + 4 * h4 + r)) & 1)) s[u][r] = -INFINITY;
+            for (int s = 0; s < KS; ++s) {
+                qf[s] = load8(qp + 32 * s);
+                if (neg) qf[s] = -qf[s];
+            }
         }
-        float mx = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
-                         fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
-        mx = fmaxf(mx, __shfl_xor(mx, 16));
-        mx = fmaxf(m, fmaxf(mx, __shfl_xor(mx, 32)));
-        const float mc = mx == -INFINITY ? 0.f : mx * c;
-        if (__any(mx > m)) {
-            const float alpha = m == -INFINITY ? 0.f : ex2(m * c - mc);
-            l *= alpha;
-#pragma unroll
-            for (int t = 0; t < DT; ++t) acc[t] *= alpha;
-            m = mx;
-        }
-        float w[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            w[i] = ex2(fmaf(s[i >> 2][i & 3], c, -mc));
-            l += w[i];
-        }
-        const frag_t<T> pf = pack8<T>(w);
-#pragma unroll
-        for (int t = 0; t < DT; ++t) acc[t] = mma16(ColRead16<T, D>::get(tile, vb, t), pf, acc[t]);
-    }
-    l += __shfl_xor(l, 16);
-    l += __shfl_xor(l, 32);
 
-    // the four waves' parts, joined in LDS in wave order
-    __syncthreads();
-    float* jo = reinterpret_cast<float*>(smem);
-    float* jm = jo + kWaves * 16 * C::kPitch;
-    {
-        float* dst = jo + (wave * 16 + c16) * C::kPitch + 4 * h4;
+        // List entry i (entries past the end repeat the last one and are hidden):
+        // its key, and its row in the page tensors.  kNew: the new token's own
+        // row is taken from the call's k and v, as its page is being written.
+        const int first = at_block * kBlock, last = min(sp.count, first + take * kBlock);
+        auto key_of = [&](int i) {
+            i = min(i, last - 1);
+            return i < sp.sinks ? i : i - sp.sinks + sp.w_lo;
+        };
+        auto row_of = [&](int i, int page) {
+            const int key = key_of(i);
+            if (i >= last) return kNone;
+            if (key == sp.pos) return kNew;
+            if (page < 0 || page >= a.num_pages) return kNone;
+            return ((page * a.Hkv + hk) << a.page_shift) + (key & slot_mask);
+        };
+        // Copies on their way to LDS: the table entries of a step, its keys, its
+        // values (unit by unit, each lane fetching what belongs at its place;
+        // hidden rows read row 0).
+        auto fetch_table = [&](int i, int slot) {
+            gather_words(tt_at + 256 * slot, trow + (key_of(i) >> a.page_shift));
+        };
+        int row[kCopies];  // of the units this lane fetches
+        auto rows_to_lanes = [&](int rid) {
 #pragma unroll
-        for (int t = 0; t < DT; ++t) *reinterpret_cast<f32x4*>(dst + 16 * t) = acc[t];
-        if (h4 == 0) {
-            jm[(wave * 16 + c16) * 2] = m;
-            jm[(wave * 16 + c16) * 2 + 1] = l;
+            for (int j = 0; j < kCopies; ++j) row[j] = __shfl(rid, kPer * j + lane / L::kUnits);
+        };
+        auto fetch = [&](uint32_t lds, const T* pages, const T* fresh) {
+#pragma unroll
+            for (int j = 0; j < kCopies; ++j) {
+                const int u = (lane % L::kUnits) ^ L::swz(kPer * j + lane / L::kUnits);
+                const T* p = row[j] == kNew ? fresh + new_row * D : pages + static_cast<size_t>(max(row[j], 0)) * D;
+                stream_1k(lds + 1024 * j, p + u * (16 / sizeof(T)));
+            }
+        };
+
+        f32x4 acc[DT];
+#pragma unroll
+        for (int t = 0; t < DT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        float m = -INFINITY, l = 0.f;
+
+        // A wave's step: 32 keys.  Its table entries were fetched two steps
+        // before, its keys once the step before had read its own, its values once
+        // that step was done.
+        int at = first + wave * kStep, slot = 0, rid = kNone;
+        const int mine = lane & 31;
+        if (at < last) {
+            fetch_table(at + mine, 0);
+            fetch_table(at + kBlock + mine, 1);
+            wait_loads<0>();
+            rid = row_of(at + mine, *reinterpret_cast<const int*>(tt + 4 * mine));
+            rows_to_lanes(rid);
+            fetch(kt_at, k_pages, knew);
+            fetch(vt_at, v_pages, vnew);
         }
-    }
-    __syncthreads();
-    const int head = threadIdx.x >> 4;
-    if (head >= nheads) return;
-    float mw[kWaves], M = -INFINITY;
+#pragma unroll 1
+        for (; at < last; at += kBlock, slot ^= 1) {
+            const uint32_t shown = static_cast<uint32_t>(__ballot(rid != kNone));
+            const bool more = at + kBlock < last;
+            wait_loads<kCopies>();  // the keys; the values may still come
+            f32x4 s[2];
 #pragma unroll
-    for (int x = 0; x < kWaves; ++x) {
-        mw[x] = jm[(x * 16 + head) * 2];
-        M = fmaxf(M, mw[x]);
-    }
-    float lt = 0.f;
+            for (int u = 0; u < 2; ++u) {
+                s[u] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int x = 0; x < kWaves; ++x) {
-        mw[x] = mw[x] == -INFINITY ? 0.f : ex2((mw[x] - M) * c);
-        lt = fmaf(jm[(x * 16 + head) * 2 + 1], mw[x], lt);
-    }
-    const size_t orow = static_cast<size_t>(b) * a.Hq + head0 + head;
-    const bool whole = sp.parts == 1;
-    const float inv = whole ? (lt == 0.f ? 0.f : 1.f / lt) : 1.f;
-    const size_t prow = orow * a.splits + split;
+                for (int e = 0; e < KS; ++e)
+                    s[u] = mma16(RowRead16<T, D>::get(kt + 16 * u * L::kRow, kb, e), qf[e], s[u]);
+            }
+            if (more) {
+                rid = row_of(at + kBlock + mine, *reinterpret_cast<const int*>(tt + 256 * (slot ^ 1) + 4 * mine));
+                rows_to_lanes(rid);
+                wait_lds();
+                fetch_table(at + 2 * kBlock + mine, slot);
+                fetch(kt_at, k_pages, knew);
+            }
+            if (shown != 0xffffffffu) {
 #pragma unroll
-    for (int e = 0; e < D / 64; ++e) {
-        const int d = 64 * e + 4 * (threadIdx.x & 15);
-        f32x4 sum = f32x4{0.f, 0.f, 0.f, 0.f};
+                for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int x = 0; x < kWaves; ++x)
-            if (mw[x] != 0.f) sum += *reinterpret_cast<const f32x4*>(jo + (x * 16 + head) * C::kPitch + d) * mw[x];
-        if (whole)
-            store4<T>(o + orow * D + d, sum[0] * inv, sum[1] * inv, sum[2] * inv, sum[3] * inv);
-        else
-            *reinterpret_cast<f32x4*>(part_o + prow * D + d) = sum;
-    }
-    if (!whole && (threadIdx.x & 15) == 0) {
-        part_ml[prow * 2] = M == -INFINITY ? M : M * c;
-        part_ml[prow * 2 + 1] = lt;
+                    for (int r = 0; r < 4; ++r)
+                        if (!((shown >> (16 * u + 4 * h4 + r)) & 1)) s[u][r] = -INFINITY;
+            }
+            float mx = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
+                             fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
+            mx = fmaxf(mx, __shfl_xor(mx, 16));
+            mx = fmaxf(m, fmaxf(mx, __shfl_xor(mx, 32)));
+            const float mc = mx == -INFINITY ? 0.f : mx * c;
+            if (__any(mx > m)) {
+                const float alpha = m == -INFINITY ? 0.f : ex2(m * c - mc);
+                l *= alpha;
+#pragma unroll
+                for (int t = 0; t < DT; ++t) acc[t] *= alpha;
+                m = mx;
+            }
+            float w[8];
+#pragma unroll
+            for (int y = 0; y < 8; ++y) {
+                w[y] = ex2(fmaf(s[y >> 2][y & 3], c, -mc));
+                l += w[y];
+            }
+            const frag_t<T> pf = pack8<T>(w);
+            if (more)
+                wait_loads<kCopies + 1>();  // the values; the next keys and table entries may still come
+            else
+                wait_loads<0>();
+            if (shown != 0xffffffffu) {  // a weight of 0 needs a value that is finite
+#pragma unroll
+                for (int j = 0; j < kCopies; ++j)
+                    if (!((shown >> (kPer * j + lane / L::kUnits)) & 1))
+                        *reinterpret_cast<uint4*>(vt + 1024 * j + 16 * lane) = make_uint4(0u, 0u, 0u, 0u);
+            }
+#pragma unroll
+            for (int t = 0; t < DT; ++t) acc[t] = mma16(ColRead16<T, D>::get(vt, vb, t), pf, acc[t]);
+            if (more) {
+                wait_lds();
+                fetch(vt_at, v_pages, vnew);
+            }
+        }
+        l += __shfl_xor(l, 16);
+        l += __shfl_xor(l, 32);
+
+        // the four waves' parts, joined in LDS in wave order
+        __syncthreads();
+        float* jo = reinterpret_cast<float*>(smem);
+        float* jm = jo + kWaves * 16 * C::kPitch;
+        {
+            float* dst = jo + (wave * 16 + c16) * C::kPitch + 4 * h4;
+#pragma unroll
+            for (int t = 0; t < DT; ++t) *reinterpret_cast<f32x4*>(dst + 16 * t) = acc[t];
+            if (h4 == 0) {
+                jm[(wave * 16 + c16) * 2] = m;
+                jm[(wave * 16 + c16) * 2 + 1] = l;
+            }
+        }
+        __syncthreads();
+        const int head = threadIdx.x >> 4;
+        const bool whole = take == sp.blocks;
+        if (head < nheads) {
+            float mw[kWaves], M = -INFINITY;
+#pragma unroll
+            for (int x = 0; x < kWaves; ++x) {
+                mw[x] = jm[(x * 16 + head) * 2];
+                M = fmaxf(M, mw[x]);
+            }
+            float lt = 0.f;
+#pragma unroll
+            for (int x = 0; x < kWaves; ++x) {
+                mw[x] = mw[x] == -INFINITY ? 0.f : ex2((mw[x] - M) * c);
+                lt = fmaf(jm[(x * 16 + head) * 2 + 1], mw[x], lt);
+            }
+            const size_t orow = static_cast<size_t>(b) * a.Hq + head0 + head;
+            const float inv = lt == 0.f ? 0.f : 1.f / lt;
+            // a shared unit's part: slot 1 holds its beginning, slot 0 what does not begin here
+            const size_t prow = (static_cast<size_t>(blockIdx.x) * 2 + (at_block == 0)) * a.heads + head;
+#pragma unroll
+            for (int e = 0; e < D / 64; ++e) {
+                const int d = 64 * e + 4 * (threadIdx.x & 15);
+                f32x4 sum = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int x = 0; x < kWaves; ++x)
+                    if (mw[x] != 0.f) sum += *reinterpret_cast<const f32x4*>(jo + (x * 16 + head) * C::kPitch + d) * mw[x];
+                if (whole)
+                    store4<T>(o + orow * D + d, sum[0] * inv, sum[1] * inv, sum[2] * inv, sum[3] * inv);
+                else
+                    *reinterpret_cast<f32x4*>(part_o + prow * D + d) = sum;
+            }
+            if (!whole && (threadIdx.x & 15) == 0) {
+                part_ml[prow * 2] = M == -INFINITY ? M : M * c;
+                part_ml[prow * 2 + 1] = lt;
+            }
+        }
+        left -= take;
+        at_block = 0;
+        ++unit;
+        if (left > 0) __syncthreads();  // LDS is free for the next unit
     }
 }
 
-// Joins a sequence's parts, one workgroup per query head: every wave forms the
-// parts' weights 2^(m_s - max m) (lane s holds part s) and adds a quarter of
-// the parts, the channels over its lanes; the four sums are added in order.
+// Joins the parts of a shared unit, one workgroup per query head: part 0 is
+// slot 1 of the unit's first share, the others slot 0 of the shares after it.
+// 64 parts at a time, lane s holding part s's weight 2^(m_s - max m); a wave
+// adds every fourth part, the channels over its lanes, and the four sums are
+// added in order.
 template <typename T, int D>
 __global__ __launch_bounds__(256) void join_kernel(DecodeArgs a, const int* __restrict__ table,
                                                    const int* __restrict__ lengths,
                                                    const float* __restrict__ part_o,
                                                    const float* __restrict__ part_ml, T* __restrict__ o) {
-    constexpr int N = D / 64, W = 4;
+    constexpr int N = D / 64, W = 4, kEach = 64 / W;
     __shared__ float sums[W - 1][D];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const size_t row = blockIdx.x;
-    const Span sp = span_of(a, static_cast<int>(row / a.Hq), table, lengths);
-    if (sp.pos < 0 || sp.parts == 1) return;
-    const size_t prow = row * a.splits;
-    float m = -INFINITY, l = 0.f;
-    if (lane < sp.parts) {
-        m = part_ml[(prow + lane) * 2];
-        l = part_ml[(prow + lane) * 2 + 1];
-    }
-    const float* p = part_o + prow * D + N * lane;
-    float x[kMaxSplits / W][N];
+    const int b = blockIdx.x / a.Hq, hq = blockIdx.x - b * a.Hq;
+    const Span sp = span_of(a, b, table, lengths);
+    if (sp.pos < 0) return;
+    const int per = a.Hkv * a.head_tiles, hk = hq / a.G, g = hq - hk * a.G;
+    const long long n = per * blocks_before(a, a.B, table, lengths, lane);
+    const long long lo = per * blocks_before(a, b, table, lengths, lane) +
+                         static_cast<long long>(hk * a.head_tiles + g / 16) * sp.blocks;
+    const int used = shares_of(a, n), w0 = owner(lo, n, used), parts = owner(lo + sp.blocks - 1, n, used) - w0 + 1;
+    if (parts == 1) return;  // written whole
+    auto slot = [&](int s) { return (static_cast<size_t>(w0 + s) * 2 + (s == 0)) * a.heads + (g & 15); };
+    float M = -INFINITY, total = 0.f, acc[N] = {};
+    for (int s0 = 0; s0 < parts; s0 += 64) {
+        float m = -INFINITY, l = 0.f;
+        if (s0 + lane < parts) {
+            m = part_ml[slot(s0 + lane) * 2];
+            l = part_ml[slot(s0 + lane) * 2 + 1];
+        }
+        float x[kEach][N];
 #pragma unroll
-    for (int i = 0; i < kMaxSplits / W; ++i)  // all loads before the first use
+        for (int i = 0; i < kEach; ++i) {  // all loads before the first use
+            const int s = s0 + W * i + wave;
 #pragma unroll
-        for (int e = 0; e < N; ++e)
-            x[i][e] = W * i + wave < sp.parts ? p[static_cast<size_t>(W * i + wave) * D + e] : 0.f;
-    float M = m;
+            for (int e = 0; e < N; ++e) x[i][e] = s < parts ? part_o[slot(s) * D + N * lane + e] : 0.f;
+        }
+        float mx = m;
 #pragma unroll
-    for (int s = 1; s < 64; s <<= 1) M = fmaxf(M, __shfl_xor(M, s));
-    const float w = m == -INFINITY ? 0.f : ex2(m - M);
-    float total = l * w;
+        for (int s = 1; s < 64; s <<= 1) mx = fmaxf(mx, __shfl_xor(mx, s));
+        mx = fmaxf(M, mx);
+        const float old = M == -INFINITY ? 0.f : ex2(M - mx), w = m == -INFINITY ? 0.f : ex2(m - mx);
+        M = mx;
+        float add = l * w;
 #pragma unroll
-    for (int s = 1; s < 64; s <<= 1) total += __shfl_xor(total, s);
-    float acc[N] = {};
+        for (int s = 1; s < 64; s <<= 1) add += __shfl_xor(add, s);
+        total = total * old + add;
 #pragma unroll
-    for (int i = 0; i < kMaxSplits / W; ++i) {
-        const float ws = __shfl(w, W * i + wave);
+        for (int e = 0; e < N; ++e) acc[e] *= old;
 #pragma unroll
-        for (int e = 0; e < N; ++e) acc[e] = fmaf(ws, x[i][e], acc[e]);
+        for (int i = 0; i < kEach; ++i) {
+            const float ws = __shfl(w, W * i + wave);
+#pragma unroll
+            for (int e = 0; e < N; ++e) acc[e] = fmaf(ws, x[i][e], acc[e]);
+        }
     }
     if (wave > 0) {
 #pragma unroll
@@ -352,6 +497,7 @@ __global__ __launch_bounds__(256) void join_kernel(DecodeArgs a, const int* __re
     __syncthreads();
     if (wave > 0) return;
     const float inv = total == 0.f ? 0.f : 1.f / total;
+    const size_t row = static_cast<size_t>(b) * a.Hq + hq;
 #pragma unroll
     for (int e = 0; e < N; ++e) {
 #pragma unroll
@@ -364,8 +510,14 @@ template <typename T, int D>
 hipError_t launch_decode_t(const DecodeArgs& a, const void* q, const void* k, const void* v, void* k_pages,
                            void* v_pages, const int* table, const int* lengths, void* o, float* ws, hipStream_t st) {
     using C = DecodeCfg<T, D>;
-    const unsigned long long blocks = static_cast<unsigned long long>(a.B) * a.Hkv * a.head_tiles * a.splits;
+    const unsigned long long blocks =
+        a.shares ? a.shares : static_cast<unsigned long long>(a.B) * a.Hkv * a.head_tiles;
     const unsigned long long rows = static_cast<unsigned long long>(a.B) * a.Hq;
+    // a share's blocks have to fit an int
+    if (a.shares && static_cast<unsigned long long>(a.B) * a.Hkv * a.head_tiles *
+                            ((static_cast<unsigned long long>(a.max_pages) << a.page_shift) / kBlock + 1) / a.shares >
+                        0x7fffffffull)
+        return hipErrorInvalidConfiguration;
     if (!grid_fits(blocks, 64 * kWaves) || !grid_fits(rows, 256)) return hipErrorInvalidConfiguration;
     auto* f = decode_kernel<T, D>;
     if (C::kLds > 64 * 1024) {
@@ -374,13 +526,13 @@ hipError_t launch_decode_t(const DecodeArgs& a, const void* q, const void* k, co
         if (e != hipSuccess) return e;
     }
     float* part_o = ws;
-    float* part_ml = ws ? ws + rows * a.splits * D : nullptr;
+    float* part_ml = ws ? ws + static_cast<size_t>(a.shares) * 2 * a.heads * D : nullptr;
     hipLaunchKernelGGL(f, dim3(static_cast<unsigned>(blocks)), dim3(64 * kWaves), C::kLds, st, a,
                        static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v),
                        static_cast<T*>(k_pages), static_cast<T*>(v_pages), table, lengths, static_cast<T*>(o),
                        part_o, part_ml);
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess || a.splits == 1) return e;
+    if (e != hipSuccess || a.shares == 0) return e;
     hipLaunchKernelGGL((join_kernel<T, D>), dim3(static_cast<unsigned>(rows)), dim3(256), 0, st, a, table,
                        lengths, part_o, part_ml, static_cast<T*>(o));
     return hipGetLastError();
@@ -425,27 +577,21 @@ int log2_of(int x) {
     return s;
 }
 
-// Parts per sequence and key head: enough workgroups for several rounds of
-// what fits the GPU at a time, no part below 256 keys of the longest sequence
-// the page table can hold; up to 512 keys the second launch costs more than
-// the parts save.
-int decode_splits(int B, int Hkv, int G, int page_size, int max_pages, int window, int sinks) {
+// Shares of the blocks: two workgroups per CU, which the registers and LDS of
+// the largest kernels allow at a time, so that all start and end together; none
+// (one workgroup per unit) where no sequence can show more than 512 keys.
+int decode_shares(int page_size, int max_pages, int window, int sinks) {
     long long keys = static_cast<long long>(max_pages) * page_size;
     if (window && keys > static_cast<long long>(window) + sinks) keys = static_cast<long long>(window) + sinks;
-    const long long units = static_cast<long long>(B) * Hkv * ((G + 15) / 16);
-    if (units == 0 || keys <= 512) return 1;
-    long long s = 2048 / units;
-    if (s > (keys + 255) / 256) s = (keys + 255) / 256;
-    return static_cast<int>(s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : s);
+    return keys <= 512 ? 0 : 512;
 }
 
 }  // namespace
 }  // namespace attn
 
-size_t attn_decode_workspace_floats(int B, int Hq, int Hkv, int d, int page_size, int max_pages, int window,
-                                    int sinks) {
-    const int s = attn::decode_splits(B, Hkv, Hq / Hkv, page_size, max_pages, window, sinks);
-    return s == 1 ? 0 : static_cast<size_t>(B) * Hq * s * (d + 2);
+size_t attn_decode_workspace_floats(int Hq, int Hkv, int d, int page_size, int max_pages, int window, int sinks) {
+    const int G = Hq / Hkv;
+    return static_cast<size_t>(attn::decode_shares(page_size, max_pages, window, sinks)) * 2 * (G < 16 ? G : 16) * (d + 2);
 }
 
 hipError_t launch_attn_decode(int dtype, int B, int Hq, int Hkv, int d, int page_size, int num_pages, int max_pages,
@@ -464,7 +610,8 @@ hipError_t launch_attn_decode(int dtype, int B, int Hq, int Hkv, int d, int page
     a.window = window;
     a.sinks = sinks;
     a.scale = scale;
-    a.splits = attn::decode_splits(B, Hkv, a.G, page_size, max_pages, window, sinks);
+    a.shares = attn::decode_shares(page_size, max_pages, window, sinks);
+    a.heads = a.G < 16 ? a.G : 16;
     auto* f = dtype == GDR_DTYPE_F32 ? (d == 64 ? attn::launch_decode_t<float, 64> : attn::launch_decode_t<float, 128>)
                                      : (d == 64 ? attn::launch_decode_t<bf16_t, 64> : attn::launch_decode_t<bf16_t, 128>);
     return f(a, q, k, v, k_pages, v_pages, table, lengths, o, ws, st);

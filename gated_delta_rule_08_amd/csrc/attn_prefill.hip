@@ -21,12 +21,6 @@ namespace gdr {
 namespace attn {
 namespace {
 
-// Copies issued before this point have landed and every wave has read what it
-// needed: LDS may be read and the other buffer refilled.
-__device__ __forceinline__ void tile_barrier() {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-}
-
 constexpr int kWaves = 4;
 constexpr int kRows = 32 * kWaves;  // query rows of a workgroup
 
@@ -154,7 +148,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prefill_kernel(PrefillArgs a, 
     const T* vbase = v + (k0 * a.Hkv + hk) * D;
     auto tile_of = [&](int i) { return i < t_sink ? i : i - t_sink + t_lo; };
     auto fetch = [&](int i) {
-        unsigned char* buf = smem + (i & (C::kBufs - 1)) * 2 * C::kTileBytes;
+        const uint32_t buf = lds_addr(smem) + (i & (C::kBufs - 1)) * 2 * C::kTileBytes;
         const int j0 = tile_of(i) * BN;
         copy_rows<T, D, BN, kWaves>(buf, kbase + j0 * kstride, buf + C::kTileBytes, vbase + j0 * kstride, wave, lane,
                                     [&](int r) { return min(r, Tk - 1 - j0) * a.Hkv * D; });

@@ -143,8 +143,7 @@ hipError_t launch_attn_backward(int dtype, int B, int Tq, int Tk, int Hq, int Hk
                                 float scale, const void* q, const void* k, const void* v, const void* o,
                                 const float* lse, const void* go, void* gq, void* gk, void* gv, float* ws,
                                 hipStream_t s);
-size_t attn_decode_workspace_floats(int B, int Hq, int Hkv, int d, int page_size, int max_pages, int window,
-                                    int sinks);
+size_t attn_decode_workspace_floats(int Hq, int Hkv, int d, int page_size, int max_pages, int window, int sinks);
 hipError_t launch_attn_decode(int dtype, int B, int Hq, int Hkv, int d, int page_size, int num_pages, int max_pages,
                               int window, int sinks, float scale, const void* q, const void* k, const void* v,
                               void* k_pages, void* v_pages, const int* table, const int* lengths, void* o, float* ws,
