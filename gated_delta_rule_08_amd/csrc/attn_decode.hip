@@ -38,36 +38,34 @@ struct DecodeArgs {
     int heads;   // query heads of a unit: min(16, G)
 };
 
-// What one sequence's step covers, from its device data alone (the same in
-// every workgroup and in the join).
+// What one sequence's step covers, from its length alone (the same in every
+// workgroup and in the join).
 struct Span {
-    int pos;     // position of the new token; -1: the sequence is skipped
+    int pos;     // position of the new token
     int w_lo;    // first key of the window
     int sinks;   // keys before it that stay visible
     int count;   // visible keys
-    int blocks;
+    int blocks;  // 0: the length is out of range
 };
-
-__device__ __forceinline__ Span span_of(const DecodeArgs& a, int b, const int* __restrict__ table,
-                                        const int* __restrict__ lengths) {
+__device__ __forceinline__ Span span_of(const DecodeArgs& a, int p) {
     Span s;
-    const int p = lengths[b];
-    s.pos = -1;
-    s.blocks = 0;
-    if (p < 0 || (p >> a.page_shift) >= a.max_pages) return s;
-    const int page = table[static_cast<size_t>(b) * a.max_pages + (p >> a.page_shift)];
-    if (page < 0 || page >= a.num_pages) return s;
     s.pos = p;
     s.w_lo = a.window ? max(0, p - a.window + 1) : 0;
     s.sinks = min(a.sinks, s.w_lo);
     s.count = s.sinks + (p - s.w_lo) + 1;
-    s.blocks = (s.count - 1) / kBlock + 1;
+    s.blocks = p < 0 || (p >> a.page_shift) >= a.max_pages ? 0 : (s.count - 1) / kBlock + 1;
     return s;
+}
+// A sequence whose new position has no page is skipped (its blocks count all
+// the same).
+__device__ __forceinline__ bool has_page(const DecodeArgs& a, int b, int p, const int* __restrict__ table) {
+    const int page = table[static_cast<size_t>(b) * a.max_pages + (p >> a.page_shift)];
+    return page >= 0 && page < a.num_pages;
 }
 
 // The blocks of the batch in a row: sequence by sequence, within one unit by
-// unit (key head, 16 query heads), `per` units each.  A wave sums them 64
-// sequences at a time.
+// unit (key head, 16 query heads), `per` units each.  A wave sums them 256
+// sequences at a time, four to a lane, so that their lengths come together.
 __device__ __forceinline__ int scan64(int x, int lane) {  // inclusive
 #pragma unroll
     for (int s = 1; s < 64; s <<= 1) {
@@ -76,13 +74,38 @@ __device__ __forceinline__ int scan64(int x, int lane) {  // inclusive
     }
     return x;
 }
-__device__ __forceinline__ long long blocks_before(const DecodeArgs& a, int b, const int* table, const int* lengths,
-                                                   int lane) {  // of one unit per sequence, sequences 0 .. b-1
+struct Blocks4 {
+    int each[4], upto;  // of sequences at + 4 lane .. + 3; blocks of at .. and these
+};
+__device__ __forceinline__ Blocks4 blocks_of(const DecodeArgs& a, int at, const int* __restrict__ lengths, int lane) {
+    Blocks4 r;
+    int sum = 0, len[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) len[x] = at + 4 * lane + x < a.B ? lengths[at + 4 * lane + x] : -1;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) sum += r.each[x] = span_of(a, len[x]).blocks;
+    r.upto = scan64(sum, lane);
+    return r;
+}
+// Blocks of one unit per sequence: of the whole batch, and of the sequences before b.
+__device__ __forceinline__ long long all_blocks(const DecodeArgs& a, const int* lengths, int lane, int b, long long& before) {
     long long sum = 0;
-    for (int at = 0; at < b; at += 64)
-        sum += __shfl(scan64(at + lane < b ? span_of(a, at + lane, table, lengths).blocks : 0, lane), 63);
+    before = 0;
+    for (int at = 0; at < a.B; at += 256) {
+        const Blocks4 r = blocks_of(a, at, lengths, lane);
+        if (b >= at && b < at + 256) {
+            const int x = b - at, rest = x & 3;
+            int mine = r.upto;  // up to and with this lane's four, less those not before b
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+                if (y >= rest) mine -= r.each[y];
+            before = sum + __shfl(mine, x >> 2);
+        }
+        sum += __shfl(r.upto, 63);
+    }
     return sum;
 }
+
 // Shares in use: no share is empty, so a unit's parts are consecutive shares.
 __device__ __forceinline__ int shares_of(const DecodeArgs& a, long long n) {
     return static_cast<int>(n < a.shares ? n : a.shares);
@@ -194,31 +217,38 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(T) * D <= 256 ? 2 : 1) void dec
     if (a.shares == 0) {
         b = blockIdx.x / per;
         unit = blockIdx.x - b * per;
-        sp = span_of(a, b, table, lengths);
+        sp = span_of(a, lengths[b]);
         at_block = 0;
         left = sp.blocks;
     } else {
-        const long long n = per * blocks_before(a, a.B, table, lengths, lane);
+        long long before;
+        const long long n = per * all_blocks(a, lengths, lane, -1, before);
         const int W = shares_of(a, n);
         if (static_cast<int>(blockIdx.x) >= W) return;
         const long long lo = n * blockIdx.x / W, hi = n * (blockIdx.x + 1) / W;
         left = __builtin_amdgcn_readfirstlane(static_cast<int>(hi - lo));
-        long long before = 0;  // per unit
-        for (b = 0; b < a.B; b += 64) {
-            const int mine = b + lane < a.B ? span_of(a, b + lane, table, lengths).blocks : 0;
-            const int upto = scan64(mine, lane);
-            const uint64_t past = __ballot((before + upto) * per > lo);
-            if (past) {  // the first sequence that ends after lo
-                const int x = __builtin_ctzll(past);
-                before += __shfl(upto - mine, x);
-                b += x;
+        before = 0;  // per unit
+        for (b = 0; b < a.B; b += 256) {  // the first sequence that ends after lo
+            const Blocks4 r = blocks_of(a, b, lengths, lane);
+            const uint64_t past = __ballot((before + r.upto) * per > lo);
+            if (past) {
+                int x = 0, upto = r.upto - r.each[0] - r.each[1] - r.each[2] - r.each[3];
+#pragma unroll
+                for (int y = 0; y < 3; ++y)
+                    if (x == y && (before + upto + r.each[y]) * per <= lo) {
+                        upto += r.each[y];
+                        ++x;
+                    }
+                const int from = __builtin_ctzll(past);
+                before += __shfl(upto, from);
+                b += 4 * from + __shfl(x, from);
                 break;
             }
-            before += __shfl(upto, 63);
+            before += __shfl(r.upto, 63);
         }
         b = __builtin_amdgcn_readfirstlane(b);
         if (b >= a.B) return;  // not reached unless the lengths change under the call
-        sp = span_of(a, b, table, lengths);
+        sp = span_of(a, lengths[b]);
         const long long in = lo - before * per;
         unit = __builtin_amdgcn_readfirstlane(static_cast<int>(in / max(1, sp.blocks)));
         at_block = __builtin_amdgcn_readfirstlane(static_cast<int>(in - static_cast<long long>(unit) * sp.blocks));
@@ -229,10 +259,16 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(T) * D <= 256 ? 2 : 1) void dec
         if (unit >= per || sp.blocks == 0) {  // the next sequence that is not skipped
             if (++b >= a.B) return;
             unit = 0;
-            sp = span_of(a, b, table, lengths);
+            sp = span_of(a, lengths[b]);
             continue;
         }
         const int take = min(left, sp.blocks - at_block);
+        if (!has_page(a, b, sp.pos, table)) {
+            left -= take;
+            at_block = 0;
+            ++unit;
+            continue;
+        }
         const int hk = unit / a.head_tiles, ht = unit - hk * a.head_tiles;
         const int* trow = table + static_cast<size_t>(b) * a.max_pages;
         const size_t new_row = static_cast<size_t>(b) * a.Hkv + hk;
@@ -448,12 +484,12 @@ __global__ __launch_bounds__(256) void join_kernel(DecodeArgs a, const int* __re
     __shared__ float sums[W - 1][D];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int b = blockIdx.x / a.Hq, hq = blockIdx.x - b * a.Hq;
-    const Span sp = span_of(a, b, table, lengths);
-    if (sp.pos < 0) return;
+    const Span sp = span_of(a, lengths[b]);
+    if (sp.blocks == 0 || !has_page(a, b, sp.pos, table)) return;
     const int per = a.Hkv * a.head_tiles, hk = hq / a.G, g = hq - hk * a.G;
-    const long long n = per * blocks_before(a, a.B, table, lengths, lane);
-    const long long lo = per * blocks_before(a, b, table, lengths, lane) +
-                         static_cast<long long>(hk * a.head_tiles + g / 16) * sp.blocks;
+    long long before;
+    const long long n = per * all_blocks(a, lengths, lane, b, before);
+    const long long lo = per * before + static_cast<long long>(hk * a.head_tiles + g / 16) * sp.blocks;
     const int used = shares_of(a, n), w0 = owner(lo, n, used), parts = owner(lo + sp.blocks - 1, n, used) - w0 + 1;
     if (parts == 1) return;  // written whole
     auto slot = [&](int s) { return (static_cast<size_t>(w0 + s) * 2 + (s == 0)) * a.heads + (g & 15); };
