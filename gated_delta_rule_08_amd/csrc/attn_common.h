@@ -282,6 +282,30 @@ __device__ __forceinline__ void copy_rows(uint32_t tile_a, const T* a, uint32_t 
         copy_1k(tile_b + jj * 1024, b, off);
     }
 }
+// Copies ROWS rows, `stride` elements apart, of which `left` (at least 1) exist
+// (the last one stands in for the rest).  Where a wave's copies are a multiple
+// of 16 rows apart their swizzle is the same, and away from the end they share
+// one lane offset.
+template <typename T, int D, int ROWS, int WAVES>
+__device__ __forceinline__ void copy_keys(uint32_t tile, const T* base, size_t stride, int left, int wave, int lane) {
+    using L = Tile<T, D>;
+    constexpr int kPer = 1024 / L::kRow, kCopies = ROWS / kPer / WAVES, kApart = kPer * WAVES;
+    static_assert(1024 % L::kRow == 0 && ROWS % kApart == 0, "whole rows, the same number for every wave");
+    const int r0 = wave * kPer + lane / L::kUnits, x = lane % L::kUnits;
+    const uint32_t bytes = static_cast<uint32_t>(stride) * sizeof(T);
+    if (kApart % 16 == 0 && left >= ROWS) {
+        const uint32_t off = r0 * bytes + ((x ^ L::swz(r0)) << 4);
+#pragma unroll
+        for (int j = 0; j < kCopies; ++j) copy_1k(tile + (wave + j * WAVES) * 1024, base + j * kApart * stride, off);
+    } else {
+#pragma unroll
+        for (int j = 0; j < kCopies; ++j) {
+            const int r = r0 + j * kApart;
+            copy_1k(tile + (wave + j * WAVES) * 1024, base, min(r, left - 1) * bytes + ((x ^ L::swz(r)) << 4));
+        }
+    }
+}
+
 // Keys and queries of one sequence.  Query i is at position i + off; key j is
 // visible to position p if j <= p and (window == 0 or j > p - window or j <
 // sinks).  window is at most the number of keys, so p + window cannot wrap.

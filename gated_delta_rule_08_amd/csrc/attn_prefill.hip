@@ -150,8 +150,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prefill_kernel(PrefillArgs a, 
     auto fetch = [&](int i) {
         const uint32_t buf = lds_addr(smem) + (i & (C::kBufs - 1)) * 2 * C::kTileBytes;
         const int j0 = tile_of(i) * BN;
-        copy_rows<T, D, BN, kWaves>(buf, kbase + j0 * kstride, buf + C::kTileBytes, vbase + j0 * kstride, wave, lane,
-                                    [&](int r) { return min(r, Tk - 1 - j0) * a.Hkv * D; });
+        copy_keys<T, D, BN, kWaves>(buf, kbase + j0 * kstride, kstride, Tk - j0, wave, lane);
+        copy_keys<T, D, BN, kWaves>(buf + C::kTileBytes, vbase + j0 * kstride, kstride, Tk - j0, wave, lane);
     };
     if (C::kBufs == 2 && n > 0) fetch(0);
 
@@ -211,15 +211,17 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prefill_kernel(PrefillArgs a, 
 #pragma unroll
             for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[u][r]);
         mx = fmaxf(m, fmaxf(mx, other_half(mx)));
-        // a row that has seen no key yet keeps m = -inf and weights 0
-        const float mc = mx == -INFINITY ? 0.f : mx * c;
-        if (__any(mx > m)) {
-            const float alpha = m == -INFINITY ? 0.f : ex2(m * c - mc);
+        // The sums are rescaled only where a row's maximum has grown by more than
+        // a factor 2^8 since: weights then reach 2^8, which costs no precision
+        // (every rounding is relative), and most tiles leave the sums alone.
+        if (__any((mx - m) * c > 8.f)) {
+            const float alpha = m == -INFINITY ? 0.f : ex2((m - mx) * c);
             l *= alpha;
 #pragma unroll
             for (int t = 0; t < DT; ++t) acc[t] *= alpha;
             m = mx;
         }
+        const float mc = m == -INFINITY ? 0.f : m * c;  // a row that has seen no key: weights 0
         frag_t<T> pf[2 * NS];
         float ls = 0.f;
 #pragma unroll
