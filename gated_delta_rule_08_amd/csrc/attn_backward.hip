@@ -38,7 +38,7 @@ struct BwdArgs {
     int rows, pitch;          // rows of a (sequence, key head); pitch of the row statistics
     int key_blocks, row_tiles;
     bool split;               // dq: 32 rows per workgroup, a quarter of the keys per wave
-    int slices;               // parts of every key's rows (small problems; else 1)
+    int slices, slice_rows;   // rows of a key block in one workgroup, and how many that makes (at most)
     int sink_tiles, segs;     // 32-key tiles that hold sinks, segments of each (at most; 0 with slices > 1)
     int seg_rows;
     int part_tiles, slots;    // key tiles whose gradients come in parts, parts of each (at most)
@@ -48,11 +48,12 @@ struct BwdArgs {
 
 // Rows (query * G + head) that see keys [j0, j1] through the window or, with
 // no window, causally: [lo, hi).
-__device__ __forceinline__ void rows_of(const BwdArgs& a, int j0, int j1, int& lo, int& hi) {
+__host__ __device__ __forceinline__ void rows_of(const BwdArgs& a, int j0, int j1, int& lo, int& hi) {
     const int off = a.Tk - a.Tq;
-    lo = max(0, j0 - off) * a.G.d;
-    const int last = a.window ? min(a.Tq - 1, j1 + a.window - 1 - off) : a.Tq - 1;
-    hi = max(lo, (last + 1) * a.G.d);
+    lo = (j0 > off ? j0 - off : 0) * a.G.d;
+    int last = a.Tq - 1;
+    if (a.window && j1 + a.window - 1 - off < last) last = j1 + a.window - 1 - off;
+    hi = (last + 1) * a.G.d > lo ? (last + 1) * a.G.d : lo;
     if (a.slices > 1 && a.window && j0 < a.sinks) hi = a.rows;  // no segments: the sinks' rows are sliced with the rest
 }
 
@@ -114,15 +115,8 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && WAVES == 4 ? 2 : 1) v
     extern __shared__ unsigned char smem[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h2 = lane >> 5;
     const int per = kSeg ? a.sink_tiles * a.segs : a.key_blocks * a.slices;
-    const int heads = a.B * a.Hkv;
-    int bid = blockIdx.x, head, x;
-    if (heads % 8 == 0) {  // one head's blocks on one XCD
-        head = (bid / 8 / per) * 8 + (bid & 7);
-        x = (bid / 8) % per;
-    } else {
-        head = bid % heads;
-        x = bid / heads;
-    }
+    int head, x;
+    place(blockIdx.x, a.B * a.Hkv, per, head, x);  // the first keys are seen by the most rows
     const int b = head / a.Hkv, hk = head - b * a.Hkv;
     const int cuts = kSeg ? a.segs : a.slices, y = x / cuts, cut = x - y * cuts;
     const int tile = kSeg ? y : y * WAVES + wave;  // 32-key tile of this wave
@@ -136,10 +130,12 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && WAVES == 4 ? 2 : 1) v
     if (kSeg) {  // past what the main workgroup takes
         lo = hi + cut * a.seg_rows;
         hi = min(a.rows, lo + a.seg_rows);
-    } else if (a.slices > 1) {
-        const int len = ((hi - lo + a.slices - 1) / a.slices + 31) / 32 * 32;
-        lo = min(hi, lo + cut * len);
-        hi = min(hi, lo + len);
+    }
+    const bool parts = kSeg || hi - lo > a.slice_rows;  // the keys' rows are not all here
+    if (!kSeg) {
+        lo += cut * a.slice_rows;
+        hi = min(hi, lo + a.slice_rows);
+        if (cut > 0 && lo >= hi) return;
     }
     if (kSeg && lo >= hi) return;
     const bool wave_live = j0 < a.Tk;
@@ -255,7 +251,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && WAVES == 4 ? 2 : 1) v
 
     // the keys' gradients, or this part of them
     float* part = nullptr;
-    if (tile < a.part_tiles)
+    if (parts || tile < a.sink_tiles)
         part = a.part + ((static_cast<size_t>(head) * a.part_tiles + tile) * a.slots + (kSeg ? 1 + cut : cut)) * 64 * D;
     bool bad = false;
 #pragma unroll
@@ -286,6 +282,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && WAVES == 4 ? 2 : 1) v
             const int ch = 32 * t + row32(r, h2);
             const f32x16 g = dk[t] * a.scale;
             if (part) {
+                if (kSeg && key >= a.sinks) continue;  // not read by the join
                 store4<float>(part + (lane & 31) * D + ch, g[r], g[r + 1], g[r + 2], g[r + 3]);
                 store4<float>(part + (32 + (lane & 31)) * D + ch, dv[t][r], dv[t][r + 1], dv[t][r + 2], dv[t][r + 3]);
             } else if (key < a.Tk) {
@@ -295,21 +292,34 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && WAVES == 4 ? 2 : 1) v
         }
 }
 
-// Adds the parts of one key tile in order, four elements a thread.
+// Adds the parts of one key tile: 32 groups of four elements a workgroup, eight
+// threads to each, every thread its parts in order and then their sums in order.
 template <typename T, int D>
 __global__ __launch_bounds__(256) void join_kernel(BwdArgs a, T* __restrict__ gk, T* __restrict__ gv) {
+    __shared__ f32x4 sums[8][32];
     const int head = blockIdx.x / a.part_tiles, tile = blockIdx.x % a.part_tiles;
     const int b = head / a.Hkv, hk = head - b * a.Hkv;
     const int m0 = 32 * tile / kKeys * kKeys;
-    int lo, end, parts = a.slices;
+    int lo, end, parts = 1;
     rows_of(a, m0, min(m0 + kKeys, a.Tk) - 1, lo, end);
-    if (a.segs && a.rows > end) parts += (a.rows - end - 1) / a.seg_rows + 1;
+    if (a.slices > 1) {
+        if (end - lo <= a.slice_rows) return;  // written whole
+        parts = (end - lo - 1) / a.slice_rows + 1;
+    }
+    const int segs = a.segs && a.rows > end ? (a.rows - end - 1) / a.seg_rows + 1 : 0;
     const float* part = a.part + (static_cast<size_t>(head) * a.part_tiles + tile) * a.slots * 64 * D;
-    const int i = blockIdx.y * 256 + threadIdx.x, row = i / (D / 4), ch = 4 * (i % (D / 4)), key = 32 * tile + (row & 31);
-    if (key >= a.Tk) return;
+    const int x = threadIdx.x & 31, first = threadIdx.x >> 5;
+    const int i = blockIdx.y * 32 + x, row = i / (D / 4), ch = 4 * (i % (D / 4)), key = 32 * tile + (row & 31);
+    if (key < a.sinks) parts += segs;  // the others have none
     f32x4 s = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll 8
-    for (int p = 0; p < parts; ++p) s += *reinterpret_cast<const f32x4*>(part + static_cast<size_t>(p) * 64 * D + 4 * i);
+    for (int p = first; p < parts; p += 8)
+        s += *reinterpret_cast<const f32x4*>(part + static_cast<size_t>(p) * 64 * D + 4 * i);
+    sums[first][x] = s;
+    __syncthreads();
+    if (first > 0 || key >= a.Tk) return;
+#pragma unroll
+    for (int p = 1; p < 8; ++p) s += sums[p][x];
     T* dst = (row >= 32 ? gv : gk) + ((static_cast<size_t>(b) * a.Tk + key) * a.Hkv + hk) * D + ch;
     store4<T>(dst, s[0], s[1], s[2], s[3]);
 }
@@ -360,15 +370,9 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(T) == 2 ? 2 : 1) void dq_kernel
     constexpr int BN = C::BN, KS = D / 16, DT = D / 32, kGroup = SPLIT ? 32 : kRows;
     extern __shared__ unsigned char smem[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h2 = lane >> 5;
-    const int heads = a.B * a.Hkv, bid = blockIdx.x;
     int head, tile;
-    if (heads % 8 == 0) {
-        head = (bid / 8 / a.row_tiles) * 8 + (bid & 7);
-        tile = a.row_tiles - 1 - (bid / 8) % a.row_tiles;
-    } else {
-        head = bid % heads;
-        tile = a.row_tiles - 1 - bid / heads;
-    }
+    place(blockIdx.x, a.B * a.Hkv, a.row_tiles, head, tile);
+    tile = a.row_tiles - 1 - tile;  // the last rows see the most keys
     const int b = head / a.Hkv, hk = head - b * a.Hkv;
     const int off = a.Tk - a.Tq, row0 = tile * kGroup, wrow = row0 + (SPLIT ? 0 : 32 * wave);
     const Mask mask{a.window, a.sinks};
@@ -442,10 +446,12 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(T) == 2 ? 2 : 1) void dq_kernel
                 if (!mask.sees(pos, j0 + row32(r, h2))) dp[r] = 0.f;
         }
         const frag_t<T> df[2] = {pack_regs<T>(dp, 0), pack_regs<T>(dp, 1)};
+        if (D == 128) __builtin_amdgcn_s_setprio(1);  // as in the forward (full T=4096: 1.0% of the training step)
 #pragma unroll
         for (int t = 0; t < DT; ++t)
 #pragma unroll
             for (int u = 0; u < 2; ++u) dq[t] = mma32(ColRead<T, D>::get(smem, cb, t, u), df[u], dq[t]);
+        if (D == 128) __builtin_amdgcn_s_setprio(0);
     }
     if constexpr (SPLIT) {  // the waves' sums, added in wave order by the first
         static_assert(C::kLds >= (kWaves - 1) * 64 * DT * 64, "LDS holds the other waves' sums");
@@ -503,14 +509,39 @@ BwdArgs make_args(int B, int Tq, int Tk, int Hq, int Hkv, int window, int sinks,
     const long long heads = static_cast<long long>(B) * Hkv, groups = heads * a.key_blocks;
     a.split = heads * ((a.rows + kRows - 1) / kRows) < 256;  // fewer workgroups than CUs
     a.row_tiles = a.split ? (a.rows + 31) / 32 : (a.rows + kRows - 1) / kRows;
-    // Below one workgroup per CU the rows are sliced, to two per CU and no
-    // slice under 64 rows.
+    // The rows of a key block are sliced where the blocks alone would leave CUs
+    // idle: below one workgroup per CU, or below two where the causal mask makes
+    // the first block's list much longer than the others'.  Slices of a 384th of
+    // all rows, 64 at least (training step T=4096, 32 query on 8 key heads: 1023
+    // us unsliced, 748 with a 256th, 708, 724 with a 768th, 765 with a 1024th).
     a.slices = 1;
-    if (groups > 0 && groups < 256) {
-        const long long want = (512 + groups - 1) / groups, most = (a.rows + 63) / 64;
-        a.slices = static_cast<int>(want < most ? want : most > 0 ? most : 1);
+    a.slice_rows = a.rows > 0 ? a.rows : 1;
+    if (groups > 0 && groups < 512 && a.rows > 0) {
+        long long total = 0, longest = 0;
+        for (int j = 0; j < a.key_blocks; ++j) {
+            int lo, hi;
+            rows_of(a, j * kKeys, (j + 1) * kKeys < Tk ? (j + 1) * kKeys - 1 : Tk - 1, lo, hi);
+            total += hi - lo;
+            if (hi - lo > longest) longest = hi - lo;
+        }
+        if (groups < 256 || 2 * longest * a.key_blocks > 3 * total) {
+            const long long even = (total * heads / 384 + 31) / 32 * 32;
+            a.slice_rows = static_cast<int>(even < 64 ? 64 : even < a.rows ? even : a.rows);
+            a.slices = 2;  // several: the sinks' rows are sliced with the rest
+            longest = 0;
+            for (int j = 0; j < a.key_blocks; ++j) {
+                int lo, hi;
+                rows_of(a, j * kKeys, (j + 1) * kKeys < Tk ? (j + 1) * kKeys - 1 : Tk - 1, lo, hi);
+                if (hi - lo > longest) longest = hi - lo;
+            }
+            a.slices = static_cast<int>((longest + a.slice_rows - 1) / a.slice_rows);
+            if (a.slices <= 1) {
+                a.slices = 1;
+                a.slice_rows = a.rows;
+            }
+        }
     }
-    // Sink segments: about one wave per SIMD, no segment under 128 rows.
+    // Sink segments: one wave per SIMD, no segment under 128 rows.
     if (a.slices == 1 && window && Tq > 0) a.sink_tiles = (sinks + 31) / 32;
     if (a.sink_tiles) {
         const long long even = heads * a.sink_tiles * a.rows / 1024;
@@ -536,7 +567,7 @@ hipError_t launch(const BwdArgs& a, const void* q_, const void* k_, const void* 
     const unsigned long long kv_blocks = heads * a.key_blocks * a.slices, q_blocks = heads * a.row_tiles;
     const unsigned long long seg_blocks = heads * a.sink_tiles * a.segs, join_blocks = heads * a.part_tiles;
     if (!grid_fits(kv_blocks, 64 * kWaves) || !grid_fits(q_blocks, 64 * kWaves) ||
-        !grid_fits(seg_blocks, 64) || !grid_fits(join_blocks * (D / 16), 256))
+        !grid_fits(seg_blocks, 64) || !grid_fits(join_blocks * (D / 2), 256))
         return hipErrorInvalidConfiguration;
     using CK = DkdvCfg<T, D, kWaves>;
     auto* dq = a.split ? dq_kernel<T, D, true> : dq_kernel<T, D, false>;
@@ -555,7 +586,7 @@ hipError_t launch(const BwdArgs& a, const void* q_, const void* k_, const void* 
         hipLaunchKernelGGL((dkdv_kernel<T, D, 1>), dim3(static_cast<unsigned>(seg_blocks)), dim3(64), CK::kLds, st, a, q, k,
                            v, go, static_cast<T*>(gk), static_cast<T*>(gv));
     if (join_blocks)
-        hipLaunchKernelGGL((join_kernel<T, D>), dim3(static_cast<unsigned>(join_blocks), 64 * D / 4 / 256), dim3(256), 0,
+        hipLaunchKernelGGL((join_kernel<T, D>), dim3(static_cast<unsigned>(join_blocks), 64 * D / 4 / 32), dim3(256), 0,
                            st, a, static_cast<T*>(gk), static_cast<T*>(gv));
     return hipGetLastError();
 }

@@ -306,6 +306,29 @@ __device__ __forceinline__ void copy_keys(uint32_t tile, const T* base, size_t s
     }
 }
 
+// Which of `tiles` pieces of work (rank 0 the longest) of which head workgroup
+// bid takes.  Workgroups go round the 8 XCDs: a head's pieces stay on one, whose
+// L2 then holds what they share, the longest first.  Where all fit at once, two
+// to a CU (32 CUs to an XCD, filled in turn), the second round goes backwards,
+// so that a long piece shares its CU with a short one.
+__device__ __forceinline__ void place(int bid, int heads, int tiles, int& head, int& rank) {
+    if (heads % 8 == 0) {
+        const int y = bid >> 3, here = heads >> 3, all = here * tiles;
+        if (all > 32 && all <= 64) {
+            const int r = y < 32 ? y : all - 1 - (y - 32);
+            rank = r / here;
+            head = (r - rank * here) * 8 + (bid & 7);
+        } else {
+            head = (y / tiles) * 8 + (bid & 7);
+            rank = y % tiles;
+        }
+    } else {
+        const int all = heads * tiles, r = all > 256 && all <= 512 && bid >= 256 ? all - 1 - (bid - 256) : bid;
+        head = r % heads;
+        rank = r / heads;
+    }
+}
+
 // Keys and queries of one sequence.  Query i is at position i + off; key j is
 // visible to position p if j <= p and (window == 0 or j > p - window or j <
 // sinks).  window is at most the number of keys, so p + window cannot wrap.

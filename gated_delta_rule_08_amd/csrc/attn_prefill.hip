@@ -95,18 +95,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prefill_kernel(PrefillArgs a, 
     extern __shared__ unsigned char smem[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int h2 = lane >> 5;
-    // Workgroups go round the 8 XCDs: consecutive row tiles of a key head stay
-    // on one XCD, whose L2 then holds that head's keys and values.  The rows
-    // with the most visible keys (the last) start first.
-    const int heads = a.B * a.Hkv, bid = blockIdx.x;
     int head, tile;
-    if (heads % 8 == 0) {
-        head = (bid / 8 / a.tiles) * 8 + (bid & 7);
-        tile = a.tiles - 1 - (bid / 8) % a.tiles;
-    } else {
-        head = bid % heads;
-        tile = a.tiles - 1 - bid / heads;
-    }
+    place(blockIdx.x, a.B * a.Hkv, a.tiles, head, tile);
+    tile = a.tiles - 1 - tile;  // the last rows see the most keys
     const int b = head / a.Hkv, hk = head - b * a.Hkv;
     int Tq = a.Tq, Tk = a.Tk;
     size_t q0 = static_cast<size_t>(b) * a.Tq, k0 = static_cast<size_t>(b) * a.Tk;
@@ -190,6 +181,11 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prefill_kernel(PrefillArgs a, 
         const int j0 = tile_of(i) * BN + sub;
         if (!wave_live || mask.none(wp0, wp1, j0, j0 + 32 * NS - 1)) continue;
 
+        // The other wave of the SIMD is in another phase: a wave in its products
+        // goes first, the exponentials of the other fill the gaps.  With d = 128
+        // only in the second product (T=8192: 520 us, both products 541, neither
+        // 540), with d = 64 in both (B=2 T=4096: 86 us, second 93, neither 88).
+        if (D == 64) __builtin_amdgcn_s_setprio(1);
         f32x16 s[NS];
 #pragma unroll
         for (int u = 0; u < NS; ++u) {
@@ -198,6 +194,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prefill_kernel(PrefillArgs a, 
             for (int e = 0; e < KS; ++e)
                 s[u] = mma32(RowRead<T, D>::get(smem, kb, e, 32 * u * Tile<T, D>::kRow), qf[e], s[u]);
         }
+        if (D == 64) __builtin_amdgcn_s_setprio(0);
         if (!mask.all(wp0, wp1, j0, j0 + 32 * NS - 1)) {
 #pragma unroll
             for (int u = 0; u < NS; ++u)
@@ -235,10 +232,12 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prefill_kernel(PrefillArgs a, 
             for (int x = 0; x < 2; ++x) pf[2 * u + x] = pack_regs<T>(s[u], x);
         }
         l += ls;
+        __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int t = 0; t < DT; ++t)
 #pragma unroll
             for (int x = 0; x < 2 * NS; ++x) acc[t] = mma32(ColRead<T, D>::get(smem, vb, t, x), pf[x], acc[t]);
+        __builtin_amdgcn_s_setprio(0);
     }
 
     l += other_half(l);
