@@ -97,7 +97,7 @@ size_t gdr_attn_backward_workspace_bytes(int dtype, int B, int Tq, int Tk, int H
         !sizes_ok(B, Tq, Hq, d) || !sizes_ok(B, Tk, Hkv, d) || B == 0 || Hq == 0 || Tq == 0)
         return 0;
     window = clamp_window(window, Tk);
-    return gdr::attn_backward_workspace_floats(B, Tq, Tk, Hq, Hkv, d, window, clamp_sinks(sinks, window, Tk)) *
+    return gdr::attn_backward_workspace_floats(dtype, B, Tq, Tk, Hq, Hkv, d, window, clamp_sinks(sinks, window, Tk)) *
            sizeof(float);
 }
 

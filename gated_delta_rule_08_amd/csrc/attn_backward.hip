@@ -122,7 +122,6 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && WAVES == 4 ? 2 : 1) v
     const int tile = kSeg ? y : y * WAVES + wave;  // 32-key tile of this wave
     const int j0 = 32 * tile, j1 = min(j0 + 31, a.Tk - 1), key = j0 + (lane & 31);
     const int off = a.Tk - a.Tq;
-    const Mask mask{a.window, a.sinks};
 
     int lo, hi;
     const int m0 = kSeg ? j0 / kKeys * kKeys : y * kKeys;  // the keys of a main workgroup
@@ -139,10 +138,6 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && WAVES == 4 ? 2 : 1) v
     }
     if (kSeg && lo >= hi) return;
     const bool wave_live = j0 < a.Tk;
-    // this lane's key is visible to rows [key_lo, key_hi) of [lo, hi)
-    const int key_lo = min(a.Tq, max(0, key - off)) * a.G.d;
-    const int key_hi = a.window == 0 || key < a.sinks ? hi : min(hi, min(a.Tq, max(0, key + a.window - off)) * a.G.d);
-
     const size_t kstride = static_cast<size_t>(a.Hkv) * D;
     const size_t k0 = (static_cast<size_t>(b) * a.Tk * a.Hkv + hk) * D;
     frag_t<T> kf[KS], vf[KS];
@@ -161,19 +156,41 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && WAVES == 4 ? 2 : 1) v
     const float* stat = a.stats + static_cast<size_t>(head) * 2 * a.pitch;
     const size_t q0 = (static_cast<size_t>(b) * a.Tq * a.Hq + static_cast<size_t>(hk) * a.G.d) * D;
 
-    auto fetch = [&](int i) {
+    // Where the group size divides 32 the rows of a step lie the same way from
+    // its first one, and steps the same way apart.
+    const bool even = 32 % a.G.d == 0;
+    const size_t qstep = static_cast<size_t>(BM / a.G.d) * a.Hq * D;
+    const TileCopy<T, D, BM, WAVES> copy(wave, lane, [&](int r) {
+        const int y = a.G(r);
+        return (y * a.Hq + (r - y * a.G.d)) * D * static_cast<int>(sizeof(T));
+    });
+    const T *qp = q + q0 + static_cast<size_t>(a.G(lo)) * a.Hq * D, *gp = go + q0 + static_cast<size_t>(a.G(lo)) * a.Hq * D;
+    auto fetch = [&](int i) {  // steps in turn
         const uint32_t buf = lds_addr(smem) + (i & 1) * C::kBuf;
-        const int r0 = lo + BM * i, i0 = a.G(r0);
-        const size_t base = q0 + static_cast<size_t>(i0) * a.Hq * D;
-        copy_rows<T, D, BM, WAVES>(buf, q + base, buf + C::kTile, go + base, wave, lane, [&](int r) {
-            const int row = min(r0 + r, a.rows - 1), y = a.G(row);
-            return ((y - i0) * a.Hq + (row - y * a.G.d)) * D;
-        });
-        if (wave < NM) {  // lanes 0..31: lse2, 32..63: delta
-            const int r = min(32 * wave + (lane & 31), a.rows - 1 - r0);
-            copy_words(lds_addr(smem) + C::kStat + (i & 1) * C::kStatBuf + 256 * wave, stat + r0, 4u * (h2 * a.pitch + r));
+        const uint32_t st = lds_addr(smem) + C::kStat + (i & 1) * C::kStatBuf + 256 * wave;
+        const int r0 = lo + BM * i;
+        if (even && r0 + BM <= a.rows) {
+            copy.run(buf, qp);
+            copy.run(buf + C::kTile, gp);
+            if (wave < NM) copy_words(st, stat + r0, (again(lane) < 32 ? 0u : 4u * a.pitch) + 4u * (32 * wave + (again(lane) & 31)));  // lanes 0..31: lse2, 32..63: delta
+        } else {
+            auto row = [&](int r) {
+                r = min(r0 + r, a.rows - 1);
+                const int y = a.G(r);
+                return q0 + (static_cast<size_t>(y) * a.Hq + (r - y * a.G.d)) * D;
+            };
+            copy.gather(buf, [&](int r) { return q + row(r); });
+            copy.gather(buf + C::kTile, [&](int r) { return go + row(r); });
+            if (wave < NM) copy_words(st, stat + r0, 4u * (h2 * a.pitch + min(32 * wave + (lane & 31), a.rows - 1 - r0)));
         }
+        qp += qstep;
+        gp += qstep;
     };
+    // rows [whole_lo, whole_hi) see all of the wave's keys, rows outside [any_lo, any_hi) none
+    auto rows_to = [&](int j) { return min(a.Tq, max(0, j - off)) * a.G.d; };
+    const int any_lo = wave_live ? rows_to(j0) : hi, whole_lo = min(a.Tq + 1, max(0, j0 + 31 - off)) * a.G.d;
+    const int any_hi = a.window == 0 || j0 < a.sinks ? hi : min(hi, rows_to(j1 + a.window));
+    const int whole_hi = a.window == 0 || j0 + 31 < a.sinks ? hi : min(hi, rows_to(j0 + a.window));
     const int n = (hi - lo + BM - 1) / BM;
     const int rb0 = RowRead<T, D>::base(lane & 31, h2), cb0 = ColRead<T, D>::base(lane);
     if (n > 0) fetch(0);
@@ -183,10 +200,9 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && WAVES == 4 ? 2 : 1) v
         if (i + 1 < n) fetch(i + 1);
         const int buf = (i & 1) * C::kBuf, rb = rb0 + buf, cb = cb0 + buf;
         const int r0 = lo + BM * i;
-        const int p0 = a.G(r0) + off, p1 = a.G(min(r0 + BM - 1, hi - 1)) + off;
-        if (!wave_live || mask.none(p0, p1, j0, j1)) continue;
+        if (r0 + BM <= any_lo || r0 >= any_hi) continue;
         const float* st = reinterpret_cast<const float*>(smem + C::kStat + (i & 1) * C::kStatBuf) + 4 * h2;
-        const bool whole = mask.all(p0, p1, j0, j0 + 31) && r0 + BM <= hi;
+        const bool whole = r0 >= whole_lo && r0 + BM <= whole_hi;
 #pragma unroll
         for (int w = 0; w < NM; ++w) {
             // P: registers of S as they stand are the B operand of dV
@@ -202,10 +218,12 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && WAVES == 4 ? 2 : 1) v
 #pragma unroll
                 for (int y = 0; y < 4; ++y) s[r + y] = ex2(fmaf(s[r + y], c, -ls[y]));
             }
-            if (!whole) {
+            if (!whole) {  // the lane's key is visible to rows [key_lo, key_hi)
+                const int mine = again(lane), at = j0 + (mine & 31);
+                const int key_lo = rows_to(at), key_hi = a.window == 0 || at < a.sinks ? hi : min(hi, rows_to(at + a.window));
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
-                    const int row = r0 + 32 * w + row32(r, h2);
+                    const int row = r0 + 32 * w + row32(r, mine >> 5);
                     if (row < key_lo || row >= key_hi) s[r] = 0.f;
                 }
             }
@@ -383,21 +401,29 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(T) == 2 ? 2 : 1) void dq_kernel
     const int wp0 = __builtin_amdgcn_readfirstlane(a.G(wr0) + off);
     const int wp1 = __builtin_amdgcn_readfirstlane(a.G(wr1) + off);
     const size_t qrow = (static_cast<size_t>(b) * a.Tq + qi) * a.Hq + static_cast<size_t>(hk) * a.G.d + (row - qi * a.G.d);
-    const int p0 = a.G(row0) + off, p1 = a.G(min(row0 + kGroup - 1, a.rows - 1)) + off;
-    const int w_lo = a.window ? max(0, p0 - a.window + 1) : 0;
-    const int t_lo = w_lo / BN, t_hi = p1 < 0 ? -1 : p1 / BN;
-    const int t_sink = a.window ? min((a.sinks + BN - 1) / BN, t_lo) : 0;
-    const int n = t_hi < t_lo ? 0 : t_sink + t_hi - t_lo + 1;
+    const KeyList keys(a.window, a.sinks, a.G(row0) + off, a.G(min(row0 + kGroup - 1, a.rows - 1)) + off);
+    const int n = (keys.count + BN - 1) / BN;
 
     const size_t kstride = static_cast<size_t>(a.Hkv) * D;
     const T* kbase = k + (static_cast<size_t>(b) * a.Tk * a.Hkv + hk) * D;
     const T* vbase = v + (static_cast<size_t>(b) * a.Tk * a.Hkv + hk) * D;
-    auto tile_of = [&](int i) { return i < t_sink ? i : i - t_sink + t_lo; };
-    auto fetch = [&](int i) {
+    const int sub = SPLIT ? 32 * wave : 0;  // this wave's keys of a step
+    const TileRange range = TileRange::of<BN, 32>(keys, a.window, a.Tk, sub, wp0, wp1);
+    const int end_tile = wave_live ? range.end : 0;
+    const TileCopy<T, D, BN, kWaves> copy(wave, lane, [&](int r) { return r * static_cast<int>(kstride * sizeof(T)); });
+    const T *kp = kbase + keys.jump * kstride, *vp = vbase + keys.jump * kstride;  // the next tile's first rows
+    auto fetch = [&](int i) {  // tiles in turn
         const uint32_t buf = lds_addr(smem) + (i & (C::kBufs - 1)) * 2 * C::kTile;
-        const int j0 = tile_of(i) * BN;
-        copy_rows<T, D, BN, kWaves>(buf, kbase + j0 * kstride, buf + C::kTile, vbase + j0 * kstride, wave, lane,
-                                    [&](int r) { return min(r, a.Tk - 1 - j0) * a.Hkv * D; });
+        if (i >= range.full_lo && i < range.full_hi) {
+            copy.run(buf, kp);
+            copy.run(buf + C::kTile, vp);
+        } else {
+            auto key = [&](int r) { return static_cast<size_t>(min(keys.key(i * BN + r), a.Tk - 1)) * kstride; };
+            copy.gather(buf, [&](int r) { return kbase + key(r); });
+            copy.gather(buf + C::kTile, [&](int r) { return vbase + key(r); });
+        }
+        kp += BN * kstride;
+        vp += BN * kstride;
     };
     if (C::kBufs == 2 && n > 0) fetch(0);
 
@@ -419,7 +445,6 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(T) == 2 ? 2 : 1) void dq_kernel
     f32x16 dq[DT];
 #pragma unroll
     for (int t = 0; t < DT; ++t) dq[t] = zero16();
-    const int sub = SPLIT ? 32 * wave : 0;  // this wave's keys of a step
     const int rb0 = RowRead<T, D>::base(lane & 31, h2) + sub * Tile<T, D>::kRow;
     const int cb0 = ColRead<T, D>::base(lane) + sub * Tile<T, D>::kRow;
 #pragma unroll 1
@@ -431,8 +456,7 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(T) == 2 ? 2 : 1) void dq_kernel
         tile_barrier();
         if (C::kBufs == 2 && i + 1 < n) fetch(i + 1);
         const int buf = (i & (C::kBufs - 1)) * 2 * C::kTile, rb = rb0 + buf, cb = cb0 + buf;
-        const int j0 = tile_of(i) * BN + sub;
-        if (!wave_live || mask.none(wp0, wp1, j0, j0 + 31)) continue;
+        if (i >= end_tile) continue;
         f32x16 s = zero16(), dp = zero16();
 #pragma unroll
         for (int e = 0; e < KS; ++e) s = mma32(RowRead<T, D>::get(smem, rb, e, 0), qf[e], s);
@@ -440,10 +464,11 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(T) == 2 ? 2 : 1) void dq_kernel
         for (int e = 0; e < KS; ++e) dp = mma32(RowRead<T, D>::get(smem, rb, e, C::kTile), gf[e], dp);
 #pragma unroll
         for (int r = 0; r < 16; ++r) dp[r] = ex2(fmaf(s[r], c, -lse2)) * (dp[r] - delta);
-        if (!mask.all(wp0, wp1, j0, j0 + 31)) {
+        if (i < range.whole_lo || i >= range.whole_hi) {
+            const int x0 = i * BN + sub;
 #pragma unroll
             for (int r = 0; r < 16; ++r)
-                if (!mask.sees(pos, j0 + row32(r, h2))) dp[r] = 0.f;
+                if (!mask.sees(pos, keys.key(x0 + row32(r, h2)))) dp[r] = 0.f;
         }
         const frag_t<T> df[2] = {pack_regs<T>(dp, 0), pack_regs<T>(dp, 1)};
         if (D == 128) __builtin_amdgcn_s_setprio(1);  // as in the forward (full T=4096: 1.0% of the training step)
@@ -492,7 +517,7 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(T) == 2 ? 2 : 1) void dq_kernel
     }
 }
 
-BwdArgs make_args(int B, int Tq, int Tk, int Hq, int Hkv, int window, int sinks, float scale) {
+BwdArgs make_args(bool f32, int B, int Tq, int Tk, int Hq, int Hkv, int window, int sinks, float scale) {
     BwdArgs a{};
     a.B = B;
     a.Tq = Tq;
@@ -507,7 +532,7 @@ BwdArgs make_args(int B, int Tq, int Tk, int Hq, int Hkv, int window, int sinks,
     a.pitch = (a.rows + 3) / 4 * 4;
     a.key_blocks = (Tk + kKeys - 1) / kKeys;
     const long long heads = static_cast<long long>(B) * Hkv, groups = heads * a.key_blocks;
-    a.split = heads * ((a.rows + kRows - 1) / kRows) < 256;  // fewer workgroups than CUs
+    a.split = heads * ((a.rows + kRows - 1) / kRows) < (f32 ? 257 : 192);  // as the forward does
     a.row_tiles = a.split ? (a.rows + 31) / 32 : (a.rows + kRows - 1) / kRows;
     // The rows of a key block are sliced where the blocks alone would leave CUs
     // idle: below one workgroup per CU, or below two where the causal mask makes
@@ -594,8 +619,8 @@ hipError_t launch(const BwdArgs& a, const void* q_, const void* k_, const void* 
 }  // namespace
 }  // namespace attn
 
-size_t attn_backward_workspace_floats(int B, int Tq, int Tk, int Hq, int Hkv, int d, int window, int sinks) {
-    const attn::BwdArgs a = attn::make_args(B, Tq, Tk, Hq, Hkv, window, sinks, 1.f);
+size_t attn_backward_workspace_floats(int dtype, int B, int Tq, int Tk, int Hq, int Hkv, int d, int window, int sinks) {
+    const attn::BwdArgs a = attn::make_args(dtype == GDR_DTYPE_F32, B, Tq, Tk, Hq, Hkv, window, sinks, 1.f);
     const size_t heads = static_cast<size_t>(B) * Hkv;
     return heads * (2 * static_cast<size_t>(a.pitch) + static_cast<size_t>(a.part_tiles) * a.slots * 64 * d);
 }
@@ -604,7 +629,7 @@ hipError_t launch_attn_backward(int dtype, int B, int Tq, int Tk, int Hq, int Hk
                                 float scale, const void* q, const void* k, const void* v, const void* o,
                                 const float* lse, const void* go, void* gq, void* gk, void* gv, float* ws,
                                 hipStream_t st) {
-    attn::BwdArgs a = attn::make_args(B, Tq, Tk, Hq, Hkv, window, sinks, scale);
+    attn::BwdArgs a = attn::make_args(dtype == GDR_DTYPE_F32, B, Tq, Tk, Hq, Hkv, window, sinks, scale);
     const size_t heads = static_cast<size_t>(B) * Hkv;
     a.stats = ws;
     a.part = ws + heads * 2 * a.pitch;

@@ -237,15 +237,14 @@ template <int D> struct ColRead<float, D> {
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {
     return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const void*)p));
 }
-__device__ __forceinline__ void copy_1k(uint32_t lds, const void* base, uint32_t off) {  // base is wave-uniform
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
-                 : "memory");
+__device__ __forceinline__ void copy_1k_from(uint32_t lds, const void* p) {  // an address per lane
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(p) : "memory");
 }
 __device__ __forceinline__ void copy_words(uint32_t lds, const void* base, uint32_t off) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(off), "s"(base)
                  : "memory");
 }
-__device__ __forceinline__ void stream_1k(uint32_t lds, const void* p) {  // an address per lane, not to be cached
+__device__ __forceinline__ void stream_1k(uint32_t lds, const void* p) {  // the same, not to be kept in the caches
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off nt" ::"s"(lds), "v"(p) : "memory");
 }
 __device__ __forceinline__ void gather_words(uint32_t lds, const void* p) {
@@ -262,49 +261,46 @@ __device__ __forceinline__ void tile_barrier() {
     asm volatile("" ::: "memory");
 }
 
-// Copies ROWS rows of two tensors of one layout into two LDS tiles, straight
-// from global memory: an instruction fills 1024 / row bytes rows, each lane
-// fetching the unit that belongs at its place.  offset(r) is the element
-// offset of row r of the tile from the (wave-uniform) bases.  The caller waits
-// for the copies (vmcnt) and passes a barrier before reading them.
-template <typename T, int D, int ROWS, int WAVES, typename OffsetFn>
-__device__ __forceinline__ void copy_rows(uint32_t tile_a, const T* a, uint32_t tile_b, const T* b, int wave, int lane,
-                                          OffsetFn offset) {
+// A wave's copies of a tile of ROWS rows: an instruction fills 1024 / row bytes
+// rows, each lane fetching the unit that belongs at its place.  The lanes'
+// offsets from the tile's first row are formed once; where a tile's rows exist
+// and follow one another, a step costs no address arithmetic but the base's.
+// The kernels wait for the copies (vmcnt) and pass a barrier before reading.
+template <typename T, int D, int ROWS, int WAVES> struct TileCopy {
     using L = Tile<T, D>;
-    constexpr int kPer = 1024 / L::kRow, kInstr = ROWS / kPer;
-    static_assert(1024 % L::kRow == 0 && kInstr % WAVES == 0, "whole rows, the same number for every wave");
+    static constexpr int kPer = 1024 / L::kRow, kCopies = ROWS / kPer / WAVES;
+    static_assert(1024 % L::kRow == 0 && kPer * kCopies * WAVES == ROWS, "whole rows, the same number for every wave");
+    // copies a multiple of 16 rows apart have the same swizzle and share an offset
+    static constexpr bool kShared = kPer * WAVES % 16 == 0;
+    static constexpr int kOffsets = kShared ? 1 : kCopies;
+    uint32_t off[kOffsets], apart;
+    int wave, lane;
+    // offset(r): bytes from the tile's first row to row r; rows kPer * WAVES
+    // apart are the same number of bytes apart everywhere
+    template <typename F> __device__ __forceinline__ TileCopy(int wave_, int lane_, F offset) : wave(wave_), lane(lane_) {
 #pragma unroll
-    for (int j = 0; j < kInstr / WAVES; ++j) {
-        const int jj = wave + j * WAVES, r = jj * kPer + lane / L::kUnits;
-        const uint32_t u = (lane % L::kUnits) ^ L::swz(r);  // the unit that belongs there
-        const uint32_t off = static_cast<uint32_t>(offset(r)) * sizeof(T) + u * 16;
-        copy_1k(tile_a + jj * 1024, a, off);
-        copy_1k(tile_b + jj * 1024, b, off);
+        for (int j = 0; j < kOffsets; ++j) off[j] = static_cast<uint32_t>(offset(row(j))) + unit(j);
+        apart = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(offset(kPer * WAVES)));
     }
-}
-// Copies ROWS rows, `stride` elements apart, of which `left` (at least 1) exist
-// (the last one stands in for the rest).  Where a wave's copies are a multiple
-// of 16 rows apart their swizzle is the same, and away from the end they share
-// one lane offset.
-template <typename T, int D, int ROWS, int WAVES>
-__device__ __forceinline__ void copy_keys(uint32_t tile, const T* base, size_t stride, int left, int wave, int lane) {
-    using L = Tile<T, D>;
-    constexpr int kPer = 1024 / L::kRow, kCopies = ROWS / kPer / WAVES, kApart = kPer * WAVES;
-    static_assert(1024 % L::kRow == 0 && ROWS % kApart == 0, "whole rows, the same number for every wave");
-    const int r0 = wave * kPer + lane / L::kUnits, x = lane % L::kUnits;
-    const uint32_t bytes = static_cast<uint32_t>(stride) * sizeof(T);
-    if (kApart % 16 == 0 && left >= ROWS) {
-        const uint32_t off = r0 * bytes + ((x ^ L::swz(r0)) << 4);
-#pragma unroll
-        for (int j = 0; j < kCopies; ++j) copy_1k(tile + (wave + j * WAVES) * 1024, base + j * kApart * stride, off);
-    } else {
+    __device__ __forceinline__ int row(int j) const { return (wave + j * WAVES) * kPer + lane / L::kUnits; }
+    __device__ __forceinline__ uint32_t unit(int j) const { return ((lane % L::kUnits) ^ L::swz(row(j))) << 4; }
+    __device__ __forceinline__ void run(uint32_t tile, const void* base) const {
+        const uint32_t at = tile + wave * 1024;
 #pragma unroll
         for (int j = 0; j < kCopies; ++j) {
-            const int r = r0 + j * kApart;
-            copy_1k(tile + (wave + j * WAVES) * 1024, base, min(r, left - 1) * bytes + ((x ^ L::swz(r)) << 4));
+            const void* from = kShared ? static_cast<const unsigned char*>(base) + j * apart : base;
+            asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at),
+                         "v"(off[kShared ? 0 : j]), "s"(from), "n"(j * WAVES * 1024)
+                         : "memory", "scc");
         }
     }
-}
+    // any other tile: address(r) is row r's
+    template <typename F> __device__ __forceinline__ void gather(uint32_t tile, F address) const {
+#pragma unroll
+        for (int j = 0; j < kCopies; ++j)
+            copy_1k_from(tile + (wave + j * WAVES) * 1024, reinterpret_cast<const unsigned char*>(address(row(j))) + unit(j));
+    }
+};
 
 // Which of `tiles` pieces of work (rank 0 the longest) of which head workgroup
 // bid takes.  Workgroups go round the 8 XCDs: a head's pieces stay on one, whose
@@ -329,6 +325,45 @@ __device__ __forceinline__ void place(int bid, int heads, int tiles, int& head, 
     }
 }
 
+// The keys that the rows of a workgroup may see, as one list: the sinks before
+// the window of its first row, then everything from there to its last row's
+// position.  Tiles are cut from the list, so neither the sinks nor a window that
+// starts anywhere cost a tile of their own.
+struct KeyList {
+    int sinks;  // keys 0 .. sinks-1 come first
+    int jump;   // entry x >= sinks is key x + jump
+    int count;
+    // rows at positions p0 .. p1 (p1 < 0: no keys)
+    __device__ __forceinline__ KeyList(int window, int sink_keys, int p0, int p1) {
+        const int lo = window ? max(0, p0 - window + 1) : 0;
+        sinks = min(sink_keys, lo);
+        jump = lo - sinks;
+        count = p1 < 0 ? 0 : p1 - jump + 1;
+    }
+    __device__ __forceinline__ int key(int x) const { return x < sinks ? x : x + jump; }
+};
+
+// Tiles of BN entries of a list, as a wave looks at them (its 32 NS keys of a
+// tile begin at entry `sub`, its rows are at positions p0 .. p1).
+struct TileRange {
+    int full_lo, full_hi;    // tiles whose keys follow one another and exist
+    int whole_lo, whole_hi;  // tiles that every row sees all of
+    int end;                 // tiles from here on no row sees
+    template <int BN, int SPAN>
+    static __device__ __forceinline__ TileRange of(const KeyList& keys, int window, int Tk, int sub, int p0, int p1) {
+        static_assert((BN & (BN - 1)) == 0, "shifts floor, also below zero");
+        constexpr int lg = __builtin_ctz(BN);
+        TileRange t;
+        t.full_lo = (keys.sinks + BN - 1) >> lg;
+        t.full_hi = (Tk - keys.jump) >> lg;
+        t.whole_lo = (keys.sinks - sub + BN - 1) >> lg;
+        if (window) t.whole_lo = max(t.whole_lo, (p1 - window + 1 - keys.jump - sub + BN - 1) >> lg);
+        t.whole_hi = ((p0 + 1 - SPAN - keys.jump - sub) >> lg) + 1;
+        t.end = ((p1 - keys.jump - sub) >> lg) + 1;
+        return t;
+    }
+};
+
 // Keys and queries of one sequence.  Query i is at position i + off; key j is
 // visible to position p if j <= p and (window == 0 or j > p - window or j <
 // sinks).  window is at most the number of keys, so p + window cannot wrap.
@@ -336,14 +371,6 @@ struct Mask {
     int window, sinks;
     __device__ __forceinline__ bool sees(int p, int j) const {
         return j <= p && (window == 0 || j > p - window || j < sinks);
-    }
-    // every key of [j0, j1] is visible from every position of [p0, p1]
-    __device__ __forceinline__ bool all(int p0, int p1, int j0, int j1) const {
-        return j1 <= p0 && (window == 0 || j0 > p1 - window || j1 < sinks);
-    }
-    // no key of [j0, j1] is visible from any position of [p0, p1]
-    __device__ __forceinline__ bool none(int p0, int p1, int j0, int j1) const {
-        return j0 > p1 || (window != 0 && j1 <= p0 - window && j0 >= sinks);
     }
 };
 

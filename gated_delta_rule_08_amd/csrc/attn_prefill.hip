@@ -86,7 +86,7 @@ __device__ __forceinline__ void exact_rows(Mask mask, int pos, bool live, int wp
 // 32 rows per wave, or with SPLIT 32 rows per workgroup, each wave taking a
 // quarter of the keys and the four joined at the end.
 template <typename T, int D, bool SPLIT>
-__global__ __launch_bounds__(64 * kWaves, 2) void prefill_kernel(PrefillArgs a, const T* __restrict__ q,
+__global__ __launch_bounds__(64 * kWaves, (PrefillCfg<T, D, SPLIT>::kBufs)) void prefill_kernel(PrefillArgs a, const T* __restrict__ q,
                                                                  const T* __restrict__ k,
                                                                  const T* __restrict__ v, T* __restrict__ o,
                                                                  float* __restrict__ lse) {
@@ -126,23 +126,29 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prefill_kernel(PrefillArgs a, 
     const int wp1 = __builtin_amdgcn_readfirstlane(G(wr1) + off);
     const size_t qrow = (q0 + qi) * a.Hq + static_cast<size_t>(hk) * G.d + g;
 
-    // key tiles of the workgroup's rows: the sinks before the window, then the window
-    const int p0 = G(row0) + off, p1 = G(min(row0 + kGroup - 1, nrows - 1)) + off;
-    const int win = a.window;
-    const int w_lo = win ? max(0, p0 - win + 1) : 0;
-    const int t_lo = w_lo / BN, t_hi = p1 < 0 ? -1 : p1 / BN;  // p1 <= Tk - 1
-    const int t_sink = win ? min((a.sinks + BN - 1) / BN, t_lo) : 0;
-    const int n = t_hi < t_lo ? 0 : t_sink + t_hi - t_lo + 1;
+    const KeyList keys(a.window, a.sinks, G(row0) + off, G(min(row0 + kGroup - 1, nrows - 1)) + off);
+    const int n = (keys.count + BN - 1) / BN;
 
     const size_t kstride = static_cast<size_t>(a.Hkv) * D;
     const T* kbase = k + (k0 * a.Hkv + hk) * D;
     const T* vbase = v + (k0 * a.Hkv + hk) * D;
-    auto tile_of = [&](int i) { return i < t_sink ? i : i - t_sink + t_lo; };
-    auto fetch = [&](int i) {
+    const int sub = SPLIT ? 32 * wave : 0;  // this wave's keys of a step
+    const TileRange range = TileRange::of<BN, 32 * NS>(keys, a.window, Tk, sub, wp0, wp1);
+    const int end = wave_live ? range.end : 0;
+    const TileCopy<T, D, BN, kWaves> copy(wave, lane, [&](int r) { return r * static_cast<int>(kstride * sizeof(T)); });
+    const T *kp = kbase + keys.jump * kstride, *vp = vbase + keys.jump * kstride;  // the next tile's first rows
+    auto fetch = [&](int i) {  // tiles in turn
         const uint32_t buf = lds_addr(smem) + (i & (C::kBufs - 1)) * 2 * C::kTileBytes;
-        const int j0 = tile_of(i) * BN;
-        copy_keys<T, D, BN, kWaves>(buf, kbase + j0 * kstride, kstride, Tk - j0, wave, lane);
-        copy_keys<T, D, BN, kWaves>(buf + C::kTileBytes, vbase + j0 * kstride, kstride, Tk - j0, wave, lane);
+        if (i >= range.full_lo && i < range.full_hi) {
+            copy.run(buf, kp);
+            copy.run(buf + C::kTileBytes, vp);
+        } else {
+            auto row = [&](int r) { return static_cast<size_t>(min(keys.key(i * BN + r), Tk - 1)) * kstride; };
+            copy.gather(buf, [&](int r) { return kbase + row(r); });
+            copy.gather(buf + C::kTileBytes, [&](int r) { return vbase + row(r); });
+        }
+        kp += BN * kstride;
+        vp += BN * kstride;
     };
     if (C::kBufs == 2 && n > 0) fetch(0);
 
@@ -166,7 +172,6 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prefill_kernel(PrefillArgs a, 
     for (int t = 0; t < DT; ++t) acc[t] = zero16();
     float m = -INFINITY, l = 0.f;
 
-    const int sub = SPLIT ? 32 * wave : 0;  // this wave's keys of a step
     const int kb0 = RowRead<T, D>::base(lane & 31, h2) + sub * Tile<T, D>::kRow;
     const int vb0 = ColRead<T, D>::base(lane) + sub * Tile<T, D>::kRow + C::kTileBytes;
 #pragma unroll 1
@@ -178,8 +183,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prefill_kernel(PrefillArgs a, 
         tile_barrier();
         if (C::kBufs == 2 && i + 1 < n) fetch(i + 1);
         const int buf = (i & (C::kBufs - 1)) * 2 * C::kTileBytes, kb = kb0 + buf, vb = vb0 + buf;
-        const int j0 = tile_of(i) * BN + sub;
-        if (!wave_live || mask.none(wp0, wp1, j0, j0 + 32 * NS - 1)) continue;
+        if (i >= end) continue;
 
         // The other wave of the SIMD is in another phase: a wave in its products
         // goes first, the exponentials of the other fill the gaps.  With d = 128
@@ -195,12 +199,13 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prefill_kernel(PrefillArgs a, 
                 s[u] = mma32(RowRead<T, D>::get(smem, kb, e, 32 * u * Tile<T, D>::kRow), qf[e], s[u]);
         }
         if (D == 64) __builtin_amdgcn_s_setprio(0);
-        if (!mask.all(wp0, wp1, j0, j0 + 32 * NS - 1)) {
+        if (i < range.whole_lo || i >= range.whole_hi) {
+            const int x0 = i * BN + sub;
 #pragma unroll
             for (int u = 0; u < NS; ++u)
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
-                    if (!mask.sees(pos, j0 + 32 * u + row32(r, h2))) s[u][r] = -INFINITY;
+                    if (!mask.sees(pos, keys.key(x0 + 32 * u + row32(r, h2)))) s[u][r] = -INFINITY;
         }
         float mx = s[0][0];
 #pragma unroll
@@ -315,13 +320,15 @@ hipError_t launch_tiles(const PrefillArgs& a, const void* q, const void* k, cons
     return hipGetLastError();
 }
 
-// Fewer 128-row workgroups than CUs: 32-row workgroups instead, each wave a
-// quarter of the keys.
+// Few 128-row workgroups: 32-row workgroups instead, each wave a quarter of the
+// keys, which costs four times the copies to LDS.  bf16 below 192 (8 heads:
+// T=1024 16 against 29 us, T=2048 39 / 52; 32 query on 8 key heads: T=768, 192
+// workgroups, 30 / 24), fp32 up to 256 (T=1000 120 / 146).
 template <typename T, int D>
 hipError_t launch(PrefillArgs a, const void* q, const void* k, const void* v, void* o, float* lse, hipStream_t st) {
     const long long rows = static_cast<long long>(a.Tq) * a.G.d, heads = static_cast<long long>(a.B) * a.Hkv;
     a.tiles = static_cast<int>((rows + kRows - 1) / kRows);
-    if (heads * a.tiles >= 256) return launch_tiles<T, D, false>(a, q, k, v, o, lse, st);
+    if (heads * a.tiles >= (sizeof(T) == 2 ? 192 : 257)) return launch_tiles<T, D, false>(a, q, k, v, o, lse, st);
     a.tiles = static_cast<int>((rows + 31) / 32);
     return launch_tiles<T, D, true>(a, q, k, v, o, lse, st);
 }

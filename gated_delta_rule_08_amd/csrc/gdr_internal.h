@@ -138,7 +138,7 @@ hipError_t launch_attn_prefill(int dtype, int B, int Tq, int Tk, int Hq, int Hkv
                                float scale, const void* q, const void* k, const void* v, void* o, float* lse,
                                hipStream_t s, const AttnPacked& pk = AttnPacked());
 
-size_t attn_backward_workspace_floats(int B, int Tq, int Tk, int Hq, int Hkv, int d, int window, int sinks);
+size_t attn_backward_workspace_floats(int dtype, int B, int Tq, int Tk, int Hq, int Hkv, int d, int window, int sinks);
 hipError_t launch_attn_backward(int dtype, int B, int Tq, int Tk, int Hq, int Hkv, int d, int window, int sinks,
                                 float scale, const void* q, const void* k, const void* v, const void* o,
                                 const float* lse, const void* go, void* gq, void* gk, void* gv, float* ws,
