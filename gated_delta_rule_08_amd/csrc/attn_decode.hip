@@ -25,6 +25,8 @@ namespace gdr {
 namespace attn {
 namespace {
 
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
 constexpr int kWaves = 4;
 constexpr int kStep = 32;                // keys of a wave's step
 constexpr int kBlock = kStep * kWaves;   // keys of a workgroup's step
@@ -574,37 +576,61 @@ hipError_t launch_decode_t(const DecodeArgs& a, const void* q, const void* k, co
     return hipGetLastError();
 }
 
-// Append: one 16-byte unit of one key head's new row (K and V) per thread.
-__global__ __launch_bounds__(256) void append_kernel(int N, int total, int Hkv, int units, int page_shift,
-                                                     int num_pages, int max_pages, const uint4* __restrict__ k,
-                                                     const uint4* __restrict__ v, const int* __restrict__ cu,
-                                                     const int* __restrict__ lengths, uint4* __restrict__ k_pages,
-                                                     uint4* __restrict__ v_pages, const int* __restrict__ table) {
-    const int per = Hkv * units;  // units of one token
-    const size_t n = static_cast<size_t>(total) * per;
-    for (size_t i = static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x; i < n;
-         i += static_cast<size_t>(gridDim.x) * 256) {
-        const int t = static_cast<int>(i / per), x = static_cast<int>(i - static_cast<size_t>(t) * per);
-        int lo = 0, hi = N;  // the last sequence that starts at or before t
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (cu[mid] <= t)
-                lo = mid;
-            else
-                hi = mid;
-        }
-        const int begin = cu[lo], len = lengths[lo];
-        if (begin < 0 || t < begin || t >= cu[lo + 1] || len < 0) continue;
-        const long long pos = static_cast<long long>(len) + (t - begin);
-        if ((pos >> page_shift) >= max_pages) continue;
-        const int page = table[static_cast<size_t>(lo) * max_pages + (pos >> page_shift)];
-        if (page < 0 || page >= num_pages) continue;
-        const int hk = x / units, u = x - hk * units;
-        const size_t row = ((static_cast<size_t>(page) * Hkv + hk) << page_shift) +
-                           static_cast<size_t>(pos & ((1 << page_shift) - 1));
-        k_pages[row * units + u] = k[i];
-        v_pages[row * units + u] = v[i];
+// Append: a workgroup copies 1024 consecutive 16-byte units of the new keys and
+// the same of the values, four of each per thread.  The first unit's sequence is
+// searched for once; the others start from it.
+constexpr int kAppendUnits = 4;
+
+__global__ __launch_bounds__(256) void append_kernel(int N, unsigned long long n, FastDiv per, FastDiv units,
+                                                     int page_shift, int num_pages, int max_pages, int Hkv,
+                                                     const u32x4* __restrict__ k, const u32x4* __restrict__ v,
+                                                     const int* __restrict__ cu, const int* __restrict__ lengths,
+                                                     u32x4* __restrict__ k_pages, u32x4* __restrict__ v_pages,
+                                                     const int* __restrict__ table) {
+    const unsigned long long first = static_cast<unsigned long long>(blockIdx.x) * (256 * kAppendUnits);
+    const int t0 = static_cast<int>(first / per.d), x0 = static_cast<int>(first - static_cast<unsigned long long>(t0) * per.d);
+    int seq = 0;  // the last sequence that starts at or before token t0
+    for (int hi = N; hi - seq > 1;) {
+        const int mid = (seq + hi) >> 1;
+        if (cu[mid] <= t0)
+            seq = mid;
+        else
+            hi = mid;
     }
+    const int mask = (1 << page_shift) - 1;
+    u32x4 a[kAppendUnits], b[kAppendUnits];
+    size_t to[kAppendUnits];
+    bool ok[kAppendUnits];
+#pragma unroll
+    for (int j = 0; j < kAppendUnits; ++j) {
+        const int i = threadIdx.x + 256 * j;
+        ok[j] = first + i < n;
+        if (!ok[j]) continue;
+        a[j] = __builtin_nontemporal_load(k + first + i);
+        b[j] = __builtin_nontemporal_load(v + first + i);
+    }
+#pragma unroll
+    for (int j = 0; j < kAppendUnits; ++j) {
+        if (!ok[j]) continue;
+        const int i = x0 + threadIdx.x + 256 * j, y = per(i), t = t0 + y, x = i - y * per.d;
+        int s = seq;
+        while (s + 1 < N && cu[s + 1] <= t) ++s;
+        const int begin = cu[s], len = lengths[s];
+        const long long pos = static_cast<long long>(len) + (t - begin);
+        ok[j] = begin >= 0 && t >= begin && t < cu[s + 1] && len >= 0 && (pos >> page_shift) < max_pages;
+        if (!ok[j]) continue;
+        const int page = table[static_cast<size_t>(s) * max_pages + (pos >> page_shift)];
+        ok[j] = page >= 0 && page < num_pages;
+        const int hk = units(x), u = x - hk * units.d;
+        const size_t row = ((static_cast<size_t>(page) * Hkv + hk) << page_shift) + static_cast<size_t>(pos & mask);
+        to[j] = row * units.d + u;
+    }
+#pragma unroll
+    for (int j = 0; j < kAppendUnits; ++j)
+        if (ok[j]) {
+            __builtin_nontemporal_store(a[j], k_pages + to[j]);
+            __builtin_nontemporal_store(b[j], v_pages + to[j]);
+        }
 }
 
 int log2_of(int x) {
@@ -658,12 +684,12 @@ hipError_t launch_attn_append(int dtype, int N, int total, int Hkv, int d, int p
                               void* k_pages, void* v_pages, const int* table, hipStream_t st) {
     const int units = d * (dtype == GDR_DTYPE_F32 ? 4 : 2) / 16;
     const unsigned long long n = static_cast<unsigned long long>(total) * Hkv * units;
-    const unsigned long long want = (n + 255) / 256;
-    const unsigned blocks = static_cast<unsigned>(want < 16384 ? want : 16384);
-    hipLaunchKernelGGL(attn::append_kernel, dim3(blocks), dim3(256), 0, st, N, total, Hkv, units,
-                       attn::log2_of(page_size), num_pages, max_pages, static_cast<const uint4*>(k),
-                       static_cast<const uint4*>(v), cu, lengths, static_cast<uint4*>(k_pages),
-                       static_cast<uint4*>(v_pages), table);
+    const unsigned long long blocks = (n + 256 * attn::kAppendUnits - 1) / (256 * attn::kAppendUnits);
+    if (!grid_fits(blocks, 256)) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL(attn::append_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, N, n,
+                       attn::FastDiv(Hkv * units), attn::FastDiv(units), attn::log2_of(page_size), num_pages, max_pages, Hkv,
+                       static_cast<const attn::u32x4*>(k), static_cast<const attn::u32x4*>(v), cu, lengths,
+                       static_cast<attn::u32x4*>(k_pages), static_cast<attn::u32x4*>(v_pages), table);
     return hipGetLastError();
 }
 
