@@ -40,7 +40,7 @@ def test_prefill(lib):
     assert prefill(lib, dtype=2) == ENUM
     for kw in (dict(B=-1), dict(Tq=-1), dict(Tk=-1), dict(Hq=-1), dict(Hkv=-1), dict(window=-1), dict(sinks=-1),
                dict(Hq=5), dict(Hkv=0), dict(Tq=BIG), dict(Tk=BIG), dict(Tq=1 << 28, Hq=32), dict(B=BIG, Hq=64, Hkv=64),
-               dict(B=1 << 20, Tq=1 << 20)):
+               dict(B=1 << 20, Tq=1 << 20), dict(Hq=1 << 16, Hkv=1 << 16), dict(Tq=1 << 27), dict(Tk=1 << 28)):
         assert prefill(lib, **kw) == SHAPE, kw
     for d in (0, 16, 63, 96, 256, -64):
         assert prefill(lib, d=d) == UNSUP

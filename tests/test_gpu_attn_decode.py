@@ -83,6 +83,83 @@ def test_decode(dt, Hq, Hkv, d, page, window, sinks):
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("Hq,Hkv,d,page,window,sinks", [
+    (1, 1, 128, 1, 0, 0), (8, 2, 128, 16, 0, 0), (6, 2, 64, 4, 700, 5), (40, 1, 128, 64, 0, 0), (17, 1, 64, 32, 520, 300),
+    (4, 4, 128, 16, 600, 0), (5, 5, 128, 2, 1000, 1), (36, 2, 64, 256, 0, 0),
+])
+def test_decode_long_tables(dt, Hq, Hkv, d, page, window, sinks):
+    """Tables with room for long sequences: the shares of the batch's key blocks, joined where they meet."""
+    announce("attn decode long tables %s %s" % (dt, (Hq, Hkv, d, page, window, sinks)))
+    assert gdr.gdr_attn_decode_workspace_bytes(DT[dt], 9, Hq, Hkv, d, page, -(-900 // page), window, sinks) > 0
+    run_decode(dt, [0, 1, 127, 128, 129, 300, 640, 5, 899], Hq, Hkv, d, page, window, sinks)
+
+
+def test_decode_many_sequences():
+    """More sequences than one scan of the lengths takes, among them empty, out of range and without a page."""
+    announce("attn decode many sequences")
+    n, page, Hq, Hkv, d = 700, 16, 4, 2, 64
+    lengths = [(37 * b) % 90 if b % 5 else 0 for b in range(n)]
+    lengths[3], lengths[400], lengths[699] = 800, 1300, 600
+    c = Cache("bf16", lengths, [1] * n, Hkv, d, page)
+    q, k, v = make(1, "bf16", n, Hq, d), make(2, "bf16", n, Hkv, d), make(3, "bf16", n, Hkv, d)
+    kp, vp, table, lens = c.device()
+    bad = [0, 1, 255, 256, 257, 511, 512, 650]
+    for i, b in enumerate(bad):
+        if i % 3 == 0:
+            lens[b] = -1 - b
+        elif i % 3 == 1:
+            lens[b] = table.shape[1] * page + b
+        else:
+            table[b, lengths[b] // page] = -1
+    o = torch.full_like(q, 7.0).cuda()
+    gdr.gdr_attn_decode(q.cuda(), k.cuda(), v.cuda(), kp, vp, table, lens, o)
+    torch.cuda.synchronize()
+    for b, m in enumerate(lengths):
+        if b in bad:
+            assert (o[b] == 7).all()
+            continue
+        c.put(b, m, k[b:b + 1], v[b:b + 1])
+        full = [torch.cat([t, x[b:b + 1]]) for t, x in zip(c.tokens[b], (k, v))]
+        check("o[%d]" % b, o[b:b + 1], *attend(q[b:b + 1], *full, 0, 0, 0.125, torch.bfloat16)["o"])
+    assert same(kp, c.k) and same(vp, c.v)
+
+
+def test_cache_beyond_4_gib():
+    """Page tensors of 8.6 GB each, the sequence's pages at their far end and at their front."""
+    announce("attn cache beyond 4 GiB")
+    pages, Hkv, Hq, page, d, n = 1 << 17, 2, 4, 128, 128, 700
+    kp = torch.empty(pages, Hkv, page, d, dtype=torch.bfloat16, device="cuda")
+    vp = torch.empty_like(kp)
+    table = torch.tensor([[pages - 1, 0, pages - 2, pages // 2 + 3, 1, pages - 7, -1]], dtype=torch.int32, device="cuda")
+    k, v, q = make(1, "bf16", n + 1, Hkv, d), make(2, "bf16", n + 1, Hkv, d), make(3, "bf16", 1, Hq, d)
+    lens = torch.zeros(1, dtype=torch.int32, device="cuda")
+    gdr.gdr_attn_append(k[:n].cuda(), v[:n].cuda(), torch.tensor([0, n], dtype=torch.int32, device="cuda"), lens, kp, vp, table)
+    lens += n
+    o = torch.empty_like(q).cuda()
+    gdr.gdr_attn_decode(q.cuda(), k[n:].cuda(), v[n:].cuda(), kp, vp, table, lens, o)
+    check("o", o, *attend(q, k, v, 0, 0, d ** -0.5, torch.bfloat16)["o"])
+    assert same(kp[pages - 7, :, n % page], k[n]) and same(vp[pages - 2, :, 5], v[2 * page + 5])
+
+
+def test_append_many_sequences():
+    """Units of one workgroup from many sequences, empty ones between them."""
+    announce("attn append many sequences")
+    page, Hkv, d = 4, 1, 64
+    new = [(i * 7) % 5 for i in range(200)]
+    lengths = [(i * 3) % 11 for i in range(200)]
+    c = Cache("bf16", lengths, new, Hkv, d, page)
+    cu = [0]
+    for n in new:
+        cu.append(cu[-1] + n)
+    k, v = make(1, "bf16", cu[-1], Hkv, d), make(2, "bf16", cu[-1], Hkv, d)
+    kp, vp, table, lens = c.device()
+    gdr.gdr_attn_append(k.cuda(), v.cuda(), torch.tensor(cu, dtype=torch.int32).cuda(), lens, kp, vp, table)
+    for b, n in enumerate(new):
+        c.put(b, lengths[b], k[cu[b]:cu[b + 1]], v[cu[b]:cu[b + 1]])
+    assert same(kp, c.k) and same(vp, c.v)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
 @pytest.mark.parametrize("window,sinks", [(0, 0), (1500, 200)])
 def test_decode_split_over_the_length(dt, window, sinks):
     """Long and short sequences in one call: most are cut into parts and joined, short ones are not."""

@@ -78,6 +78,70 @@ def test_forward_and_backward(case, dt):
             check(name, got[b], *ref[name])
 
 
+# Enough heads that every workgroup takes 128 rows or keys: full causal (the first keys' row lists sliced or not) and
+# windows (sink keys' rows in segments), head counts that are and are not a multiple of 8, groups that do and do not
+# divide 32, one and several rounds of workgroups
+MANY = [
+    (33, 150, 150, 16, 8, 64, 0, 0),
+    (33, 150, 150, 16, 8, 128, 40, 3),
+    (24, 300, 300, 12, 12, 128, 0, 0),
+    (40, 97, 160, 24, 8, 128, 64, 70),
+    (26, 129, 129, 15, 5, 64, 100, 2),
+    (300, 33, 33, 1, 1, 64, 0, 0),
+    (260, 40, 20, 2, 1, 128, 0, 0),
+    (260, 64, 200, 2, 1, 64, 130, 131),
+    (8, 700, 700, 32, 4, 64, 0, 0),
+    (64, 260, 260, 7, 7, 128, 33, 1),
+]
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("case", MANY, ids=lambda c: "x".join(map(str, c)))
+def test_many_heads(case, dt):
+    B, Tq, Tk, Hq, Hkv, d, window, sinks = case
+    announce("attn many heads %s %s" % (dt, case))
+    q, k, v, go = make(1, dt, B, Tq, Hq, d), make(2, dt, B, Tk, Hkv, d), make(3, dt, B, Tk, Hkv, d), make(4, dt, B, Tq, Hq, d)
+    o, lse = forward(q, k, v, window, sinks, 0.1)
+    dq, dk, dv = (torch.full_like(x, 7.0).cuda() for x in (q, k, v))
+    gdr.gdr_attn_backward(q.cuda(), k.cuda(), v.cuda(), o, lse, go.cuda(), dq, dk, dv, window=window, sinks=sinks, scale=0.1)
+    torch.cuda.synchronize()
+    for t in (o, lse, dq, dk, dv):  # every row was written
+        assert not (t.reshape(-1, t.shape[-1]) == 7).all(-1).any()
+    for b in sorted({0, 1, B // 2, B - 1}):
+        ref = attend(q[b], k[b], v[b], window, sinks, 0.1, DT[dt], go[b])
+        for name, got in (("o", o), ("lse", lse), ("grad_q", dq), ("grad_k", dk), ("grad_v", dv)):
+            check(name, got[b], *ref[name])
+
+
+def test_tensors_beyond_4_gib():
+    """Keys and values of 4.7 GB each, the queries at their end: sinks at the front, the window at the far end."""
+    announce("attn beyond 4 GiB")
+    Tk, Tq, H, d, window, sinks = 71000, 40, 256, 128, 100, 5
+    g = torch.Generator(device="cuda").manual_seed(1)
+    k = torch.zeros(1, Tk, H, d, dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    seen = list(range(sinks)) + list(range(Tk - Tq - window, Tk))
+    for t in (k, v):
+        t[:, :sinks] = torch.randn(1, sinks, H, d, generator=g, device="cuda")
+        t[:, Tk - Tq - window:] = torch.randn(1, Tq + window, H, d, generator=g, device="cuda")
+        t[:, sinks + 1] = float("nan")  # seen by no query
+    q, go = (torch.randn(1, Tq, H, d, generator=g, device="cuda").bfloat16() for _ in range(2))
+    o, lse = torch.empty_like(q), torch.empty(1, Tq, H, device="cuda")
+    gdr.gdr_attn_prefill(q, k, v, o, lse, window=window, sinks=sinks)
+    dq, dk, dv = torch.empty_like(q), torch.full_like(k, 7.0), torch.full_like(v, 7.0)
+    gdr.gdr_attn_backward(q, k, v, o, lse, go, dq, dk, dv, window=window, sinks=sinks)
+    torch.cuda.synchronize()
+    assert not dk[:, sinks:Tk - Tq - window].any() and not dv[:, sinks:Tk - Tq - window].any()
+    for h in (0, 1, 77, 255):
+        # the keys in between are never seen, so the reference may leave them out
+        x = [t[0, seen][:, h:h + 1].cpu() for t in (k, v)]
+        ref = attend(q[0, :, h:h + 1].cpu(), *x, window, sinks, d ** -0.5, torch.bfloat16, go[0, :, h:h + 1].cpu())
+        for name, got in (("o", o[0]), ("lse", lse[0]), ("grad_q", dq[0])):
+            check(name, got[:, h:h + 1], *ref[name])
+        for name, got in (("grad_k", dk), ("grad_v", dv)):
+            check(name, got[0, seen][:, h:h + 1], *ref[name])
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.3, 2.0])
 def test_scale(scale):
     announce("attn scale %g" % scale)
@@ -103,10 +167,11 @@ def test_large_scores(dt, d):
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 @pytest.mark.parametrize("what", ["nan", "inf"])
-def test_non_finite_values_stay_with_the_rows_that_see_them(dt, what):
+@pytest.mark.parametrize("B,d", [(1, 64), (140, 64), (1, 128), (140, 128)])
+def test_non_finite_values_stay_with_the_rows_that_see_them(dt, what, B, d):
     """A non-finite key, value, query or gradient row reaches exactly the outputs its definition gives it."""
-    announce("attn non-finite %s %s" % (dt, what))
-    B, T, Hq, Hkv, d, window, sinks, at = 1, 150, 4, 2, 64, 30, 2, 77
+    announce("attn non-finite %s %s %d %d" % (dt, what, B, d))
+    T, Hq, Hkv, window, sinks, at = 150, 4, 2, 30, 2, 77
     x = float(what)
     q, k, v, go = make(1, dt, B, T, Hq, d), make(2, dt, B, T, Hkv, d), make(3, dt, B, T, Hkv, d), make(4, dt, B, T, Hq, d)
     o0, lse0 = forward(q, k, v, window, sinks, 0.125)
