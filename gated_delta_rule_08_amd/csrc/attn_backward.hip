@@ -57,41 +57,6 @@ __host__ __device__ __forceinline__ void rows_of(const BwdArgs& a, int j0, int j
     if (a.slices > 1 && a.window && j0 < a.sinks) hi = a.rows;  // no segments: the sinks' rows are sliced with the rest
 }
 
-// What a wave does when a non-finite value met its sums (a hidden pair has
-// weight 0, and 0 times an infinity or NaN is NaN): its keys' gradients row by
-// row, hidden pairs left out.  A lane holds half of its key's channels.
-template <typename T, int D>
-__device__ __forceinline__ void exact_keys(const BwdArgs& a, int b, int hk, int key, int off, int lo, int hi, const T* q,
-                                        const T* k, const T* v, const T* go, float* dk, float* dv, int h2) {
-    constexpr int N = D / 2;
-    const Mask mask{a.window, a.sinks};
-    const size_t krow = ((static_cast<size_t>(b) * a.Tk + min(key, a.Tk - 1)) * a.Hkv + hk) * D;
-    const float c = a.scale * kLog2e;
-    const float* stat = a.stats + (static_cast<size_t>(b) * a.Hkv + hk) * 2 * a.pitch;
-#pragma unroll 1
-    for (int e = 0; e < N; ++e) dk[e] = dv[e] = 0.f;
-#pragma unroll 1
-    for (int r = lo; r < hi; ++r) {
-        const int i = a.G(r);
-        const size_t qrow = ((static_cast<size_t>(b) * a.Tq + i) * a.Hq + hk * a.G.d + (r - i * a.G.d)) * D;
-        float s = 0.f, dp = 0.f;
-#pragma unroll 1
-        for (int e = N * h2; e < N * h2 + N; ++e) {
-            s = fmaf(Elem<T>::load(q + qrow + e), Elem<T>::load(k + krow + e), s);
-            dp = fmaf(Elem<T>::load(go + qrow + e), Elem<T>::load(v + krow + e), dp);
-        }
-        s += other_half(s);
-        dp += other_half(dp);
-        if (!mask.sees(i + off, key)) continue;
-        const float p = ex2(fmaf(s, c, -stat[r])), ds = p * (dp - stat[a.pitch + r]);
-#pragma unroll 1
-        for (int e = 0; e < N; ++e) {
-            dk[e] = fmaf(ds, Elem<T>::load(q + qrow + N * h2 + e), dk[e]);
-            dv[e] = fmaf(p, Elem<T>::load(go + qrow + N * h2 + e), dv[e]);
-        }
-    }
-}
-
 template <typename T, int D, int WAVES> struct DkdvCfg {
     static constexpr int BM = 32;  // rows of a step
     static constexpr int kTile = BM * D * static_cast<int>(sizeof(T));
@@ -100,6 +65,94 @@ template <typename T, int D, int WAVES> struct DkdvCfg {
     static constexpr int kStatBuf = 8 * BM;
     static constexpr int kLds = kStat + 2 * kStatBuf;
 };
+
+// What one wave of dkdv_kernel has to do.
+struct Piece {
+    int head, b, hk;
+    int tile, j0;     // its 32 keys
+    int cut, lo, hi;  // the workgroup's rows
+    bool parts;       // the keys' rows are not all here
+};
+template <int WAVES> __device__ __forceinline__ Piece piece_of(const BwdArgs& a, int bid, int wave) {
+    constexpr bool kSeg = WAVES == 1;
+    const int per = kSeg ? a.sink_tiles * a.segs : a.key_blocks * a.slices;
+    int head, x, lo, hi;
+    place(bid, a.B * a.Hkv, per, head, x);  // the first keys are seen by the most rows
+    const int b = head / a.Hkv, cuts = kSeg ? a.segs : a.slices, y = x / cuts, cut = x - y * cuts;
+    const int tile = kSeg ? y : y * WAVES + wave;
+    const int m0 = kSeg ? 32 * tile / kKeys * kKeys : y * kKeys;  // the keys of a main workgroup
+    rows_of(a, m0, min(m0 + kKeys, a.Tk) - 1, lo, hi);
+    const bool parts = kSeg || hi - lo > a.slice_rows;
+    lo = kSeg ? hi + cut * a.seg_rows : lo + cut * a.slice_rows;  // a segment's are past what the main workgroup takes
+    hi = kSeg ? min(a.rows, lo + a.seg_rows) : min(hi, lo + a.slice_rows);
+    return {head, b, head - b * a.Hkv, tile, 32 * tile, cut, lo, hi, parts};
+}
+
+// 32 channels of a key's gradients, or of this part of them (fp32, dk's 32 rows
+// before dv's).
+template <typename T, int D>
+__device__ __forceinline__ void put_key(float* part, T* gk, T* gv, int t, const f32x16& dk, const f32x16& dv, float scale,
+                                        int h2) {
+    const f32x16 g = dk * scale;
+#pragma unroll
+    for (int r = 0; r < 16; r += 4) {
+        const int ch = 32 * t + row32(r, h2);
+        if (part) {
+            store4<float>(part + ch, g[r], g[r + 1], g[r + 2], g[r + 3]);
+            store4<float>(part + 32 * D + ch, dv[r], dv[r + 1], dv[r + 2], dv[r + 3]);
+        } else {
+            store4<T>(gk + ch, g[r], g[r + 1], g[r + 2], g[r + 3]);
+            store4<T>(gv + ch, dv[r], dv[r + 1], dv[r + 2], dv[r + 3]);
+        }
+    }
+}
+
+// What a wave does when a non-finite value has met its sums (a hidden pair has
+// weight 0, and 0 times an infinity or NaN is NaN): its keys' gradients once
+// more, hidden pairs left out.  Operands straight from global memory, 32 rows and
+// 32 channels at a time, no other wave involved.
+template <typename T, int D>
+__device__ __forceinline__ void seen_keys(Mask mask, FastDiv G, int Hq, int rows, int pitch, float scale, int off, int key,
+                                          int lo, int hi, const float* stat, const T* q, const T* go, const T* k, const T* v,
+                                          float* part, T* gk, T* gv, bool store, int lane) {
+    const int h2 = lane >> 5;
+    const float c = scale * kLog2e;
+#pragma unroll 1
+    for (int t = 0; t < D / 32; ++t) {
+        f32x16 dk = zero16(), dv = zero16();
+#pragma unroll 1
+        for (int r0 = lo; r0 < hi; r0 += 32) {
+            auto row = [&](int r) {
+                r = min(r0 + r, rows - 1);
+                const int y = G(r);
+                return (static_cast<size_t>(y) * Hq + (r - y * G.d)) * D;
+            };
+            uint32_t seen = 0;
+#pragma unroll 1
+            for (int r = 0; r < 16; ++r) {
+                const int at = r0 + row32(r, h2);
+                if (at < hi && mask.sees(G(at) + off, key)) seen |= 1u << r;
+            }
+            if (__ballot(seen != 0) == 0) continue;
+            f32x16 s = zero16(), dp = zero16();
+            const size_t mine = row(lane & 31) + 8 * h2;
+#pragma unroll 1
+            for (int e = 0; e < D / 16; ++e) {
+                s = mma32(load8(q + mine + 16 * e), load8(k + 8 * h2 + 16 * e), s);
+                dp = mma32(load8(go + mine + 16 * e), load8(v + 8 * h2 + 16 * e), dp);
+            }
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int in = min(r0 + row32(r, h2), rows - 1);
+                s[r] = ex2(fmaf(s[r], c, -stat[in]));
+                dp[r] = s[r] * (dp[r] - stat[pitch + in]);
+            }
+            mma32_seen<T>(dv, [&](int r) { return go + row(r) + 32 * t; }, s, seen, lane);
+            mma32_seen<T>(dk, [&](int r) { return q + row(r) + 32 * t; }, dp, seen, lane);
+        }
+        if (store) put_key<T, D>(part, gk, gv, t, dk, dv, scale, h2);
+    }
+}
 
 // WAVES = 4: 128 keys of one key head, every row that sees them through the
 // window.  WAVES = 1 (sinks): 32 sink keys, one segment of the rows past it.
@@ -114,28 +167,11 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && WAVES == 4 ? 2 : 1) v
     constexpr bool kSeg = WAVES == 1;
     extern __shared__ unsigned char smem[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h2 = lane >> 5;
-    const int per = kSeg ? a.sink_tiles * a.segs : a.key_blocks * a.slices;
-    int head, x;
-    place(blockIdx.x, a.B * a.Hkv, per, head, x);  // the first keys are seen by the most rows
-    const int b = head / a.Hkv, hk = head - b * a.Hkv;
-    const int cuts = kSeg ? a.segs : a.slices, y = x / cuts, cut = x - y * cuts;
-    const int tile = kSeg ? y : y * WAVES + wave;  // 32-key tile of this wave
-    const int j0 = 32 * tile, j1 = min(j0 + 31, a.Tk - 1), key = j0 + (lane & 31);
+    const Piece pc = piece_of<WAVES>(a, blockIdx.x, wave);
+    const int head = pc.head, b = pc.b, hk = pc.hk, lo = pc.lo, hi = pc.hi;
+    if (!kSeg && pc.cut > 0 && lo >= hi) return;
+    const int j0 = pc.j0, j1 = min(j0 + 31, a.Tk - 1), key = j0 + (lane & 31);
     const int off = a.Tk - a.Tq;
-
-    int lo, hi;
-    const int m0 = kSeg ? j0 / kKeys * kKeys : y * kKeys;  // the keys of a main workgroup
-    rows_of(a, m0, min(m0 + kKeys, a.Tk) - 1, lo, hi);
-    if (kSeg) {  // past what the main workgroup takes
-        lo = hi + cut * a.seg_rows;
-        hi = min(a.rows, lo + a.seg_rows);
-    }
-    const bool parts = kSeg || hi - lo > a.slice_rows;  // the keys' rows are not all here
-    if (!kSeg) {
-        lo += cut * a.slice_rows;
-        hi = min(hi, lo + a.slice_rows);
-        if (cut > 0 && lo >= hi) return;
-    }
     if (kSeg && lo >= hi) return;
     const bool wave_live = j0 < a.Tk;
     const size_t kstride = static_cast<size_t>(a.Hkv) * D;
@@ -267,47 +303,33 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && WAVES == 4 ? 2 : 1) v
     }
     if (!wave_live) return;
 
-    // the keys' gradients, or this part of them
-    float* part = nullptr;
-    if (parts || tile < a.sink_tiles)
-        part = a.part + ((static_cast<size_t>(head) * a.part_tiles + tile) * a.slots + (kSeg ? 1 + cut : cut)) * 64 * D;
     bool bad = false;
 #pragma unroll
     for (int t = 0; t < DT; ++t)
 #pragma unroll
         for (int r = 0; r < 16; ++r) bad |= dk[t][r] != dk[t][r] || dv[t][r] != dv[t][r];
-    if (__any(bad && key < a.Tk)) {
-        constexpr int N = D / 2;
-        float xk[N], xv[N];
-        exact_keys<T, D>(a, b, hk, key, off, lo, hi, q, k, v, go, xk, xv, h2);
-#pragma unroll 1
-        for (int e = 0; e < N; ++e) {
-            const int ch = N * h2 + e;
-            if (part) {
-                part[(lane & 31) * D + ch] = xk[e] * a.scale;
-                part[(32 + (lane & 31)) * D + ch] = xv[e];
-            } else if (key < a.Tk) {
-                Elem<T>::store(gk + k0 + key * kstride + ch, xk[e] * a.scale);
-                Elem<T>::store(gv + k0 + key * kstride + ch, xv[e]);
-            }
-        }
-        return;
+
+    // The keys' gradients, or this part of them.  Where they go is found again:
+    // nothing of it takes registers in the loop.
+    const Piece to = piece_of<WAVES>(a, __builtin_amdgcn_readfirstlane(again(blockIdx.x)), wave);
+    const int me = to.j0 + (again(lane) & 31);
+    const size_t at = ((static_cast<size_t>(to.b) * a.Tk + me) * a.Hkv + to.hk) * D;
+    float* part = nullptr;
+    if (to.parts || to.tile < a.sink_tiles)
+        part = a.part + (((static_cast<size_t>(to.head) * a.part_tiles + to.tile) * a.slots + (kSeg ? 1 + to.cut : to.cut)) * 64 +
+                         (me & 31)) * D;
+    const bool store = part ? !kSeg || me < a.sinks : me < a.Tk;  // a segment's other keys are not read by the join
+    if (store) {
+#pragma unroll
+        for (int t = 0; t < DT; ++t) put_key<T, D>(part, gk + at, gv + at, t, dk[t], dv[t], a.scale, again(lane) >> 5);
     }
-#pragma unroll
-    for (int t = 0; t < DT; ++t)
-#pragma unroll
-        for (int r = 0; r < 16; r += 4) {
-            const int ch = 32 * t + row32(r, h2);
-            const f32x16 g = dk[t] * a.scale;
-            if (part) {
-                if (kSeg && key >= a.sinks) continue;  // not read by the join
-                store4<float>(part + (lane & 31) * D + ch, g[r], g[r + 1], g[r + 2], g[r + 3]);
-                store4<float>(part + (32 + (lane & 31)) * D + ch, dv[t][r], dv[t][r + 1], dv[t][r + 2], dv[t][r + 3]);
-            } else if (key < a.Tk) {
-                store4<T>(gk + k0 + key * kstride + ch, g[r], g[r + 1], g[r + 2], g[r + 3]);
-                store4<T>(gv + k0 + key * kstride + ch, dv[t][r], dv[t][r + 1], dv[t][r + 2], dv[t][r + 3]);
-            }
-        }
+    if (__builtin_expect(__ballot(bad && store) != 0, 0)) {
+        const size_t kr = ((static_cast<size_t>(to.b) * a.Tk + min(me, a.Tk - 1)) * a.Hkv + to.hk) * D;
+        const size_t q0 = (static_cast<size_t>(to.b) * a.Tq * a.Hq + static_cast<size_t>(to.hk) * a.G.d) * D;
+        seen_keys<T, D>(Mask{a.window, a.sinks}, a.G, a.Hq, a.rows, a.pitch, a.scale, a.Tk - a.Tq, me, to.lo, to.hi,
+                        a.stats + static_cast<size_t>(to.head) * 2 * a.pitch, q + q0, go + q0, k + kr, v + kr, part, gk + at,
+                        gv + at, store, again(lane));
+    }
 }
 
 // Adds the parts of one key tile: 32 groups of four elements a workgroup, eight
@@ -342,33 +364,36 @@ __global__ __launch_bounds__(256) void join_kernel(BwdArgs a, T* __restrict__ gk
     store4<T>(dst, s[0], s[1], s[2], s[3]);
 }
 
-// As exact_keys, for one wave's rows of dQ.
-template <typename T, int D>
-__device__ __forceinline__ void exact_dq(const BwdArgs& a, Mask mask, int pos, bool live, int wp1, float lse2, float delta,
-                                      const T* q, const T* go, const T* k, const T* v, size_t stride, T* gq, int h2) {
-    constexpr int N = D / 2;
+// As seen_keys, for one wave's rows of dQ.
+template <typename T, int D, typename P>
+__device__ __forceinline__ void seen_dq(const BwdArgs& a, Mask mask, int pos, int wp0, int wp1, float lse2, float delta,
+                                        const T* q, const T* go, const T* k, const T* v, size_t stride, int lane, P put) {
+    const int h2 = lane >> 5;
     const float c = a.scale * kLog2e;
-    float dq[N];
+    const KeyList keys(mask.window, mask.sinks, wp0, wp1);
 #pragma unroll 1
-    for (int e = 0; e < N; ++e) dq[e] = 0.f;
+    for (int t = 0; t < D / 32; ++t) {
+        f32x16 dq = zero16();
 #pragma unroll 1
-    for (int j = 0; j <= wp1; ++j) {
-        float s = 0.f, dp = 0.f;
+        for (int x0 = 0; x0 < keys.count; x0 += 32) {
+            auto row = [&](int r) { return static_cast<size_t>(min(keys.key(x0 + r), a.Tk - 1)) * stride; };
+            f32x16 s = zero16(), dp = zero16();
+            const size_t mine = row(lane & 31) + 8 * h2;
 #pragma unroll 1
-        for (int e = N * h2; e < N * h2 + N; ++e) {
-            s = fmaf(Elem<T>::load(q + e), Elem<T>::load(k + j * stride + e), s);
-            dp = fmaf(Elem<T>::load(go + e), Elem<T>::load(v + j * stride + e), dp);
+            for (int e = 0; e < D / 16; ++e) {
+                s = mma32(load8(k + mine + 16 * e), load8(q + 8 * h2 + 16 * e), s);
+                dp = mma32(load8(v + mine + 16 * e), load8(go + 8 * h2 + 16 * e), dp);
+            }
+            uint32_t seen = 0;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                if (mask.sees(pos, keys.key(x0 + row32(r, h2)))) seen |= 1u << r;
+                dp[r] = ex2(fmaf(s[r], c, -lse2)) * (dp[r] - delta);
+            }
+            mma32_seen<T>(dq, [&](int r) { return k + row(r) + 32 * t; }, dp, seen, lane);
         }
-        s += other_half(s);
-        dp += other_half(dp);
-        if (!mask.sees(pos, j)) continue;
-        const float ds = ex2(fmaf(s, c, -lse2)) * (dp - delta);
-#pragma unroll 1
-        for (int e = 0; e < N; ++e) dq[e] = fmaf(ds, Elem<T>::load(k + j * stride + N * h2 + e), dq[e]);
+        put(t, dq);
     }
-    if (!live) return;
-#pragma unroll 1
-    for (int e = 0; e < N; ++e) Elem<T>::store(gq + N * h2 + e, dq[e] * a.scale);
 }
 
 template <typename T, int D, bool SPLIT> struct DqCfg {
@@ -502,19 +527,17 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(T) == 2 ? 2 : 1) void dq_kernel
     for (int t = 0; t < DT; ++t)
 #pragma unroll
         for (int r = 0; r < 16; ++r) bad |= dq[t][r] != dq[t][r];
-    if (__any(bad && live)) {
-        exact_dq<T, D>(a, mask, pos, live, wp1, lse2, delta, q + qrow * D, go + qrow * D, kbase, vbase, kstride,
-                       gq + qrow * D, h2);
-        return;
-    }
-    if (!live) return;
-#pragma unroll
-    for (int t = 0; t < DT; ++t) {
-        const f32x16 g = dq[t] * a.scale;
+    auto put = [&](int t, const f32x16& x) {
+        const f32x16 g = x * a.scale;
+        if (!live) return;
 #pragma unroll
         for (int r = 0; r < 16; r += 4)
             store4<T>(gq + qrow * D + 32 * t + row32(r, h2), g[r], g[r + 1], g[r + 2], g[r + 3]);
-    }
+    };
+#pragma unroll
+    for (int t = 0; t < DT; ++t) put(t, dq[t]);
+    if (__builtin_expect(__ballot(bad && live) != 0, 0))
+        seen_dq<T, D>(a, mask, pos, wp0, wp1, lse2, delta, q + qrow * D, go + qrow * D, kbase, vbase, kstride, lane, put);
 }
 
 BwdArgs make_args(bool f32, int B, int Tq, int Tk, int Hq, int Hkv, int window, int sinks, float scale) {

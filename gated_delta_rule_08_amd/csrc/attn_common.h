@@ -29,8 +29,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 template <typename T> struct Frag;
-template <> struct Frag<bf16_t> { typedef bf16x8v type; };
-template <> struct Frag<float> { typedef f32x8 type; };
+template <> struct Frag<bf16_t> { typedef bf16x8v type; typedef __bf16 elem; };
+template <> struct Frag<float> { typedef f32x8 type; typedef float elem; };
 template <typename T> using frag_t = typename Frag<T>::type;
 
 __device__ __forceinline__ f32x16 zero16() {
@@ -81,7 +81,7 @@ __device__ __forceinline__ f32x8 load8(const float* p) {
 
 // fp32 values as an operand fragment (bf16: rounded to nearest even; a
 // probability or a score gradient then carries a relative error of at most
-// 2^-9, the size of the rounding of the inputs and of the output).
+// 2^-8, the size of the rounding of the inputs and of the output).
 template <typename T> __device__ __forceinline__ frag_t<T> pack8(const float (&x)[8]);
 template <> __device__ __forceinline__ bf16x8v pack8<bf16_t>(const float (&x)[8]) {
     bf16x8v r;
@@ -133,6 +133,50 @@ struct FastDiv {
         return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(n)) * mul) >> shift);
     }
 };
+
+// acc += A B over 32 elements as two mma32 would, summing the pairs whose bit in
+// `seen` is set and no others: a hidden pair's weight is 0, but 0 times an
+// infinity or NaN would be NaN.  B: the lane's 16 weights w (an accumulator
+// tile); A: column lane % 32 of the rows row(0) .. row(31), in global memory.
+// Infinities and NaN of A are counted, by products of their signs with those of
+// the weights, and added afterwards as the sum over the visible pairs has them.
+template <typename T, typename F>
+__device__ __forceinline__ void mma32_seen(f32x16& acc, F row, const f32x16& w, uint32_t seen, int lane) {
+    typedef typename Frag<T>::elem elem;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        __builtin_amdgcn_sched_barrier(0);  // one half's registers at a time
+        frag_t<T> fin, sign, mag, nan;
+        float wv[8], ws[8], wm[8], w0[8], vis[8];
+        bool odd = false;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const elem a = __builtin_bit_cast(elem, row(16 * x + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3))[lane & 31]);
+            const float af = static_cast<float>(a);
+            const bool see = (seen >> (8 * x + i)) & 1, is_nan = af != af, is_inf = fabsf(af) == INFINITY;
+            const float s = is_inf ? (af > 0.f ? 1.f : -1.f) : 0.f;
+            odd |= is_nan || is_inf;
+            fin[i] = is_nan || is_inf ? static_cast<elem>(s) : a;
+            sign[i] = static_cast<elem>(s);
+            mag[i] = static_cast<elem>(fabsf(s));
+            nan[i] = static_cast<elem>(is_nan ? 1.f : 0.f);
+            wv[i] = see ? w[8 * x + i] : 0.f;
+            ws[i] = wv[i] > 0.f ? 1.f : wv[i] < 0.f ? -1.f : 0.f;
+            wm[i] = fabsf(ws[i]);
+            vis[i] = see ? 1.f : 0.f;
+            w0[i] = see && wv[i] == 0.f ? 1.f : 0.f;
+        }
+        acc = mma32(fin, pack8<T>(wv), acc);
+        if (!__any(odd)) continue;
+        const f32x16 z1 = mma32(sign, pack8<T>(ws), zero16()), z2 = mma32(mag, pack8<T>(wm), zero16());
+        const f32x16 z3 = mma32(mag, pack8<T>(w0), mma32(nan, pack8<T>(vis), zero16()));
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            if (z2[r] > 0.f) acc[r] += z1[r] == z2[r] ? INFINITY : z1[r] == -z2[r] ? -INFINITY : NAN;
+            if (z3[r] > 0.f) acc[r] = NAN;
+        }
+    }
+}
 
 // x of the lane 32 away.
 __device__ __forceinline__ float other_half(float x) { return __shfl_xor(x, 32); }

@@ -42,45 +42,48 @@ template <typename T, int D, bool SPLIT> struct PrefillCfg {
     static constexpr int kLds = 2 * kBufs * kTileBytes;  // K and V
 };
 
-// The rows of one wave key by key, hidden keys left out: what a wave does when
-// a non-finite value meets its sums.  A lane holds half of its row's channels.
-template <typename T, int D>
-__device__ __forceinline__ void exact_rows(Mask mask, int pos, bool live, int wp0, int wp1, float c, bool neg,
-                                        const T* q, const T* k, const T* v, size_t stride, T* o, float* lse,
-                                        int h2) {
-    constexpr int N = D / 2;
-    float acc[N];
-#pragma unroll
-    for (int e = 0; e < N; ++e) acc[e] = 0.f;
-    q += N * h2;
-    k += N * h2;
-    v += N * h2;
-    const float cs = neg ? -c : c;
-    float m = -INFINITY, l = 0.f;
-    const int w_lo = mask.window ? max(0, wp0 - mask.window + 1) : 0;
+// The rows of one wave once more with hidden keys left out of every sum: what a
+// wave does when a non-finite value has met its sums.  Operands straight from
+// global memory, 32 keys and 32 channels at a time, no other wave involved;
+// put(t, sums, m, l) takes channels 32 t .. 32 t + 31.
+template <typename T, int D, typename P>
+__device__ __forceinline__ void seen_rows(Mask mask, int pos, int wp0, int wp1, int Tk, float c, bool neg, const T* q,
+                                          const T* k, const T* v, size_t stride, int lane, P put) {
+    const int h2 = lane >> 5;
+    const KeyList keys(mask.window, mask.sinks, wp0, wp1);
 #pragma unroll 1
-    for (int j = 0; j <= wp1; ++j) {
-        if (j == min(mask.sinks, w_lo)) j = w_lo;  // between the sinks and the window
-        float s = 0.f;
+    for (int t = 0; t < D / 32; ++t) {
+        f32x16 acc = zero16();
+        float m = -INFINITY, l = 0.f;
 #pragma unroll 1
-        for (int e = 0; e < N; e += 4)
+        for (int x0 = 0; x0 < keys.count; x0 += 32) {
+            auto row = [&](int r) { return static_cast<size_t>(min(keys.key(x0 + r), Tk - 1)) * stride; };
+            const T *kr = k + row(lane & 31) + 8 * h2, *qr = q + 8 * h2;
+            f32x16 s = zero16();
+#pragma unroll 1
+            for (int e = 0; e < D / 16; ++e) s = mma32(load8(kr + 16 * e), neg ? -load8(qr + 16 * e) : load8(qr + 16 * e), s);
+            uint32_t seen = 0;
+            float mx = m;
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-                s = fmaf(Elem<T>::load(q + e + x), Elem<T>::load(k + static_cast<size_t>(j) * stride + e + x), s);
-        s = (s + other_half(s)) * cs;
-        if (!mask.sees(pos, j)) continue;
-        const float mx = s > m || s != s ? s : m, mc = mx == -INFINITY ? 0.f : mx;
-        const float alpha = m == -INFINITY ? 0.f : ex2(m - mc), p = ex2(s - mc);
-        m = mx;
-        l = l * alpha + p;
+            for (int r = 0; r < 16; ++r)
+                if (mask.sees(pos, keys.key(x0 + row32(r, h2)))) {
+                    seen |= 1u << r;
+                    mx = fmaxf(mx, s[r]);
+                }
+            mx = fmaxf(mx, other_half(mx));
+            const float mc = mx == -INFINITY ? 0.f : mx * c, alpha = m == -INFINITY ? 0.f : ex2(m * c - mc);
+            m = mx;
+            l *= alpha;
+            acc *= alpha;
 #pragma unroll
-        for (int e = 0; e < N; ++e) acc[e] = fmaf(p, Elem<T>::load(v + static_cast<size_t>(j) * stride + e), acc[e] * alpha);
+            for (int r = 0; r < 16; ++r) {
+                s[r] = (seen >> r) & 1 ? ex2(fmaf(s[r], c, -mc)) : 0.f;
+                l += s[r];
+            }
+            mma32_seen<T>(acc, [&](int r) { return v + row(r) + 32 * t; }, s, seen, lane);
+        }
+        put(t, acc, m, l + other_half(l));
     }
-    if (!live) return;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-    for (int e = 0; e < N; ++e) Elem<T>::store(o + N * h2 + e, acc[e] * inv);
-    if (lse && h2 == 0) *lse = l == 0.f ? -INFINITY : (m + lg2(l)) * kLn2;
 }
 
 // 32 rows per wave, or with SPLIT 32 rows per workgroup, each wave taking a
@@ -284,22 +287,18 @@ __global__ __launch_bounds__(64 * kWaves, (PrefillCfg<T, D, SPLIT>::kBufs)) void
     for (int t = 0; t < DT; ++t)
 #pragma unroll
         for (int r = 0; r < 16; ++r) bad |= acc[t][r] != acc[t][r];
-    if (__any(bad && live)) {
-        exact_rows<T, D>(mask, pos, live, wp0, wp1, c, a.scale < 0.f, q + qrow * D, kbase, vbase, kstride, o + qrow * D,
-                         lse ? lse + qrow : nullptr, h2);
-        return;
-    }
-    const float inv = l > 0.f ? 1.f / l : 0.f;  // no visible key: zeros
-    if (live) {
-        T* op = o + qrow * D;
+    auto put = [&](int t, const f32x16& x, float m, float l) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;  // no visible key: zeros
+        if (!live) return;
 #pragma unroll
-        for (int t = 0; t < DT; ++t)
+        for (int r = 0; r < 16; r += 4)
+            store4<T>(o + qrow * D + 32 * t + row32(r, h2), x[r] * inv, x[r + 1] * inv, x[r + 2] * inv, x[r + 3] * inv);
+        if (t == 0 && lse && h2 == 0) lse[qrow] = l == 0.f ? -INFINITY : (m * c + lg2(l)) * kLn2;
+    };
 #pragma unroll
-            for (int r = 0; r < 16; r += 4)
-                store4<T>(op + 32 * t + row32(r, h2), acc[t][r] * inv, acc[t][r + 1] * inv,
-                          acc[t][r + 2] * inv, acc[t][r + 3] * inv);
-        if (lse && h2 == 0) lse[qrow] = l > 0.f ? (m * c + lg2(l)) * kLn2 : -INFINITY;
-    }
+    for (int t = 0; t < DT; ++t) put(t, acc[t], m, l);
+    if (__builtin_expect(__ballot(bad && live) != 0, 0))
+        seen_rows<T, D>(mask, pos, wp0, wp1, Tk, c, a.scale < 0.f, q + qrow * D, kbase, vbase, kstride, lane, put);
 }
 
 template <typename T, int D, bool SPLIT>

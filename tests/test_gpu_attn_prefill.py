@@ -1,11 +1,12 @@
 """Windowed attention prefill (dense and packed) and its backward against the float64 definition."""
 import itertools
+import math
 
 import pytest
 import torch
 
 import gated_delta_rule_08_amd as gdr
-from attn_ref import attend, check
+from attn_ref import attend, check, visible
 from gpu_util import announce, ensure_built
 
 pytestmark = pytest.mark.gpu
@@ -206,6 +207,46 @@ def test_non_finite_values_stay_with_the_rows_that_see_them(dt, what, B, d):
         check(name, got[0, hidden], ref[name][0][hidden], ref[name][1][hidden])
         check(name, got[0, :, :1], ref[name][0][:, :1], ref[name][1][:, :1])
     check("grad_q", dq[0][~mine], ref["grad_q"][0][~mine], ref["grad_q"][1][~mine])
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("B,d", [(1, 64), (140, 128)])
+def test_single_non_finite_elements(dt, B, d):
+    """Infinities of both signs and NaN in single elements of v and grad_o: every sum over visible pairs has the value
+    float64 gives it, element by element (an infinity, a NaN, or a number within its bound)."""
+    announce("attn single non-finite elements %s %d %d" % (dt, B, d))
+    T, window, sinks, scale = 150, 30, 2, 0.125
+    x = [make(i, dt, B, T, 1, d) for i in range(4)]
+    q, k, v, go = x
+    clean = [t[0, :, 0].double() for t in x]
+    spots = [(1, 3, "inf"), (70, 4, "inf"), (75, 4, "-inf"), (75, 5, "nan"), (90, 6, "-inf"), (149, 7, "nan"), (20, 8, "inf")]
+    bad = v.clone()
+    for j, ch, what in spots:
+        bad[:, j, 0, ch] = float(what)
+
+    def sums(see, w, t):  # sum over the visible pairs of w_ij t_j, hidden ones left out
+        return torch.stack([(w[i][see[i]].unsqueeze(-1) * t[see[i]]).sum(0) for i in range(see.shape[0])])
+
+    def compare(name, got, ref, bound):
+        got, ref = got[:, 0].double().cpu(), ref
+        odd = ~torch.isfinite(ref)
+        assert torch.equal(torch.isnan(got), torch.isnan(ref)) and torch.equal(got[torch.isinf(ref)], ref[torch.isinf(ref)]), name
+        assert ((got - ref).masked_fill(odd, 0).abs() <= bound.masked_fill(odd, 1)).all(), name
+
+    see = visible(T, T, window, sinks)
+    ref = attend(q[0], k[0], v[0], window, sinks, scale, DT[dt], go[0])
+    p = torch.softmax((clean[0] @ clean[1].t() * scale).masked_fill(~see, -math.inf), -1)
+    o0, lse = forward(q, k, v, window, sinks, scale)
+    o, lse1 = forward(q, k, bad, window, sinks, scale)
+    check("lse", lse1[0], *ref["lse"])
+    # a sum that has lost no terms has the clean sum's bound; the other channels are the clean ones
+    compare("o", o[0], sums(see, p, bad[0, :, 0].double()), ref["o"][1][:, 0])
+    badg = go.clone()
+    for j, ch, what in spots:
+        badg[:, j, 0, ch] = float(what)
+    dq, dk, dv = (torch.empty_like(t).cuda() for t in (q, k, v))
+    gdr.gdr_attn_backward(q.cuda(), k.cuda(), v.cuda(), o0, lse, badg.cuda(), dq, dk, dv, window=window, sinks=sinks, scale=scale)
+    compare("grad_v", dv[0], sums(see.t(), p.t(), badg[0, :, 0].double()), ref["grad_v"][1][:, 0])
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
