@@ -530,7 +530,7 @@ def _attn_types(q, *ts) -> int:
 
 
 def _attn_heads(Hq: int, Hkv: int) -> None:
-    if Hq % Hkv if Hkv else Hq:
+    if Hq % Hkv if Hkv and Hq else Hq != Hkv:
         raise ValueError("the query heads must be a multiple of the key heads")
 
 

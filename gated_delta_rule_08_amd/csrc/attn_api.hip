@@ -21,7 +21,7 @@ int common_checks(int dtype, int Hq, int Hkv, int d, int window, int sinks) {
     if (dtype != GDR_DTYPE_F32 && dtype != GDR_DTYPE_BF16) return GDR_ERR_BAD_ENUM;
     if (Hq < 0 || Hkv < 0 || window < 0 || sinks < 0) return GDR_ERR_BAD_SHAPE;
     if (d != 64 && d != 128) return GDR_ERR_UNSUPPORTED;
-    if (Hkv == 0 ? Hq != 0 : Hq % Hkv != 0) return GDR_ERR_BAD_SHAPE;
+    if (Hkv == 0 || Hq == 0 ? Hq != Hkv : Hq % Hkv != 0) return GDR_ERR_BAD_SHAPE;
     return GDR_OK;
 }
 

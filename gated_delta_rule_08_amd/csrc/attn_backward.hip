@@ -38,12 +38,25 @@ struct BwdArgs {
     int rows, pitch;          // rows of a (sequence, key head); pitch of the row statistics
     int key_blocks, row_tiles;
     bool split;               // dq: 32 rows per workgroup, a quarter of the keys per wave
-    int slices, slice_rows;   // rows of a key block in one workgroup, and how many that makes (at most)
-    int sink_tiles, segs;     // 32-key tiles that hold sinks, segments of each (at most; 0 with slices > 1)
+    bool sliced;              // key blocks cut their lists of rows, slice_rows to a workgroup,
+    int slice_rows;
+    int long_blocks;          // the first (those with sinks under a window) into at most long_slices,
+    int long_slices, slices;  // the others into at most slices
+    int sink_tiles, segs;     // not sliced: 32-key tiles that hold sinks, segments of each (at most)
     int seg_rows;
-    int part_tiles, slots;    // key tiles whose gradients come in parts, parts of each (at most)
+    // Key tiles whose gradients come in parts: the first long_tiles have room for
+    // long_slots parts each, the others for slots.
+    int part_tiles, long_tiles, long_slots, slots;
     float* stats;             // [B Hkv, 2, pitch]: lse log2 e, then delta
-    float* part;              // [B Hkv, part_tiles, slots, 2, 32, d]
+    float* part;              // [B Hkv, parts of a head, 2, 32, d]
+    __host__ __device__ __forceinline__ int cuts() const { return long_blocks * long_slices + (key_blocks - long_blocks) * slices; }
+    __host__ __device__ __forceinline__ size_t parts_before(int tile) const {  // within a head
+        return static_cast<size_t>(tile < long_tiles ? tile : long_tiles) * long_slots +
+               static_cast<size_t>(tile < long_tiles ? 0 : tile - long_tiles) * slots;
+    }
+    __device__ __forceinline__ float* part_of(int head, int tile, int slot, int d) const {
+        return part + (static_cast<size_t>(head) * parts_before(part_tiles) + parts_before(tile) + slot) * 64 * d;
+    }
 };
 
 // Rows (query * G + head) that see keys [j0, j1] through the window or, with
@@ -54,7 +67,7 @@ __host__ __device__ __forceinline__ void rows_of(const BwdArgs& a, int j0, int j
     int last = a.Tq - 1;
     if (a.window && j1 + a.window - 1 - off < last) last = j1 + a.window - 1 - off;
     hi = (last + 1) * a.G.d > lo ? (last + 1) * a.G.d : lo;
-    if (a.slices > 1 && a.window && j0 < a.sinks) hi = a.rows;  // no segments: the sinks' rows are sliced with the rest
+    if (a.sliced && a.window && j0 < a.sinks) hi = a.rows;  // no segments: the sinks' rows are sliced with the rest
 }
 
 template <typename T, int D, int WAVES> struct DkdvCfg {
@@ -75,14 +88,17 @@ struct Piece {
 };
 template <int WAVES> __device__ __forceinline__ Piece piece_of(const BwdArgs& a, int bid, int wave) {
     constexpr bool kSeg = WAVES == 1;
-    const int per = kSeg ? a.sink_tiles * a.segs : a.key_blocks * a.slices;
+    const int per = kSeg ? a.sink_tiles * a.segs : a.cuts();
     int head, x, lo, hi;
     place(bid, a.B * a.Hkv, per, head, x);  // the first keys are seen by the most rows
-    const int b = head / a.Hkv, cuts = kSeg ? a.segs : a.slices, y = x / cuts, cut = x - y * cuts;
+    const int first = kSeg ? 0 : a.long_blocks * a.long_slices;  // pieces of the long blocks
+    const bool in = x < first;
+    const int b = head / a.Hkv, cuts = kSeg ? a.segs : in ? a.long_slices : a.slices, z = in ? x : x - first;
+    const int z0 = z / cuts, cut = z - z0 * cuts, y = kSeg || in ? z0 : a.long_blocks + z0;
     const int tile = kSeg ? y : y * WAVES + wave;
     const int m0 = kSeg ? 32 * tile / kKeys * kKeys : y * kKeys;  // the keys of a main workgroup
     rows_of(a, m0, min(m0 + kKeys, a.Tk) - 1, lo, hi);
-    const bool parts = kSeg || hi - lo > a.slice_rows;
+    const bool parts = kSeg || (a.sliced && hi - lo > a.slice_rows);
     lo = kSeg ? hi + cut * a.seg_rows : lo + cut * a.slice_rows;  // a segment's are past what the main workgroup takes
     hi = kSeg ? min(a.rows, lo + a.seg_rows) : min(hi, lo + a.slice_rows);
     return {head, b, head - b * a.Hkv, tile, 32 * tile, cut, lo, hi, parts};
@@ -316,8 +332,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && WAVES == 4 ? 2 : 1) v
     const size_t at = ((static_cast<size_t>(to.b) * a.Tk + me) * a.Hkv + to.hk) * D;
     float* part = nullptr;
     if (to.parts || to.tile < a.sink_tiles)
-        part = a.part + (((static_cast<size_t>(to.head) * a.part_tiles + to.tile) * a.slots + (kSeg ? 1 + to.cut : to.cut)) * 64 +
-                         (me & 31)) * D;
+        part = a.part_of(to.head, to.tile, kSeg ? 1 + to.cut : to.cut, D) + (me & 31) * D;
     const bool store = part ? !kSeg || me < a.sinks : me < a.Tk;  // a segment's other keys are not read by the join
     if (store) {
 #pragma unroll
@@ -342,12 +357,12 @@ __global__ __launch_bounds__(256) void join_kernel(BwdArgs a, T* __restrict__ gk
     const int m0 = 32 * tile / kKeys * kKeys;
     int lo, end, parts = 1;
     rows_of(a, m0, min(m0 + kKeys, a.Tk) - 1, lo, end);
-    if (a.slices > 1) {
+    if (a.sliced) {
         if (end - lo <= a.slice_rows) return;  // written whole
         parts = (end - lo - 1) / a.slice_rows + 1;
     }
     const int segs = a.segs && a.rows > end ? (a.rows - end - 1) / a.seg_rows + 1 : 0;
-    const float* part = a.part + (static_cast<size_t>(head) * a.part_tiles + tile) * a.slots * 64 * D;
+    const float* part = a.part_of(head, tile, 0, D);
     const int x = threadIdx.x & 31, first = threadIdx.x >> 5;
     const int i = blockIdx.y * 32 + x, row = i / (D / 4), ch = 4 * (i % (D / 4)), key = 32 * tile + (row & 31);
     if (key < a.sinks) parts += segs;  // the others have none
@@ -562,42 +577,47 @@ BwdArgs make_args(bool f32, int B, int Tq, int Tk, int Hq, int Hkv, int window, 
     // the first block's list much longer than the others'.  Slices of a 384th of
     // all rows, 64 at least (training step T=4096, 32 query on 8 key heads: 1023
     // us unsliced, 748 with a 256th, 708, 724 with a 768th, 765 with a 1024th).
-    a.slices = 1;
-    a.slice_rows = a.rows > 0 ? a.rows : 1;
+    a.slices = a.long_slices = 1;
+    a.slice_rows = a.rows;
+    const int tiles = (Tk + 31) / 32;
     if (groups > 0 && groups < 512 && a.rows > 0) {
-        long long total = 0, longest = 0;
-        for (int j = 0; j < a.key_blocks; ++j) {
+        auto list = [&](int j) {
             int lo, hi;
             rows_of(a, j * kKeys, (j + 1) * kKeys < Tk ? (j + 1) * kKeys - 1 : Tk - 1, lo, hi);
-            total += hi - lo;
-            if (hi - lo > longest) longest = hi - lo;
+            return static_cast<long long>(hi - lo);
+        };
+        long long total = 0, longest = 0;
+        for (int j = 0; j < a.key_blocks; ++j) {
+            total += list(j);
+            longest = list(j) > longest ? list(j) : longest;
         }
         if (groups < 256 || 2 * longest * a.key_blocks > 3 * total) {
             const long long even = (total * heads / 384 + 31) / 32 * 32;
             a.slice_rows = static_cast<int>(even < 64 ? 64 : even < a.rows ? even : a.rows);
-            a.slices = 2;  // several: the sinks' rows are sliced with the rest
-            longest = 0;
+            a.sliced = true;
+            if (window) a.long_blocks = (sinks + kKeys - 1) / kKeys;
+            long long most[2] = {1, 1};
             for (int j = 0; j < a.key_blocks; ++j) {
-                int lo, hi;
-                rows_of(a, j * kKeys, (j + 1) * kKeys < Tk ? (j + 1) * kKeys - 1 : Tk - 1, lo, hi);
-                if (hi - lo > longest) longest = hi - lo;
+                const long long cuts = (list(j) + a.slice_rows - 1) / a.slice_rows;
+                if (cuts > most[j < a.long_blocks]) most[j < a.long_blocks] = cuts;
             }
-            a.slices = static_cast<int>((longest + a.slice_rows - 1) / a.slice_rows);
-            if (a.slices <= 1) {
-                a.slices = 1;
-                a.slice_rows = a.rows;
-            }
+            a.slices = static_cast<int>(most[0]);
+            a.long_slices = static_cast<int>(most[1]);
+            a.slots = a.slices > 1 ? a.slices : 0;
+            a.long_slots = a.long_slices > 1 ? a.long_slices : 0;
+            a.long_tiles = 4 * a.long_blocks < tiles ? 4 * a.long_blocks : tiles;
+            a.part_tiles = a.slots ? tiles : a.long_slots ? a.long_tiles : 0;
         }
     }
     // Sink segments: one wave per SIMD, no segment under 128 rows.
-    if (a.slices == 1 && window && Tq > 0) a.sink_tiles = (sinks + 31) / 32;
+    if (!a.sliced && window && Tq > 0) a.sink_tiles = (sinks + 31) / 32;
     if (a.sink_tiles) {
         const long long even = heads * a.sink_tiles * a.rows / 1024;
         a.seg_rows = static_cast<int>(even < 128 ? 128 : even > a.rows ? a.rows : (even + 31) / 32 * 32);
         a.segs = (a.rows + a.seg_rows - 1) / a.seg_rows;
+        a.part_tiles = a.long_tiles = a.sink_tiles;
+        a.long_slots = 1 + a.segs;
     }
-    a.part_tiles = a.slices > 1 ? (Tk + 31) / 32 : a.sink_tiles;
-    a.slots = a.slices + a.segs;
     return a;
 }
 
@@ -612,7 +632,7 @@ hipError_t launch(const BwdArgs& a, const void* q_, const void* k_, const void* 
     const T *q = static_cast<const T*>(q_), *k = static_cast<const T*>(k_), *v = static_cast<const T*>(v_),
             *o = static_cast<const T*>(o_), *go = static_cast<const T*>(go_);
     const unsigned long long heads = static_cast<unsigned long long>(a.B) * a.Hkv;
-    const unsigned long long kv_blocks = heads * a.key_blocks * a.slices, q_blocks = heads * a.row_tiles;
+    const unsigned long long kv_blocks = heads * a.cuts(), q_blocks = heads * a.row_tiles;
     const unsigned long long seg_blocks = heads * a.sink_tiles * a.segs, join_blocks = heads * a.part_tiles;
     if (!grid_fits(kv_blocks, 64 * kWaves) || !grid_fits(q_blocks, 64 * kWaves) ||
         !grid_fits(seg_blocks, 64) || !grid_fits(join_blocks * (D / 2), 256))
@@ -645,7 +665,7 @@ hipError_t launch(const BwdArgs& a, const void* q_, const void* k_, const void* 
 size_t attn_backward_workspace_floats(int dtype, int B, int Tq, int Tk, int Hq, int Hkv, int d, int window, int sinks) {
     const attn::BwdArgs a = attn::make_args(dtype == GDR_DTYPE_F32, B, Tq, Tk, Hq, Hkv, window, sinks, 1.f);
     const size_t heads = static_cast<size_t>(B) * Hkv;
-    return heads * (2 * static_cast<size_t>(a.pitch) + static_cast<size_t>(a.part_tiles) * a.slots * 64 * d);
+    return heads * (2 * static_cast<size_t>(a.pitch) + a.parts_before(a.part_tiles) * 64 * d);
 }
 
 hipError_t launch_attn_backward(int dtype, int B, int Tq, int Tk, int Hq, int Hkv, int d, int window, int sinks,

@@ -551,10 +551,10 @@ hipError_t launch_decode_t(const DecodeArgs& a, const void* q, const void* k, co
     const unsigned long long blocks =
         a.shares ? a.shares : static_cast<unsigned long long>(a.B) * a.Hkv * a.head_tiles;
     const unsigned long long rows = static_cast<unsigned long long>(a.B) * a.Hq;
-    // a share's blocks have to fit an int
-    if (a.shares && static_cast<unsigned long long>(a.B) * a.Hkv * a.head_tiles *
-                            ((static_cast<unsigned long long>(a.max_pages) << a.page_shift) / kBlock + 1) / a.shares >
-                        0x7fffffffull)
+    // a share's blocks have to fit an int, and so have those of one scan's sequences
+    const unsigned long long most = (static_cast<unsigned long long>(a.max_pages) << a.page_shift) / kBlock + 1;
+    if (a.shares && (static_cast<unsigned long long>(a.B) * a.Hkv * a.head_tiles * most / a.shares > 0x7fffffffull ||
+                     (a.B < 256 ? a.B : 256) * most > 0x7fffffffull))
         return hipErrorInvalidConfiguration;
     if (!grid_fits(blocks, 64 * kWaves) || !grid_fits(rows, 256)) return hipErrorInvalidConfiguration;
     auto* f = decode_kernel<T, D>;

@@ -389,8 +389,8 @@ size_t gdr_chunk_backward_workspace_bytes_ranged(int gate, int dtype, int B, int
  * A query that sees no key gets o = 0 and lse = -inf.  A hidden key has no
  * influence whatever its values (infinities and NaN included).
  *
- * Query heads: Hq a multiple of Hkv; query head h reads key head
- * h / (Hq / Hkv).  d in {64, 128} for keys and values alike.  With dtype BF16
+ * Query heads: Hq a multiple of Hkv, not 0 unless Hkv is; query head h reads
+ * key head h / (Hq / Hkv).  d in {64, 128} for keys and values alike.  With dtype BF16
  * the products run on bf16 matrix cores with fp32 accumulation and the
  * softmax weights (backward: and the score gradients) enter the second
  * product rounded to bf16; statistics and sums are fp32.  With dtype F32 every
@@ -469,7 +469,8 @@ size_t gdr_attn_backward_workspace_bytes(int dtype, int B, int Tq, int Tk, int H
  *   lengths          [B] int32, DEVICE: positions the cache holds before the
  *                    call; the caller advances them
  *
- * num_pages * Hkv * page_size must stay below 2^31 (rows of a page tensor).
+ * num_pages * Hkv * page_size must stay below 2^31 (rows of a page tensor), and
+ * so must max_pages * page_size (positions).
  */
 
 /*
@@ -508,8 +509,8 @@ size_t gdr_attn_decode_workspace_bytes(int dtype, int B, int Hq, int Hkv, int d,
  *               no sequence are ignored
  *   lengths, page_table, pages as above (N sequences)
  *
- * A token whose position is negative, beyond the table row or on a page
- * outside [0, num_pages) is not written.  Two tokens with the same place race.
+ * A token of a sequence with a negative length, or whose position is beyond the
+ * table row or on a page outside [0, num_pages), is not written.  Two tokens with the same place race.
  * Returns a GDR_* status.
  */
 int gdr_attn_append(int dtype, int N, int total, int Hkv, int d, int page_size, int num_pages, int max_pages,

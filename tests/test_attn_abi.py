@@ -39,7 +39,7 @@ def prefill(lib, dtype=1, B=1, Tq=8, Tk=8, Hq=4, Hkv=2, d=64, window=0, sinks=0,
 def test_prefill(lib):
     assert prefill(lib, dtype=2) == ENUM
     for kw in (dict(B=-1), dict(Tq=-1), dict(Tk=-1), dict(Hq=-1), dict(Hkv=-1), dict(window=-1), dict(sinks=-1),
-               dict(Hq=5), dict(Hkv=0), dict(Tq=BIG), dict(Tk=BIG), dict(Tq=1 << 28, Hq=32), dict(B=BIG, Hq=64, Hkv=64),
+               dict(Hq=5), dict(Hkv=0), dict(Hq=0), dict(Tq=BIG), dict(Tk=BIG), dict(Tq=1 << 28, Hq=32), dict(B=BIG, Hq=64, Hkv=64),
                dict(B=1 << 20, Tq=1 << 20), dict(Hq=1 << 16, Hkv=1 << 16), dict(Tq=1 << 27), dict(Tk=1 << 28)):
         assert prefill(lib, **kw) == SHAPE, kw
     for d in (0, 16, 63, 96, 256, -64):
@@ -48,7 +48,7 @@ def test_prefill(lib):
         assert prefill(lib, ptrs=swap(P[:5], i, None)) == NULL
         assert prefill(lib, ptrs=swap(P[:5], i, off(P[i], 8))) == MISAL
     assert prefill(lib, ptrs=swap(P[:5], 4, off(P[4], 2))) == MISAL
-    for kw in (dict(B=0), dict(Tq=0), dict(Hq=0, Hkv=0), dict(Hq=0)):
+    for kw in (dict(B=0), dict(Tq=0), dict(Hq=0, Hkv=0)):
         assert prefill(lib, ptrs=[None] * 5, **kw) == OK
     assert prefill(lib, Tk=0, ptrs=[P[0], None, None, None, None]) == NULL  # o
     # more workgroups than one launch can have
@@ -66,7 +66,7 @@ def test_prefill_varlen(lib):
     for i in range(6):
         assert call(ptrs=swap(P[:7], i, None)) == NULL
         assert call(ptrs=swap(P[:7], i, off(P[i], 2))) == MISAL
-    for kw in (dict(N=0), dict(tq=0), dict(mq=0), dict(Hq=0)):
+    for kw in (dict(N=0), dict(tq=0), dict(mq=0), dict(Hq=0, Hkv=0)):
         assert call(ptrs=[None] * 7, **kw) == OK
 
 
@@ -85,8 +85,14 @@ def test_backward(lib):
     assert call(ws=off(P[9], 8)) == MISAL
     need = size(1, 1, 8, 8, 4, 2, 64, 0, 0)
     assert need > 0 and call(ws=None) == WS and call(n=need - 1) == WS
-    for kw in (dict(B=0), dict(Hq=0), dict(Hq=0, Hkv=0), dict(Tq=0, Tk=0)):
+    for kw in (dict(B=0), dict(Hq=0, Hkv=0), dict(Tq=0, Tk=0)):
         assert call(ptrs=[None] * 9, ws=None, n=0, **kw) == OK
+    # key heads without query heads would leave their gradients unwritten
+    assert call(Hq=0) == SHAPE
+    # few key blocks, long lists of rows for the sinks' keys: room for those, not for every key
+    for T, heads in ((60000, 1), (16384, 2), (65536, 4), (4096, 1)):
+        for sinks in (1, 4, 200):
+            assert size(1, 1, T, T, heads, heads, 128, 64, sinks) < 400 << 20, (T, heads, sinks)
     # sinks under a window need room for their partial sums; without a window they hide nothing
     assert size(1, 1, 65536, 65536, 4, 2, 64, 128, 4) > size(1, 1, 65536, 65536, 4, 2, 64, 128, 0)
     assert size(1, 1, 65536, 65536, 4, 2, 64, 0, 4) == size(1, 1, 65536, 65536, 4, 2, 64, 0, 0)
@@ -103,7 +109,7 @@ def test_decode(lib):
     size = lib.gdr_attn_decode_workspace_bytes
     assert call(dtype=3) == ENUM
     for kw in (dict(B=-1), dict(Hq=-4), dict(Hq=5), dict(pages=-1), dict(width=-1), dict(window=-1), dict(sinks=-1),
-               dict(B=BIG), dict(width=1 << 28), dict(pages=1 << 27), dict(pages=1 << 26, page=16, Hkv=4)):
+               dict(B=BIG), dict(width=1 << 28), dict(B=256, width=(1 << 27) - 1024), dict(pages=1 << 27), dict(pages=1 << 26, page=16, Hkv=4)):
         assert call(**kw) == SHAPE, kw
     assert call(d=192) == UNSUP
     for page in (0, -16, 3, 24, 1 << 17):
@@ -111,7 +117,7 @@ def test_decode(lib):
     for i in range(8):
         assert call(ptrs=swap(P[:8], i, None)) == NULL
         assert call(ptrs=swap(P[:8], i, off(P[i], 2))) == MISAL
-    for kw in (dict(B=0), dict(Hq=0), dict(Hq=0, Hkv=0), dict(pages=0), dict(width=0)):
+    for kw in (dict(B=0), dict(Hq=0, Hkv=0), dict(pages=0), dict(width=0)):
         assert call(ptrs=[None] * 8, **kw) == OK
     need = size(1, 1, 8, 2, 128, 16, 1024, 0, 0)
     assert need > 0 and size(1, 1, 8, 2, 128, 16, 1024, 64, 0) < need  # a window bounds the parts
