@@ -79,6 +79,14 @@ template <typename T, int D, int WAVES> struct DkdvCfg {
     static constexpr int kLds = kStat + 2 * kStatBuf;
 };
 
+// Rows of a slice of a list: as few slices of at most slice_rows as there can
+// be, about equally long.
+__device__ __forceinline__ int slice_of(const BwdArgs& a, int list) {
+    if (!a.sliced || list <= a.slice_rows) return list;
+    const int n = (list - 1) / a.slice_rows + 1;
+    return ((list - 1) / n + 32) / 32 * 32;
+}
+
 // What one wave of dkdv_kernel has to do.
 struct Piece {
     int head, b, hk;
@@ -91,16 +99,21 @@ template <int WAVES> __device__ __forceinline__ Piece piece_of(const BwdArgs& a,
     const int per = kSeg ? a.sink_tiles * a.segs : a.cuts();
     int head, x, lo, hi;
     place(bid, a.B * a.Hkv, per, head, x);  // the first keys are seen by the most rows
-    const int first = kSeg ? 0 : a.long_blocks * a.long_slices;  // pieces of the long blocks
-    const bool in = x < first;
-    const int b = head / a.Hkv, cuts = kSeg ? a.segs : in ? a.long_slices : a.slices, z = in ? x : x - first;
-    const int z0 = z / cuts, cut = z - z0 * cuts, y = kSeg || in ? z0 : a.long_blocks + z0;
+    // The last slice of every block that has so many, then the last but one: blocks
+    // with short lists come at the end, and slices that do not exist are spread over
+    // the XCDs.
+    const int first = a.long_blocks * a.long_slices;  // pieces of the long blocks
+    const bool in = !kSeg && x < first;
+    const int b = head / a.Hkv, blocks = kSeg ? a.sink_tiles : in ? a.long_blocks : a.key_blocks - a.long_blocks;
+    const int z = kSeg || in ? x : x - first, turn = z / blocks, y = z - turn * blocks + (kSeg || in ? 0 : a.long_blocks);
+    const int cut = (kSeg ? a.segs : in ? a.long_slices : a.slices) - 1 - turn;
     const int tile = kSeg ? y : y * WAVES + wave;
     const int m0 = kSeg ? 32 * tile / kKeys * kKeys : y * kKeys;  // the keys of a main workgroup
     rows_of(a, m0, min(m0 + kKeys, a.Tk) - 1, lo, hi);
-    const bool parts = kSeg || (a.sliced && hi - lo > a.slice_rows);
-    lo = kSeg ? hi + cut * a.seg_rows : lo + cut * a.slice_rows;  // a segment's are past what the main workgroup takes
-    hi = kSeg ? min(a.rows, lo + a.seg_rows) : min(hi, lo + a.slice_rows);
+    const int size = kSeg ? a.seg_rows : slice_of(a, hi - lo);
+    const bool parts = kSeg || hi - lo > size;
+    lo = kSeg ? hi + cut * size : lo + cut * size;  // a segment's are past what the main workgroup takes
+    hi = min(kSeg ? a.rows : hi, lo + size);
     return {head, b, head - b * a.Hkv, tile, 32 * tile, cut, lo, hi, parts};
 }
 
@@ -347,34 +360,39 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && WAVES == 4 ? 2 : 1) v
     }
 }
 
-// Adds the parts of one key tile: 32 groups of four elements a workgroup, eight
-// threads to each, every thread its parts in order and then their sums in order.
-template <typename T, int D>
+// Adds the parts of one key tile, every thread four elements: PER threads share
+// them, each every PER-th part in order, and their sums are added in order.
+template <typename T, int D, int PER>
 __global__ __launch_bounds__(256) void join_kernel(BwdArgs a, T* __restrict__ gk, T* __restrict__ gv) {
-    __shared__ f32x4 sums[8][32];
+    constexpr int kFours = 256 / PER;  // groups of four elements of a workgroup
+    __shared__ f32x4 sums[PER][PER > 1 ? kFours : 1];
     const int head = blockIdx.x / a.part_tiles, tile = blockIdx.x % a.part_tiles;
     const int b = head / a.Hkv, hk = head - b * a.Hkv;
     const int m0 = 32 * tile / kKeys * kKeys;
     int lo, end, parts = 1;
     rows_of(a, m0, min(m0 + kKeys, a.Tk) - 1, lo, end);
     if (a.sliced) {
-        if (end - lo <= a.slice_rows) return;  // written whole
-        parts = (end - lo - 1) / a.slice_rows + 1;
+        const int size = slice_of(a, end - lo);
+        if (end - lo <= size) return;  // written whole
+        parts = (end - lo - 1) / size + 1;
     }
     const int segs = a.segs && a.rows > end ? (a.rows - end - 1) / a.seg_rows + 1 : 0;
     const float* part = a.part_of(head, tile, 0, D);
-    const int x = threadIdx.x & 31, first = threadIdx.x >> 5;
-    const int i = blockIdx.y * 32 + x, row = i / (D / 4), ch = 4 * (i % (D / 4)), key = 32 * tile + (row & 31);
+    const int x = threadIdx.x % kFours, first = threadIdx.x / kFours;
+    const int i = blockIdx.y * kFours + x, row = i / (D / 4), ch = 4 * (i % (D / 4)), key = 32 * tile + (row & 31);
     if (key < a.sinks) parts += segs;  // the others have none
     f32x4 s = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll 8
-    for (int p = first; p < parts; p += 8)
+    for (int p = first; p < parts; p += PER)
         s += *reinterpret_cast<const f32x4*>(part + static_cast<size_t>(p) * 64 * D + 4 * i);
-    sums[first][x] = s;
-    __syncthreads();
-    if (first > 0 || key >= a.Tk) return;
+    if constexpr (PER > 1) {
+        sums[first][x] = s;
+        __syncthreads();
+        if (first > 0) return;
 #pragma unroll
-    for (int p = 1; p < 8; ++p) s += sums[p][x];
+        for (int p = 1; p < PER; ++p) s += sums[p][x];
+    }
+    if (key >= a.Tk) return;
     T* dst = (row >= 32 ? gv : gk) + ((static_cast<size_t>(b) * a.Tk + key) * a.Hkv + hk) * D + ch;
     store4<T>(dst, s[0], s[1], s[2], s[3]);
 }
@@ -555,7 +573,7 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(T) == 2 ? 2 : 1) void dq_kernel
         seen_dq<T, D>(a, mask, pos, wp0, wp1, lse2, delta, q + qrow * D, go + qrow * D, kbase, vbase, kstride, lane, put);
 }
 
-BwdArgs make_args(bool f32, int B, int Tq, int Tk, int Hq, int Hkv, int window, int sinks, float scale) {
+BwdArgs make_args(bool f32, int B, int Tq, int Tk, int Hq, int Hkv, int d, int window, int sinks, float scale) {
     BwdArgs a{};
     a.B = B;
     a.Tq = Tq;
@@ -572,37 +590,68 @@ BwdArgs make_args(bool f32, int B, int Tq, int Tk, int Hq, int Hkv, int window, 
     const long long heads = static_cast<long long>(B) * Hkv, groups = heads * a.key_blocks;
     a.split = heads * ((a.rows + kRows - 1) / kRows) < (f32 ? 257 : 192);  // as the forward does
     a.row_tiles = a.split ? (a.rows + 31) / 32 : (a.rows + kRows - 1) / kRows;
-    // The rows of a key block are sliced where the blocks alone would leave CUs
-    // idle: below one workgroup per CU, or below two where the causal mask makes
-    // the first block's list much longer than the others'.  Slices of a 384th of
-    // all rows, 64 at least (training step T=4096, 32 query on 8 key heads: 1023
-    // us unsliced, 748 with a 256th, 708, 724 with a 768th, 765 with a 1024th).
+    // The rows of a key block are cut into slices where that is faster by this
+    // estimate (us): `row`, one CU's time for a row and 128 keys, times the rows of
+    // a CU (an equal share and half of the longest piece, or the longest alone; fp32
+    // pieces take a CU each, so that few enough to find one, 224, take as long as the
+    // longest; 96 rows' time goes to each piece's start and end); `part` for each part
+    // written and read, 4 for the kernel that joins them.  Without slices, sinks go
+    // to segments.  Of 20 training steps of different sizes, each timed with every
+    // length of slice, the one taken here is 2.0% from the fastest on average and 14%
+    // at most.
     a.slices = a.long_slices = 1;
     a.slice_rows = a.rows;
     const int tiles = (Tk + 31) / 32;
     if (groups > 0 && groups < 512 && a.rows > 0) {
+        const double row = (f32 ? 0.40 : 0.040) * d / 128, part = 0.06 * d / 128;
+        const bool sunk = window && sinks > 0;
         auto list = [&](int j) {
             int lo, hi;
             rows_of(a, j * kKeys, (j + 1) * kKeys < Tk ? (j + 1) * kKeys - 1 : Tk - 1, lo, hi);
-            return static_cast<long long>(hi - lo);
+            return hi - lo;
         };
-        long long total = 0, longest = 0;
-        for (int j = 0; j < a.key_blocks; ++j) {
-            total += list(j);
-            longest = list(j) > longest ? list(j) : longest;
-        }
-        if (groups < 256 || 2 * longest * a.key_blocks > 3 * total) {
-            const long long even = (total * heads / 384 + 31) / 32 * 32;
-            a.slice_rows = static_cast<int>(even < 64 ? 64 : even < a.rows ? even : a.rows);
-            a.sliced = true;
-            if (window) a.long_blocks = (sinks + kKeys - 1) / kKeys;
-            long long most[2] = {1, 1};
+        auto estimate = [&](int cut, int& longest) {  // cut 0: no slices
+            long long total = 0, pieces = 0, parts = 0;
+            longest = 0;
             for (int j = 0; j < a.key_blocks; ++j) {
-                const long long cuts = (list(j) + a.slice_rows - 1) / a.slice_rows;
+                const int n = list(j), here = cut && n > cut ? (n - 1) / cut + 1 : 1;
+                total += n;
+                pieces += here;
+                if (here > 1) parts += here;
+                if (n > longest) longest = n;
+            }
+            const double most = cut && cut < longest ? cut : longest, even = static_cast<double>(total) * heads / 256 + most / 2;
+            const double ends = cut ? 96.0 * pieces * heads / 256 : 96.0;
+            const bool once = f32 && cut && pieces * heads <= 224;
+            return row * ((most > even || once ? most : even) + ends) + (parts ? 4 + part * parts * heads : 0);
+        };
+        int longest, best = 0;
+        double least = estimate(0, longest);
+        if (sunk) {  // the segments' kernel and join
+            const double even = static_cast<double>(heads) * ((sinks + 31) / 32) * a.rows / 1024;
+            least += 8 + 0.13 * (even > 128 ? even : 128) * (f32 ? 5 : 1);
+        }
+        a.sliced = true;
+        estimate(0, longest);
+        for (int cut = 32; cut < longest; cut = (cut + cut / 4 + 31) / 32 * 32) {
+            int unused;
+            const double t = estimate(cut, unused);
+            if (t < least) {
+                least = t;
+                best = cut;
+            }
+        }
+        a.sliced = best > 0;
+        if (a.sliced) {
+            a.slice_rows = best;
+            if (window) a.long_blocks = (sinks + kKeys - 1) / kKeys;
+            int most[2] = {1, 1};
+            for (int j = 0; j < a.key_blocks; ++j) {
+                const int cuts = list(j) > 0 ? (list(j) - 1) / best + 1 : 1;
                 if (cuts > most[j < a.long_blocks]) most[j < a.long_blocks] = cuts;
             }
-            a.slices = static_cast<int>(most[0]);
-            a.long_slices = static_cast<int>(most[1]);
+            a.slices = most[0];
+            a.long_slices = most[1];
             a.slots = a.slices > 1 ? a.slices : 0;
             a.long_slots = a.long_slices > 1 ? a.long_slices : 0;
             a.long_tiles = 4 * a.long_blocks < tiles ? 4 * a.long_blocks : tiles;
@@ -653,9 +702,14 @@ hipError_t launch(const BwdArgs& a, const void* q_, const void* k_, const void* 
     if (seg_blocks)
         hipLaunchKernelGGL((dkdv_kernel<T, D, 1>), dim3(static_cast<unsigned>(seg_blocks)), dim3(64), CK::kLds, st, a, q, k,
                            v, go, static_cast<T*>(gk), static_cast<T*>(gv));
-    if (join_blocks)
-        hipLaunchKernelGGL((join_kernel<T, D>), dim3(static_cast<unsigned>(join_blocks), 64 * D / 4 / 32), dim3(256), 0,
-                           st, a, static_cast<T*>(gk), static_cast<T*>(gv));
+    if (join_blocks) {
+        // Eight threads to four elements where parts are many or the work is small; else one, as workgroups then cost
+        // more than loads in turn (4 heads, T=2504, 5 parts each: 20000 workgroups 23.6 us, an eighth of them 7.9).
+        const bool many = a.long_slots > 16 || a.slots > 16 || join_blocks * (D / 2) <= 4096;
+        auto* join = many ? join_kernel<T, D, 8> : join_kernel<T, D, 1>;
+        hipLaunchKernelGGL(join, dim3(static_cast<unsigned>(join_blocks), 64 * D / 4 / (many ? 32 : 256)), dim3(256), 0, st, a,
+                           static_cast<T*>(gk), static_cast<T*>(gv));
+    }
     return hipGetLastError();
 }
 
@@ -663,7 +717,7 @@ hipError_t launch(const BwdArgs& a, const void* q_, const void* k_, const void* 
 }  // namespace attn
 
 size_t attn_backward_workspace_floats(int dtype, int B, int Tq, int Tk, int Hq, int Hkv, int d, int window, int sinks) {
-    const attn::BwdArgs a = attn::make_args(dtype == GDR_DTYPE_F32, B, Tq, Tk, Hq, Hkv, window, sinks, 1.f);
+    const attn::BwdArgs a = attn::make_args(dtype == GDR_DTYPE_F32, B, Tq, Tk, Hq, Hkv, d, window, sinks, 1.f);
     const size_t heads = static_cast<size_t>(B) * Hkv;
     return heads * (2 * static_cast<size_t>(a.pitch) + a.parts_before(a.part_tiles) * 64 * d);
 }
@@ -672,7 +726,7 @@ hipError_t launch_attn_backward(int dtype, int B, int Tq, int Tk, int Hq, int Hk
                                 float scale, const void* q, const void* k, const void* v, const void* o,
                                 const float* lse, const void* go, void* gq, void* gk, void* gv, float* ws,
                                 hipStream_t st) {
-    attn::BwdArgs a = attn::make_args(dtype == GDR_DTYPE_F32, B, Tq, Tk, Hq, Hkv, window, sinks, scale);
+    attn::BwdArgs a = attn::make_args(dtype == GDR_DTYPE_F32, B, Tq, Tk, Hq, Hkv, d, window, sinks, scale);
     const size_t heads = static_cast<size_t>(B) * Hkv;
     a.stats = ws;
     a.part = ws + heads * 2 * a.pitch;
