@@ -229,11 +229,19 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && WAVES == 4 ? 2 : 1) v
         const int y = a.G(r);
         return (y * a.Hq + (r - y * a.G.d)) * D * static_cast<int>(sizeof(T));
     });
-    const T *qp = q + q0 + static_cast<size_t>(a.G(lo)) * a.Hq * D, *gp = go + q0 + static_cast<size_t>(a.G(lo)) * a.Hq * D;
-    auto fetch = [&](int i) {  // steps in turn
+    // Steps run backwards from the end of the rows or, under a window, from where
+    // the workgroups of overlapping lists are at the same rows at the same time and
+    // read them from L2 (window 1024, T=8192, 32 on 8 heads: 1.15 -> 0.18 GB from
+    // memory, 1% of the step).
+    const int n = (hi - lo + BM - 1) / BM;
+    const int from = n > 0 && a.window ? n - 1 - (lo / BM + n - 1) % n : n - 1;
+    const size_t low = q0 + static_cast<size_t>(a.G(lo)) * a.Hq * D;
+    int next = from;  // step to fetch
+    const T *qp = q + low + from * qstep, *gp = go + low + from * qstep;
+    auto fetch = [&](int i) {
         const uint32_t buf = lds_addr(smem) + (i & 1) * C::kBuf;
         const uint32_t st = lds_addr(smem) + C::kStat + (i & 1) * C::kStatBuf + 256 * wave;
-        const int r0 = lo + BM * i;
+        const int r0 = lo + BM * next;
         if (even && r0 + BM <= a.rows) {
             copy.run(buf, qp);
             copy.run(buf + C::kTile, gp);
@@ -248,15 +256,20 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && WAVES == 4 ? 2 : 1) v
             copy.gather(buf + C::kTile, [&](int r) { return go + row(r); });
             if (wave < NM) copy_words(st, stat + r0, 4u * (h2 * a.pitch + min(32 * wave + (lane & 31), a.rows - 1 - r0)));
         }
-        qp += qstep;
-        gp += qstep;
+        qp -= qstep;
+        gp -= qstep;
+        if (--next < 0) {
+            next += n;
+            qp += n * qstep;
+            gp += n * qstep;
+        }
     };
     // rows [whole_lo, whole_hi) see all of the wave's keys, rows outside [any_lo, any_hi) none
     auto rows_to = [&](int j) { return min(a.Tq, max(0, j - off)) * a.G.d; };
     const int any_lo = wave_live ? rows_to(j0) : hi, whole_lo = min(a.Tq + 1, max(0, j0 + 31 - off)) * a.G.d;
     const int any_hi = a.window == 0 || j0 < a.sinks ? hi : min(hi, rows_to(j1 + a.window));
     const int whole_hi = a.window == 0 || j0 + 31 < a.sinks ? hi : min(hi, rows_to(j0 + a.window));
-    const int n = (hi - lo + BM - 1) / BM;
+    int step = from;
     const int rb0 = RowRead<T, D>::base(lane & 31, h2), cb0 = ColRead<T, D>::base(lane);
     if (n > 0) fetch(0);
 #pragma unroll 1
@@ -264,7 +277,8 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && WAVES == 4 ? 2 : 1) v
         tile_barrier();
         if (i + 1 < n) fetch(i + 1);
         const int buf = (i & 1) * C::kBuf, rb = rb0 + buf, cb = cb0 + buf;
-        const int r0 = lo + BM * i;
+        const int r0 = lo + BM * step;
+        step = step > 0 ? step - 1 : n - 1;
         if (r0 + BM <= any_lo || r0 >= any_hi) continue;
         const float* st = reinterpret_cast<const float*>(smem + C::kStat + (i & 1) * C::kStatBuf) + 4 * h2;
         const bool whole = r0 >= whole_lo && r0 + BM <= whole_hi;
