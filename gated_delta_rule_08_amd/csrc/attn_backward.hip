@@ -20,6 +20,11 @@
 // fp32 partial sums a last kernel adds in order.  Small problems, whose keys
 // alone would leave compute units without work, cut every key's rows in the
 // same way, and the rows of dq_kernel give each wave a quarter of the keys.
+//
+// Bound by the products and the vector work between them at two waves per SIMD
+// (dK and dV of 32 keys are 128 accumulators of a lane at d=128): T=8192, window
+// 1024, 4 sinks, 32 query on 8 key heads: dq 235 us (41% matrix cores busy, 6 d
+// flops per pair), dkdv 304 (41%, 8 d), segments 30, join 5.
 #include "attn_common.h"
 
 namespace gdr {
