@@ -11,7 +11,7 @@
 // likewise; no registers hold them, and no barrier until the end.  The group's
 // query heads are the 16 columns of S^T = K Q^T, so a key read serves every head
 // of its group.  64 sequences of 16 .. 8000 tokens, 8 key heads, d=128 (1.05 GB):
-// 163 us and 11 for the join, 5.9 TB/s of the whole call; one of 32768: 24 + 5 us.
+// 163 us and 6 for the join, 6.0 TB/s of the whole call; one of 32768: 24 + 5 us.
 //
 // The visible keys of a sequence are a list (the sinks, then the window) in
 // blocks of 128.  Sequences differ in length, so it is not they that are dealt
@@ -474,20 +474,20 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(T) * D <= 256 ? 2 : 1) void dec
     }
 }
 
-// Joins the parts of a shared unit, one workgroup per query head: part 0 is
-// slot 1 of the unit's first share, the others slot 0 of the shares after it.
-// 64 parts at a time, lane s holding part s's weight 2^(m_s - max m); a wave
-// adds every fourth part, the channels over its lanes, and the four sums are
-// added in order.
-template <typename T, int D>
+// Joins the parts of a shared unit, W waves per query head: part 0 is slot 1 of
+// the unit's first share, the others slot 0 of the shares after it.  16 W parts
+// at a time, lane s holding part s's weight 2^(m_s - max m); a wave adds every
+// W-th part, the channels over its lanes, and the waves' sums are added in order.
+template <typename T, int D, int W>
 __global__ __launch_bounds__(256) void join_kernel(DecodeArgs a, const int* __restrict__ table,
                                                    const int* __restrict__ lengths,
                                                    const float* __restrict__ part_o,
                                                    const float* __restrict__ part_ml, T* __restrict__ o) {
-    constexpr int N = D / 64, W = 4, kEach = 64 / W;
-    __shared__ float sums[W - 1][D];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int b = blockIdx.x / a.Hq, hq = blockIdx.x - b * a.Hq;
+    constexpr int N = D / 64, kEach = 16;
+    __shared__ float sums[W > 1 ? W - 1 : 1][D];
+    const int lane = threadIdx.x & 63, every = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = every % W;
+    const int at = blockIdx.x * (4 / W) + every / W, b = at / a.Hq, hq = at - b * a.Hq;
+    if (b >= a.B) return;
     const Span sp = span_of(a, lengths[b]);
     if (sp.blocks == 0 || !has_page(a, b, sp.pos, table)) return;
     const int per = a.Hkv * a.head_tiles, hk = hq / a.G, g = hq - hk * a.G;
@@ -498,9 +498,9 @@ __global__ __launch_bounds__(256) void join_kernel(DecodeArgs a, const int* __re
     if (parts == 1) return;  // written whole
     auto slot = [&](int s) { return (static_cast<size_t>(w0 + s) * 2 + (s == 0)) * a.heads + (g & 15); };
     float M = -INFINITY, total = 0.f, acc[N] = {};
-    for (int s0 = 0; s0 < parts; s0 += 64) {
+    for (int s0 = 0; s0 < parts; s0 += kEach * W) {
         float m = -INFINITY, l = 0.f;
-        if (s0 + lane < parts) {
+        if (lane < kEach * W && s0 + lane < parts) {
             m = part_ml[slot(s0 + lane) * 2];
             l = part_ml[slot(s0 + lane) * 2 + 1];
         }
@@ -530,12 +530,14 @@ __global__ __launch_bounds__(256) void join_kernel(DecodeArgs a, const int* __re
             for (int e = 0; e < N; ++e) acc[e] = fmaf(ws, x[i][e], acc[e]);
         }
     }
-    if (wave > 0) {
+    if constexpr (W > 1) {
+        if (wave > 0) {
 #pragma unroll
-        for (int e = 0; e < N; ++e) sums[wave - 1][N * lane + e] = acc[e];
+            for (int e = 0; e < N; ++e) sums[wave - 1][N * lane + e] = acc[e];
+        }
+        __syncthreads();
+        if (wave > 0) return;
     }
-    __syncthreads();
-    if (wave > 0) return;
     const float inv = total == 0.f ? 0.f : 1.f / total;
     const size_t row = static_cast<size_t>(b) * a.Hq + hq;
 #pragma unroll
@@ -573,8 +575,11 @@ hipError_t launch_decode_t(const DecodeArgs& a, const void* q, const void* k, co
                        part_o, part_ml);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.shares == 0) return e;
-    hipLaunchKernelGGL((join_kernel<T, D>), dim3(static_cast<unsigned>(rows)), dim3(256), 0, st, a, table,
-                       lengths, part_o, part_ml, static_cast<T*>(o));
+    // Many heads have few parts each and take a wave (64 sequences of 32: 5.7 against 10.9 us), few heads four.
+    const bool many = rows >= 1024;
+    auto* join = many ? join_kernel<T, D, 1> : join_kernel<T, D, 4>;
+    hipLaunchKernelGGL(join, dim3(static_cast<unsigned>(many ? (rows + 3) / 4 : rows)), dim3(256), 0, st, a, table, lengths,
+                       part_o, part_ml, static_cast<T*>(o));
     return hipGetLastError();
 }
 

@@ -124,6 +124,13 @@ def test_decode_many_sequences():
     assert same(kp, c.k) and same(vp, c.v)
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_decode_many_heads_and_many_parts(dt):
+    """A long sequence, cut into dozens of parts, among short ones with enough heads that each is joined by one wave."""
+    announce("attn decode many heads and parts %s" % dt)
+    run_decode(dt, [30000] + [b % 7 for b in range(40)], 32, 4, 64, 256, 0, 0)
+
+
 def test_cache_beyond_4_gib():
     """Page tensors of 8.6 GB each, the sequence's pages at their far end and at their front."""
     announce("attn cache beyond 4 GiB")
