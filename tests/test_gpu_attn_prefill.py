@@ -351,6 +351,55 @@ def test_side_stream_and_automatic_workspace():
     del junk
 
 
+def test_two_streams_at_once():
+    """Training steps of different sizes on two streams, enqueued in turn: bitwise what each gives alone."""
+    announce("attn two streams")
+    cases = [(1, 700, 8, 2, 128, 130, 4), (2, 333, 6, 6, 64, 0, 0)]
+    x = [[make(i, "bf16", B, T, H, d).cuda() for i, H in enumerate((Hq, Hkv, Hkv, Hq))] for B, T, Hq, Hkv, d, _, _ in cases]
+
+    def step(case, x, stream):
+        B, T, Hq, Hkv, d, window, sinks = case
+        q, k, v, go = x
+        o, lse = torch.empty_like(q), torch.empty(B, T, Hq, device="cuda")
+        dq, dk, dv = (torch.empty_like(t) for t in (q, k, v))
+        gdr.gdr_attn_prefill(q, k, v, o, lse, window=window, sinks=sinks, stream=stream)
+        gdr.gdr_attn_backward(q, k, v, o, lse, go, dq, dk, dv, window=window, sinks=sinks, stream=stream)
+        return o, lse, dq, dk, dv
+
+    alone = [step(c, t, None) for c, t in zip(cases, x)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    runs = []
+    for _ in range(5):
+        for c, t, s in zip(cases, x, streams):
+            with torch.cuda.stream(s):
+                runs.append((alone[cases.index(c)], step(c, t, None)))
+    torch.cuda.synchronize()
+    for want, got in runs:
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def test_refusals_on_the_device():
+    announce("attn refusals")
+    q, k = make(1, "bf16", 2, 40, 4, 64).cuda(), make(2, "bf16", 2, 40, 2, 64).cuda()
+    o, lse = torch.full_like(q, 7.0), torch.full((2, 40, 4), 7.0, device="cuda")
+    turned = q.transpose(0, 1).contiguous().transpose(0, 1)
+    for bad in ((turned, k, k, o), (q, k, k, turned), (q[:, ::2], k, k, o[:, ::2])):
+        with pytest.raises(ValueError, match="contiguous"):
+            gdr.gdr_attn_prefill(*bad, lse if bad[0].shape == q.shape else None)
+    with pytest.raises(ValueError, match="GPU"):
+        gdr.gdr_attn_prefill(q, k, k.cpu(), o)
+    shifted = torch.zeros(q.numel() + 1, dtype=q.dtype, device="cuda")[1:].view(q.shape)
+    with pytest.raises(gdr.GdrError):  # not 16-byte aligned
+        gdr.gdr_attn_prefill(shifted, k, k, o)
+    need = gdr.gdr_attn_backward_workspace_bytes(q.dtype, 2, 40, 40, 4, 2, 64)
+    with pytest.raises(gdr.GdrError):
+        gdr.gdr_attn_backward(q, k, k, q, lse, q, o, torch.empty_like(k), torch.empty_like(k),
+                              workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
+    torch.cuda.synchronize()
+    assert (o == 7).all() and (lse == 7).all()
+
+
 def test_gradient_against_differences():
     """A directional derivative of sum(grad_o * o) by central differences of the fp32 forward.
 
