@@ -12,8 +12,8 @@
 // per wave and walks the keys, as the forward does.  Every sum has a fixed
 // order.
 //
-// The first of them, dq_kernel, also forms delta and writes the row statistics
-// the second one reads.
+// The first of them, dq_kernel, also forms delta (from o, or where few keys are
+// visible as sum_j P_ij dP_ij) and writes the row statistics the second one reads.
 //
 // Sink keys are seen by every later row, a list far longer than any other
 // key's: those rows are cut into segments of their own (one wave each), whose
@@ -448,6 +448,15 @@ __device__ __forceinline__ void seen_dq(const BwdArgs& a, Mask mask, int pos, in
     }
 }
 
+// delta = dO . o carries the rounding of o to the element type, which the
+// difference dP - delta does not shrink with: with n visible keys a share of about
+// 1 / n of a row's error (all of it for one key, where dS is 0).  Workgroups of bf16
+// rows that see at most this many keys form delta = sum_j P_ij dP_ij in fp32
+// instead, in a pass of its own (T=18, 4 heads: error of grad_q against float64
+// 1.78 -> 1.40 times that of fp32 arithmetic rounded once; T=642: 1.54 -> 1.43; 4 x
+// 155 tokens of 32 heads 40 -> 45 us, T=8192 the same); the others would not gain.
+constexpr int kFew = 256;
+
 template <typename T, int D, bool SPLIT> struct DqCfg {
     static constexpr int BN = SPLIT ? 32 * kWaves : 32;  // keys of a step
     static constexpr int kTile = BN * D * static_cast<int>(sizeof(T));
@@ -488,8 +497,9 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(T) == 2 ? 2 : 1) void dq_kernel
     const TileRange range = TileRange::of<BN, 32>(keys, a.window, a.Tk, sub, wp0, wp1);
     const int end_tile = wave_live ? range.end : 0;
     const TileCopy<T, D, BN, kWaves> copy(wave, lane, [&](int r) { return r * static_cast<int>(kstride * sizeof(T)); });
-    const T *kp = kbase + keys.jump * kstride, *vp = vbase + keys.jump * kstride;  // the next tile's first rows
-    auto fetch = [&](int i) {  // tiles in turn
+    const T *const kp0 = kbase + keys.jump * kstride, *const vp0 = vbase + keys.jump * kstride;
+    const T *kp = kp0, *vp = vp0;  // the next tile's first rows
+    auto fetch = [&](int i) {      // tiles in turn
         const uint32_t buf = lds_addr(smem) + (i & (C::kBufs - 1)) * 2 * C::kTile;
         if (i >= range.full_lo && i < range.full_hi) {
             copy.run(buf, kp);
@@ -516,13 +526,47 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(T) == 2 ? 2 : 1) void dq_kernel
     }
     delta += other_half(delta);
     const float lse2 = lse[qrow] * kLog2e;
+    const float c = a.scale * kLog2e;
+    const int rb0 = RowRead<T, D>::base(lane & 31, h2) + sub * Tile<T, D>::kRow;
+    if (sizeof(T) == 2 && n > 0 && keys.count <= kFew) {  // delta as a sum over the keys
+        float sum = 0.f;
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) {
+            tile_barrier();
+            if (i + 1 < n) fetch(i + 1);
+            const int rb = rb0 + (i & 1) * 2 * C::kTile;
+            if (i >= end_tile) continue;
+            f32x16 s = zero16(), dp = zero16();
+#pragma unroll
+            for (int e = 0; e < KS; ++e) s = mma32(RowRead<T, D>::get(smem, rb, e, 0), qf[e], s);
+#pragma unroll
+            for (int e = 0; e < KS; ++e) dp = mma32(RowRead<T, D>::get(smem, rb, e, C::kTile), gf[e], dp);
+            const int x0 = i * BN + sub;
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                sum += mask.sees(pos, keys.key(x0 + row32(r, h2))) ? ex2(fmaf(s[r], c, -lse2)) * dp[r] : 0.f;
+        }
+        sum += other_half(sum);
+        tile_barrier();
+        if constexpr (SPLIT) {  // the waves' sums, in wave order
+            float* box = reinterpret_cast<float*>(smem);
+            box[64 * wave + lane] = sum;
+            tile_barrier();
+            sum = box[lane];
+#pragma unroll
+            for (int w = 1; w < kWaves; ++w) sum += box[64 * w + lane];
+            tile_barrier();
+        }
+        delta = sum;
+        kp = kp0;
+        vp = vp0;
+        fetch(0);
+    }
     if (live && (!SPLIT || wave == 0))
         a.stats[(static_cast<size_t>(head) * 2 + h2) * a.pitch + row] = h2 ? delta : lse2;
-    const float c = a.scale * kLog2e;
     f32x16 dq[DT];
 #pragma unroll
     for (int t = 0; t < DT; ++t) dq[t] = zero16();
-    const int rb0 = RowRead<T, D>::base(lane & 31, h2) + sub * Tile<T, D>::kRow;
     const int cb0 = ColRead<T, D>::base(lane) + sub * Tile<T, D>::kRow;
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {

@@ -351,6 +351,23 @@ def test_side_stream_and_automatic_workspace():
     del junk
 
 
+@pytest.mark.parametrize("B,window,sinks", [(1, 0, 0), (60, 0, 0), (1, 1, 0), (60, 1, 0)])
+def test_a_single_visible_key_has_no_score_gradient(B, window, sinks):
+    """Softmax of one score is constant: dS = P (dP - delta) with delta = P dP is P dP (1 - P), and P is off from 1 by
+    the error of the score (a sum of d products, its scaling, 2^-24 each) and of the exponential and logarithm."""
+    announce("attn single key %d %d" % (B, window))
+    T, H, d, scale = 40, 4, 128, 0.1
+    q, k, v, go = (make(i, "bf16", B, T, H, d) for i in range(4))
+    o, lse = forward(q, k, v, window, sinks, scale)
+    dq, dk, dv = (torch.empty_like(t).cuda() for t in (q, k, v))
+    gdr.gdr_attn_backward(q.cuda(), k.cuda(), v.cuda(), o, lse, go.cuda(), dq, dk, dv, window=window, sinks=sinks, scale=scale)
+    rows = slice(0, T if window == 1 else 1)
+    q, k, v, go = (t[:, rows].double() for t in (q, k, v, go))
+    off = (d + 4) * 2 ** -24 * scale * (q * k).abs().sum(-1, keepdim=True) + 32 * 2 ** -24 * (1 + scale * (q * k).sum(-1, keepdim=True).abs())
+    bound = 1.01 * scale * k.abs() * (go * v).abs().sum(-1, keepdim=True) * (off + 2 * d * 2 ** -24)
+    assert (dq[:, rows].double().cpu().abs() <= bound).all()
+
+
 def test_two_streams_at_once():
     """Training steps of different sizes on two streams, enqueued in turn: bitwise what each gives alone."""
     announce("attn two streams")
