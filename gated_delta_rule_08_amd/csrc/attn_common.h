@@ -12,6 +12,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "attn_plan.h"
 #include "gdr_internal.h"
 
 namespace gdr {
@@ -116,23 +117,6 @@ template <> __device__ __forceinline__ void store4<bf16_t>(bf16_t* p, float a, f
 
 __device__ __forceinline__ float ex2(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ float lg2(float x) { return __builtin_amdgcn_logf(x); }
-
-// n / d for 0 <= n < 2^31 by one multiplication: with 2^s >= d the smallest
-// such power and m = ceil(2^(31+s) / d), n m / 2^(31+s) exceeds n / d by less
-// than n / 2^31 / d < 1 / d, so its floor is exact.
-struct FastDiv {
-    uint32_t mul, shift;
-    int d;
-    __host__ FastDiv(int div = 1) : d(div) {
-        int s = 0;
-        while ((1ll << s) < div) ++s;
-        mul = static_cast<uint32_t>(((1ull << (31 + s)) + div - 1) / div);
-        shift = 31 + s;
-    }
-    __device__ __forceinline__ int operator()(int n) const {
-        return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(n)) * mul) >> shift);
-    }
-};
 
 // acc += A B over 32 elements as two mma32 would, summing the pairs whose bit in
 // `seen` is set and no others: a hidden pair's weight is 0, but 0 times an
@@ -345,29 +329,6 @@ template <typename T, int D, int ROWS, int WAVES> struct TileCopy {
             copy_1k_from(tile + (wave + j * WAVES) * 1024, reinterpret_cast<const unsigned char*>(address(row(j))) + unit(j));
     }
 };
-
-// Which of `tiles` pieces of work (rank 0 the longest) of which head workgroup
-// bid takes.  Workgroups go round the 8 XCDs: a head's pieces stay on one, whose
-// L2 then holds what they share, the longest first.  Where all fit at once, two
-// to a CU (32 CUs to an XCD, filled in turn), the second round goes backwards,
-// so that a long piece shares its CU with a short one.
-__device__ __forceinline__ void place(int bid, int heads, int tiles, int& head, int& rank) {
-    if (heads % 8 == 0) {
-        const int y = bid >> 3, here = heads >> 3, all = here * tiles;
-        if (all > 32 && all <= 64) {
-            const int r = y < 32 ? y : all - 1 - (y - 32);
-            rank = r / here;
-            head = (r - rank * here) * 8 + (bid & 7);
-        } else {
-            head = (y / tiles) * 8 + (bid & 7);
-            rank = y % tiles;
-        }
-    } else {
-        const int all = heads * tiles, r = all > 256 && all <= 512 && bid >= 256 ? all - 1 - (bid - 256) : bid;
-        head = r % heads;
-        rank = r / heads;
-    }
-}
 
 // The keys that the rows of a workgroup may see, as one list: the sinks before
 // the window of its first row, then everything from there to its last row's
