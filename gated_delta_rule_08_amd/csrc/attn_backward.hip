@@ -247,16 +247,14 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && WAVES == 4 ? 2 : 1) v
                 dp = mma32(RowRead<T, D>::get(smem, rb2, e, C::kTile + 32 * w * L::kRow), vf[e], dp);
                 if (e % 4 == 3) __builtin_amdgcn_sched_barrier(0);
             }
+            // dS is 0 where P is, unless dP - delta is not finite: then, as for dV, the
+            // sums become NaN and seen_keys tells hidden pairs from visible ones whose
+            // weight underflowed.
 #pragma unroll
             for (int r = 0; r < 16; r += 4) {
                 const f32x4 de = *reinterpret_cast<const f32x4*>(st + 64 * w + 32 + 2 * r);
 #pragma unroll
                 for (int y = 0; y < 4; ++y) dp[r + y] = s[r + y] * (dp[r + y] - de[y]);
-            }
-            if (!whole) {  // a hidden pair's weight is 0, its dP may be anything
-#pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    if (s[r] == 0.f) dp[r] = 0.f;
             }
             {
                 frag_t<T> df[2] = {pack_regs<T>(dp, 0), pack_regs<T>(dp, 1)};
