@@ -455,8 +455,8 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(T) * D <= 256 ? 2 : 1) void dec
                 const int d = 64 * e + 4 * (threadIdx.x & 15);
                 f32x4 sum = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int x = 0; x < kWaves; ++x)
-                    if (mw[x] != 0.f) sum += *reinterpret_cast<const f32x4*>(jo + (x * 16 + head) * C::kPitch + d) * mw[x];
+                for (int x = 0; x < kWaves; ++x)  // a wave without keys holds zeros; one whose weight underflows may hold a NaN
+                    sum += *reinterpret_cast<const f32x4*>(jo + (x * 16 + head) * C::kPitch + d) * mw[x];
                 if (whole)
                     store4<T>(o + orow * D + d, sum[0] * inv, sum[1] * inv, sum[2] * inv, sum[3] * inv);
                 else

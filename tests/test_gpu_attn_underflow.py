@@ -52,3 +52,39 @@ def test_gradients_of_rows_whose_output_is_not_finite(dt, B, d, what):
         check("grad_k", dk[b, other], ref["grad_k"][0][other], ref["grad_k"][1][other])
         assert torch.isnan(dk[b, list(keys)].float()).all()
         check("grad_v", dv[b], *ref["grad_v"])
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("pages", [8, 64])  # one workgroup to a head; key blocks dealt out and joined
+@pytest.mark.parametrize("what", ["nan", "inf"])
+def test_decode_values_whose_weight_underflows(dt, d, pages, what):
+    """One key has all the weight (a score of 400 against about 1) and another, of the same or another wave's keys,
+    before or after it, a non-finite value: the output is not finite in that value's channel and as ever in the others."""
+    announce("attn underflow, decode %s %d %d %s" % (dt, d, pages, what))
+    page, Hq, Hkv, n = 16, 4, 2, 127
+    assert (gdr.gdr_attn_decode_workspace_bytes(DT[dt], 8, Hq, Hkv, d, page, pages) > 0) == (pages == 64)
+    spots = [(3, 5), (3, 40), (3, 126), (70, 2), (70, 75), (70, 100), (120, 1), (120, 127)]  # (heavy key, odd value)
+    B = len(spots)
+    q = torch.ones(B, Hq, d, dtype=DT[dt])
+    k, v = make(1, dt, B, n + 1, Hkv, d) * 0.125, make(2, dt, B, n + 1, Hkv, d)
+    for b, (heavy, _) in enumerate(spots):
+        k[b, heavy] = 400 / d
+    bad = v.clone()
+    for b, (_, odd) in enumerate(spots):
+        bad[b, odd, :, 9] = float(what)
+    table = torch.full((B, pages), -1, dtype=torch.int32)
+    table[:, :8] = torch.randperm(8 * B, generator=torch.Generator().manual_seed(1)).reshape(B, 8).int()
+    kp, vp = (torch.zeros(8 * B, Hkv, page, d, dtype=DT[dt]) for _ in range(2))
+    for b in range(B):
+        for pool, t in ((kp, k), (vp, bad)):
+            pool[table[b, :8].long()] = t[b].reshape(8, page, Hkv, d).transpose(1, 2)
+    lens = torch.full((B,), n, dtype=torch.int32)
+    o = torch.full((B, Hq, d), 7.0, dtype=DT[dt], device="cuda")
+    gdr.gdr_attn_decode(q.cuda(), k[:, n].contiguous().cuda(), bad[:, n].contiguous().cuda(), kp.cuda(), vp.cuda(), table.cuda(),
+                        lens.cuda(), o, scale=1.0)
+    rest = [c for c in range(d) if c != 9]
+    for b in range(B):
+        ref = attend(q[b:b + 1], k[b], v[b], 0, 0, 1.0, DT[dt])["o"]
+        check("o", o[b:b + 1, :, rest], ref[0][..., rest], ref[1][..., rest])
+        assert not torch.isfinite(o[b, :, 9].float()).any(), spots[b]
