@@ -314,13 +314,14 @@ __global__ __launch_bounds__(256) void join_kernel(BwdArgs a, T* __restrict__ gk
     }
     const int segs = a.segs && a.rows > end ? (a.rows - end - 1) / a.seg_rows + 1 : 0;
     const float* part = a.part_of(head, tile, 0, D);
+    const size_t apart = static_cast<size_t>(a.part_step) * 64 * D;
     const int x = threadIdx.x % kFours, first = threadIdx.x / kFours;
     const int i = blockIdx.y * kFours + x, row = i / (D / 4), ch = 4 * (i % (D / 4)), key = 32 * tile + (row & 31);
     if (key < a.sinks) parts += segs;  // the others have none
     f32x4 s = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll 8
     for (int p = first; p < parts; p += PER)
-        s += *reinterpret_cast<const f32x4*>(part + static_cast<size_t>(p) * 64 * D + 4 * i);
+        s += *reinterpret_cast<const f32x4*>(part + p * apart + 4 * i);
     if constexpr (PER > 1) {
         sums[first][x] = s;
         __syncthreads();
@@ -479,6 +480,8 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(T) == 2 ? 2 : 1) void dq_kernel
         vp = vp0;
         fetch(0);
     }
+    if (a.sliced && blockIdx.x == 0)
+        for (int j = threadIdx.x; j < a.part_blocks; j += 64 * kWaves) a.slots[j] = a.slots_before(j);
     if (live && (!SPLIT || wave == 0))
         a.stats[(static_cast<size_t>(head) * 2 + h2) * a.pitch + row] = h2 ? delta : lse2;
     f32x16 dq[DT];
@@ -588,7 +591,7 @@ hipError_t launch(const BwdArgs& a, const void* q_, const void* k_, const void* 
     if (join_blocks) {
         // Eight threads to four elements where parts are many or the work is small; else one, as workgroups then cost
         // more than loads in turn (4 heads, T=2504, 5 parts each: 20000 workgroups 23.6 us, an eighth of them 7.9).
-        const bool many = a.long_slots > 16 || a.slots > 16 || join_blocks * (D / 2) <= 4096;
+        const bool many = (a.sliced ? max(a.slices, a.long_slices) : 1 + a.segs) > 16 || join_blocks * (D / 2) <= 4096;
         auto* join = many ? join_kernel<T, D, 8> : join_kernel<T, D, 1>;
         hipLaunchKernelGGL(join, dim3(static_cast<unsigned>(join_blocks), 64 * D / 4 / (many ? 32 : 256)), dim3(256), 0, st, a,
                            static_cast<T*>(gk), static_cast<T*>(gv));
@@ -600,9 +603,7 @@ hipError_t launch(const BwdArgs& a, const void* q_, const void* k_, const void* 
 }  // namespace attn
 
 size_t attn_backward_workspace_floats(int dtype, int B, int Tq, int Tk, int Hq, int Hkv, int d, int window, int sinks) {
-    const attn::BwdArgs a = attn::make_args(dtype == GDR_DTYPE_F32, B, Tq, Tk, Hq, Hkv, d, window, sinks, 1.f);
-    const size_t heads = static_cast<size_t>(B) * Hkv;
-    return heads * (2 * static_cast<size_t>(a.pitch) + a.parts_before(a.part_tiles) * 64 * d);
+    return attn::workspace_floats(attn::make_args(dtype == GDR_DTYPE_F32, B, Tq, Tk, Hq, Hkv, d, window, sinks, 1.f));
 }
 
 hipError_t launch_attn_backward(int dtype, int B, int Tq, int Tk, int Hq, int Hkv, int d, int window, int sinks,
@@ -610,9 +611,7 @@ hipError_t launch_attn_backward(int dtype, int B, int Tq, int Tk, int Hq, int Hk
                                 const float* lse, const void* go, void* gq, void* gk, void* gv, float* ws,
                                 hipStream_t st) {
     attn::BwdArgs a = attn::make_args(dtype == GDR_DTYPE_F32, B, Tq, Tk, Hq, Hkv, d, window, sinks, scale);
-    const size_t heads = static_cast<size_t>(B) * Hkv;
-    a.stats = ws;
-    a.part = ws + heads * 2 * a.pitch;
+    attn::set_workspace(a, ws);
     auto* f = dtype == GDR_DTYPE_F32 ? (d == 64 ? attn::launch<float, 64> : attn::launch<float, 128>)
                                      : (d == 64 ? attn::launch<bf16_t, 64> : attn::launch<bf16_t, 128>);
     return f(a, q, k, v, o, lse, go, gq, gk, gv, st);

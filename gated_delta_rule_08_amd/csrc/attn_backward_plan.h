@@ -16,7 +16,7 @@ constexpr int kKeys = 32 * kWaves;  // keys of a dkdv workgroup
 constexpr int kRows = 32 * kWaves;  // rows of a dq workgroup
 
 struct BwdArgs {
-    int B, Tq, Tk, Hq, Hkv;
+    int B, Tq, Tk, Hq, Hkv, d;
     FastDiv G;
     int window, sinks;
     float scale;
@@ -29,20 +29,46 @@ struct BwdArgs {
     int long_slices, slices;  // the others into at most slices
     int sink_tiles, segs;     // not sliced: 32-key tiles that hold sinks, segments of each (at most)
     int seg_rows;
-    // Key tiles whose gradients come in parts: the first long_tiles have room for
-    // long_slots parts each, the others for slots.
-    int part_tiles, long_tiles, long_slots, slots;
+    // Key tiles whose gradients may come in parts.  Not sliced: the sinks' tiles, room
+    // for 1 + segs parts each.  Sliced: those of the first part_blocks blocks, room for
+    // what each block's list needs; slot s of a block's four tiles lie side by side.
+    int part_tiles, part_blocks;
+    int part_step;            // tiles from one part of a tile to its next
+    size_t head_parts;        // parts of a head
+    // The workspace: the row statistics, the slots, the parts.
     float* stats;             // [B Hkv, 2, pitch]: lse log2 e, then delta
+    int* slots;               // sliced: [512], slots_before each block
     float* part;              // [B Hkv, parts of a head, 2, 32, d]
     __host__ __device__ __forceinline__ int cuts() const { return long_blocks * long_slices + (key_blocks - long_blocks) * slices; }
-    __host__ __device__ __forceinline__ size_t parts_before(int tile) const {  // within a head
-        return static_cast<size_t>(tile < long_tiles ? tile : long_tiles) * long_slots +
-               static_cast<size_t>(tile < long_tiles ? 0 : tile - long_tiles) * slots;
+    __host__ __device__ __forceinline__ long long rows_before(int block) const;
+    // Slots before a block's: a block of n rows has (rows before it + n) / slice_rows -
+    // (rows before it) / slice_rows + 1 of them, at least n / slice_rows rounded up.
+    // dq_kernel, which runs first, leaves them in `slots`: formed by every workgroup of
+    // the join, the division takes as long as the join itself.
+    __host__ __device__ __forceinline__ int slots_before(int block) const {
+        return static_cast<int>(rows_before(block) / slice_rows) + block;
     }
-    __host__ __device__ __forceinline__ float* part_of(int head, int tile, int slot, int d) const {
-        return part + (static_cast<size_t>(head) * parts_before(part_tiles) + parts_before(tile) + slot) * 64 * d;
+    __device__ __forceinline__ float* part_of(int head, int tile, int slot, int d) const {
+        const size_t at = sliced ? 4 * static_cast<size_t>(slots[tile >> 2] + slot) + (tile & 3)
+                                 : static_cast<size_t>(tile) * (1 + segs) + slot;
+        return part + (head * head_parts + at) * 64 * d;
     }
 };
+
+// Rows in the lists of the key blocks before `block`, or a little more (sliced
+// only).  In queries, key block i is seen by at most clamp(Tk - 128 i, 0, most) of
+// them: by those from its first key on, under a window by no more than window + 127.
+__host__ __device__ __forceinline__ long long rows_before(const BwdArgs& a, int block, int most) {
+    const long long n = block, k = a.Tk < most ? 0 : min(block, (a.Tk - most) / kKeys + 1);  // the first k blocks have `most`
+    return k * most + (n - k) * a.Tk - kKeys * ((n * (n - 1) - k * (k - 1)) / 2);
+}
+__host__ __device__ __forceinline__ long long BwdArgs::rows_before(int block) const {
+    if (window == 0) return attn::rows_before(*this, block, Tq) * G.d;
+    const int longs = min(block, long_blocks), most = min(Tq, window + kKeys - 1);
+    // blocks whose last key's window ends before the first query
+    const int past = Tk - Tq - window + 1, none = min(block, max(longs, past > 0 ? past / kKeys : 0));
+    return (attn::rows_before(*this, longs, Tq) + attn::rows_before(*this, block, most) - attn::rows_before(*this, none, most)) * G.d;
+}
 
 // Rows (query * G + head) that see keys [j0, j1] through the window or, with
 // no window, causally: [lo, hi).  Counted in queries that exist before the
@@ -94,6 +120,17 @@ template <int WAVES> __host__ __device__ __forceinline__ Piece piece_of(const Bw
     return {head, b, head - b * a.Hkv, tile, 32 * tile, cut, lo, hi, parts};
 }
 
+// Most bytes that the parts of slices may take.  Shorter slices balance the compute
+// units better, but leave a part of 128 keys each; lists are sliced below 512 key
+// blocks only, whose gradients take at most 64 MiB in fp32.  By the estimate below
+// the bound costs 0.07% on average over 4000 random training steps and 7% at most
+// (8% at T=65408 with 32 query heads on one, for 256 MiB instead of 1.6 GB).
+// Measured at T=16384, 32 query on 2 key heads, d=128: 229 MB of parts 10.0 ms,
+// without the bound 415 MB and 9.6 ms.
+constexpr size_t kPartBytes = 256 << 20;
+
+constexpr int kSliced = 512;  // key blocks of all heads from which on none is sliced
+
 inline BwdArgs make_args(bool f32, int B, int Tq, int Tk, int Hq, int Hkv, int d, int window, int sinks, float scale) {
     BwdArgs a{};
     a.B = B;
@@ -101,6 +138,7 @@ inline BwdArgs make_args(bool f32, int B, int Tq, int Tk, int Hq, int Hkv, int d
     a.Tk = Tk;
     a.Hq = Hq;
     a.Hkv = Hkv;
+    a.d = d;
     a.G = FastDiv(Hq / Hkv);
     a.window = window;
     a.sinks = sinks;
@@ -123,7 +161,7 @@ inline BwdArgs make_args(bool f32, int B, int Tq, int Tk, int Hq, int Hkv, int d
     a.slices = a.long_slices = 1;
     a.slice_rows = a.rows;
     const int tiles = (Tk + 31) / 32;
-    if (groups > 0 && groups < 512 && a.rows > 0) {
+    if (groups > 0 && groups < kSliced && a.rows > 0) {
         const double row = (f32 ? 0.40 : 0.040) * d / 128, part = 0.06 * d / 128;
         const bool sunk = window && sinks > 0;
         auto list = [&](int j) {
@@ -131,9 +169,9 @@ inline BwdArgs make_args(bool f32, int B, int Tq, int Tk, int Hq, int Hkv, int d
             rows_of(a, j * kKeys, (j + 1) * kKeys < Tk ? (j + 1) * kKeys - 1 : Tk - 1, lo, hi);
             return hi - lo;
         };
-        auto estimate = [&](int cut, int& longest) {  // cut 0: no slices
+        auto estimate = [&](int cut) {  // cut 0: no slices
             long long total = 0, pieces = 0, parts = 0;
-            longest = 0;
+            int longest = 0;
             for (int j = 0; j < a.key_blocks; ++j) {
                 const int n = list(j), here = cut && n > cut ? (n - 1) / cut + 1 : 1;
                 total += n;
@@ -146,17 +184,29 @@ inline BwdArgs make_args(bool f32, int B, int Tq, int Tk, int Hq, int Hkv, int d
             const bool once = f32 && cut && pieces * heads <= 224;
             return row * ((most > even || once ? most : even) + ends) + (parts ? 4 + part * parts * heads : 0);
         };
-        int longest, best = 0;
-        double least = estimate(0, longest);
+        double least = estimate(0);
         if (sunk) {  // the segments' kernel and join
             const double even = static_cast<double>(heads) * ((sinks + 31) / 32) * a.rows / 1024;
             least += 8 + 0.13 * (even > 128 ? even : 128) * (f32 ? 5 : 1);
         }
         a.sliced = true;
-        estimate(0, longest);
-        for (int cut = 32; cut < longest; cut = (cut + cut / 4 + 31) / 32 * 32) {
-            int unused;
-            const double t = estimate(cut, unused);
+        if (window) a.long_blocks = (sinks + kKeys - 1) / kKeys;
+        int longest[2] = {0, 0}, best = 0;  // lists, of blocks without and with sinks
+        for (int j = 0; j < a.key_blocks; ++j) {
+            int& most = longest[j < a.long_blocks];
+            if (list(j) > most) most = list(j);
+        }
+        auto set = [&](int cut) {
+            a.slice_rows = cut;
+            a.slices = longest[0] > cut ? (longest[0] - 1) / cut + 1 : 1;
+            a.long_slices = longest[1] > cut ? (longest[1] - 1) / cut + 1 : 1;
+            a.part_blocks = a.slices > 1 ? a.key_blocks : a.long_slices > 1 ? a.long_blocks : 0;
+            a.head_parts = 4 * static_cast<size_t>(a.slots_before(a.part_blocks));
+        };
+        for (int cut = 32; cut < longest[0] || cut < longest[1]; cut = (cut + cut / 4 + 31) / 32 * 32) {
+            set(cut);
+            if (heads * a.head_parts * 64 * d * sizeof(float) > kPartBytes) continue;
+            const double t = estimate(cut);
             if (t < least) {
                 least = t;
                 best = cut;
@@ -164,19 +214,13 @@ inline BwdArgs make_args(bool f32, int B, int Tq, int Tk, int Hq, int Hkv, int d
         }
         a.sliced = best > 0;
         if (a.sliced) {
-            a.slice_rows = best;
-            if (window) a.long_blocks = (sinks + kKeys - 1) / kKeys;
-            int most[2] = {1, 1};
-            for (int j = 0; j < a.key_blocks; ++j) {
-                const int cuts = list(j) > 0 ? (list(j) - 1) / best + 1 : 1;
-                if (cuts > most[j < a.long_blocks]) most[j < a.long_blocks] = cuts;
-            }
-            a.slices = most[0];
-            a.long_slices = most[1];
-            a.slots = a.slices > 1 ? a.slices : 0;
-            a.long_slots = a.long_slices > 1 ? a.long_slices : 0;
-            a.long_tiles = 4 * a.long_blocks < tiles ? 4 * a.long_blocks : tiles;
-            a.part_tiles = a.slots ? tiles : a.long_slots ? a.long_tiles : 0;
+            set(best);
+            a.part_tiles = 4 * a.part_blocks < tiles ? 4 * a.part_blocks : tiles;
+            a.part_step = 4;
+        } else {
+            set(a.rows);
+            a.long_blocks = a.part_blocks = 0;
+            a.head_parts = 0;
         }
     }
     // Sink segments: one wave per SIMD, no segment under 128 rows.
@@ -185,10 +229,23 @@ inline BwdArgs make_args(bool f32, int B, int Tq, int Tk, int Hq, int Hkv, int d
         const long long even = heads * a.sink_tiles * a.rows / 1024;
         a.seg_rows = static_cast<int>(even < 128 ? 128 : even > a.rows ? a.rows : (even + 31) / 32 * 32);
         a.segs = (a.rows + a.seg_rows - 1) / a.seg_rows;
-        a.part_tiles = a.long_tiles = a.sink_tiles;
-        a.long_slots = 1 + a.segs;
+        a.part_tiles = a.sink_tiles;
+        a.part_step = 1;
+        a.head_parts = static_cast<size_t>(a.part_tiles) * (1 + a.segs);
     }
     return a;
+}
+
+// Floats of the workspace, and where its pieces are in one that begins at ws.
+inline size_t workspace_floats(const BwdArgs& a) {
+    const size_t heads = static_cast<size_t>(a.B) * a.Hkv;
+    return heads * 2 * a.pitch + (a.sliced ? kSliced : 0) + heads * a.head_parts * 64 * a.d;
+}
+inline void set_workspace(BwdArgs& a, float* ws) {
+    a.stats = ws;
+    ws += static_cast<size_t>(a.B) * a.Hkv * 2 * a.pitch;
+    a.slots = reinterpret_cast<int*>(ws);
+    a.part = ws + (a.sliced ? kSliced : 0);
 }
 
 }  // namespace attn

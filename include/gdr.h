@@ -446,6 +446,10 @@ int gdr_attn_prefill_varlen(int dtype, int N, int total_q, int total_k, int max_
  * grad_k and grad_v sum over the query heads of a key head.  A query that sees
  * no key has a zero gradient, and so has a key that no query sees.  Returns a
  * GDR_* status.
+ *
+ * The workspace holds 8 bytes for each query and head and, where a key's rows are
+ * cut to fill the GPU, 2 KiB and partial gradients: at most 256 MiB, or 32 MiB and
+ * twice the gradients of the sink keys in fp32 where that is more.
  */
 int gdr_attn_backward(int dtype, int B, int Tq, int Tk, int Hq, int Hkv, int d, int window, int sinks,
                       float scale, const void* q, const void* k, const void* v, const void* o,

@@ -98,6 +98,53 @@ void check_cover(Case c) {
         }
 }
 
+// The parts of the key tiles that have any lie apart from each other and inside the workspace, which is bounded.
+void check_parts(Case c) {
+    const BwdArgs a = plan(c);
+    const long long heads = static_cast<long long>(c.B) * c.Hkv;
+    const double bytes = static_cast<double>(heads) * a.head_parts * 64 * c.d * 4;
+    const double sinks = 2.0 * heads * ((c.sinks + 31) / 32) * 64 * c.d * 4 + (32 << 20);
+    if (bytes > std::max(256.0 * (1 << 20), sinks)) fail(c, "workspace of the parts", static_cast<long long>(bytes));
+    if (c.Tq > 3000 || c.Tk > 5000) return;
+    std::vector<long long> used(heads * a.head_parts, -1);
+    if (a.sliced && a.part_blocks > kSliced) fail(c, "slots of too many blocks");
+    auto at_of = [&](int head, int tile, int slot) {  // as part_of has it
+        return static_cast<long long>(head * a.head_parts + (a.sliced ? 4 * static_cast<size_t>(a.slots_before(tile >> 2) + slot) + (tile & 3)
+                                                                      : static_cast<size_t>(tile) * (1 + a.segs) + slot));
+    };
+    auto take = [&](int head, int tile, int slot, bool read) {
+        const long long at = at_of(head, tile, slot);
+        if (tile >= a.part_tiles || at < 0 || at >= static_cast<long long>(used.size())) return fail(c, "part out of range", tile, slot);
+        const long long me = (static_cast<long long>(head) * a.part_tiles + tile) * 100000 + slot;
+        if (read ? used[at] != me : used[at] >= 0) fail(c, "part of another", tile, slot);
+        used[at] = me;
+        if (at - at_of(head, tile, 0) != static_cast<long long>(slot) * a.part_step) fail(c, "distance of parts", tile, slot);
+    };
+    for (int bid = 0; bid < heads * a.cuts(); ++bid)
+        for (int wave = 0; wave < kWaves; ++wave) {
+            const Piece p = piece_of<kWaves>(a, bid, wave);
+            if (p.j0 < a.Tk && (p.cut == 0 || p.lo < p.hi) && (p.parts || p.tile < a.sink_tiles)) take(p.head, p.tile, p.cut, false);
+        }
+    for (int bid = 0; bid < heads * a.sink_tiles * a.segs; ++bid) {
+        const Piece p = piece_of<1>(a, bid, 0);
+        if (p.lo < p.hi) take(p.head, p.tile, 1 + p.cut, false);
+    }
+    // what the join reads: as many parts as a tile's list has slices, from the first
+    for (int head = 0; head < heads; ++head)
+        for (int tile = 0; tile < a.part_tiles; ++tile) {
+            const int m0 = 32 * tile / kKeys * kKeys;
+            int lo, hi, n = 1;
+            rows_of(a, m0, std::min(m0 + kKeys, a.Tk) - 1, lo, hi);
+            if (a.sliced) {
+                const int size = slice_of(a, hi - lo);
+                n = hi - lo <= size ? 0 : (hi - lo - 1) / size + 1;
+            } else if (a.segs && a.rows > hi) {
+                n += (a.rows - hi - 1) / a.seg_rows + 1;
+            }
+            for (int slot = 0; slot < n; ++slot) take(head, tile, slot, true);
+        }
+}
+
 unsigned long long state = 1;
 int pick(int n) {
     state = state * 6364136223846793005ULL + 1442695040888963407ULL;
@@ -116,7 +163,16 @@ int main() {
         {0, 1, (1 << 29) - 1, (1 << 29) - 1, 1, 1, 128, 7, 1 << 28},
         {0, 1, 1 << 16, 1 << 26, 1 << 12, 4, 64, 1 << 20, 77},
     };
-    for (const Case& c : large) check_lists(c);
+    for (const Case& c : large) {
+        check_lists(c);
+        check_parts(c);
+    }
+    // few heads and long sequences, where lists are sliced, up to and past the 512 key blocks
+    for (int T : {300, 4096, 16384, 65408, 65536})
+        for (int g : {1, 8, 32, 128})
+            for (int hkv : {1, 2, 8})
+                for (int window : {0, 64, 4096})
+                    for (int sinks : {0, 4, 5000}) check_parts({g == 8, 1, T, T, g * hkv, hkv, 128, window, sinks});
     const int group[] = {1, 1, 2, 3, 4, 5, 8, 16, 40};
     for (int i = 0; i < 700; ++i) {
         Case c{};
@@ -131,6 +187,7 @@ int main() {
         c.sinks = pick(3) == 0 ? pick(1 + c.Tk) : pick(6);
         check_lists(c);
         check_cover(c);
+        check_parts(c);
     }
     if (failures) {
         fprintf(stderr, "%d checks failed\n", failures);

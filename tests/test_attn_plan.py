@@ -11,6 +11,8 @@ import subprocess
 
 import pytest
 
+import gated_delta_rule_08_amd as gdr
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "gated_delta_rule_08_amd", "csrc")
 
@@ -28,3 +30,22 @@ def test_backward_plan(tmp_path):
     r = subprocess.run([exe], capture_output=True, text=True, timeout=300,
                        env=dict(os.environ, UBSAN_OPTIONS="print_stacktrace=1"))
     assert r.returncode == 0 and "all checks passed" in r.stdout, r.stdout + r.stderr
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(gdr.library_path()):
+        from gated_delta_rule_08_amd import build
+        build.build()
+    return gdr.load_library()
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (8, 1), (32, 1), (32, 2), (32, 8)])
+def test_backward_workspace_is_bounded(lib, dtype, Hq, Hkv):
+    """Partial gradients take at most 256 MiB beside the 8 bytes of statistics for each query and head (and 2 KiB), on both sides of
+    512 key blocks (65408 keys of one head), without and with a window."""
+    for T in (300, 4096, 16384, 32768, 65408, 65409, 65500, 131072):
+        for window in (0, 64, 4096):
+            need = lib.gdr_attn_backward_workspace_bytes(dtype, 1, T, T, Hq, Hkv, 128, window, 0)
+            assert 8 * T * Hq <= need <= 8 * (T * Hq + 4 * Hkv) + 2048 + (256 << 20), (T, window, need)
