@@ -3,6 +3,7 @@
 #include <limits.h>
 #include <stdint.h>
 
+#include "attn_backward_plan.h"
 #include "gdr_internal.h"
 
 namespace {
@@ -48,6 +49,12 @@ int page_checks(int Hkv, int page_size, int num_pages, int max_pages) {
 // A window that reaches past the first key hides nothing.
 inline int clamp_window(int window, int keys) { return window >= keys ? 0 : window; }
 inline int clamp_sinks(int sinks, int window, int keys) { return window == 0 ? 0 : sinks < keys ? sinks : keys; }
+
+// The backward's plan for arguments that passed the checks.
+gdr::attn::BwdArgs backward_plan(int dtype, int B, int Tq, int Tk, int Hq, int Hkv, int d, int window, int sinks, float scale) {
+    window = clamp_window(window, Tk);
+    return gdr::attn::make_args(dtype == GDR_DTYPE_F32, B, Tq, Tk, Hq, Hkv, d, window, clamp_sinks(sinks, window, Tk), scale);
+}
 
 }  // namespace
 
@@ -96,9 +103,7 @@ size_t gdr_attn_backward_workspace_bytes(int dtype, int B, int Tq, int Tk, int H
     if (common_checks(dtype, Hq, Hkv, d, window, sinks) != GDR_OK || B < 0 || Tq < 0 || Tk < 0 ||
         !sizes_ok(B, Tq, Hq, d) || !sizes_ok(B, Tk, Hkv, d) || B == 0 || Hq == 0 || Tq == 0)
         return 0;
-    window = clamp_window(window, Tk);
-    return gdr::attn_backward_workspace_floats(dtype, B, Tq, Tk, Hq, Hkv, d, window, clamp_sinks(sinks, window, Tk)) *
-           sizeof(float);
+    return gdr::attn::workspace_floats(backward_plan(dtype, B, Tq, Tk, Hq, Hkv, d, window, sinks, 1.f)) * sizeof(float);
 }
 
 int gdr_attn_backward(int dtype, int B, int Tq, int Tk, int Hq, int Hkv, int d, int window, int sinks, float scale,
@@ -108,19 +113,20 @@ int gdr_attn_backward(int dtype, int B, int Tq, int Tk, int Hq, int Hkv, int d, 
     const int st = common_checks(dtype, Hq, Hkv, d, window, sinks);
     if (st != GDR_OK) return st;
     if (B < 0 || Tq < 0 || Tk < 0 || !sizes_ok(B, Tq, Hq, d) || !sizes_ok(B, Tk, Hkv, d)) return GDR_ERR_BAD_SHAPE;
-    const size_t need = gdr_attn_backward_workspace_bytes(dtype, B, Tq, Tk, Hq, Hkv, d, window, sinks);
+    if (B == 0 || Hq == 0) return GDR_OK;
+    gdr::attn::BwdArgs plan = backward_plan(dtype, B, Tq, Tk, Hq, Hkv, d, window, sinks, scale);
+    const size_t need = Tq > 0 ? gdr::attn::workspace_floats(plan) * sizeof(float) : 0;
     if (workspace_bytes < need || (need > 0 && !workspace)) return GDR_ERR_WORKSPACE;
-    if (B == 0 || Hq == 0 || (Tq == 0 && Tk == 0)) return GDR_OK;
+    if (Tq == 0 && Tk == 0) return GDR_OK;
     if (Tq > 0 && (!q || !o || !lse || !grad_o || !grad_q)) return GDR_ERR_NULL_PTR;
     if (Tk > 0 && (!k || !v || !grad_k || !grad_v)) return GDR_ERR_NULL_PTR;
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(grad_o, 16) ||
         !aligned(grad_q, 16) || !aligned(grad_k, 16) || !aligned(grad_v, 16) || !aligned(workspace, 16) ||
         !aligned(lse, 4))
         return GDR_ERR_MISALIGNED;
-    window = clamp_window(window, Tk);
-    return status_of(gdr::launch_attn_backward(dtype, B, Tq, Tk, Hq, Hkv, d, window, clamp_sinks(sinks, window, Tk),
-                                               scale, q, k, v, o, lse, grad_o, grad_q, grad_k, grad_v,
-                                               static_cast<float*>(workspace), static_cast<hipStream_t>(stream)));
+    gdr::attn::set_workspace(plan, static_cast<float*>(workspace));
+    return status_of(gdr::launch_attn_backward(dtype, plan, q, k, v, o, lse, grad_o, grad_q, grad_k, grad_v,
+                                               static_cast<hipStream_t>(stream)));
 }
 
 size_t gdr_attn_decode_workspace_bytes(int dtype, int B, int Hq, int Hkv, int d, int page_size, int max_pages,

@@ -602,18 +602,10 @@ hipError_t launch(const BwdArgs& a, const void* q_, const void* k_, const void* 
 }  // namespace
 }  // namespace attn
 
-size_t attn_backward_workspace_floats(int dtype, int B, int Tq, int Tk, int Hq, int Hkv, int d, int window, int sinks) {
-    return attn::workspace_floats(attn::make_args(dtype == GDR_DTYPE_F32, B, Tq, Tk, Hq, Hkv, d, window, sinks, 1.f));
-}
-
-hipError_t launch_attn_backward(int dtype, int B, int Tq, int Tk, int Hq, int Hkv, int d, int window, int sinks,
-                                float scale, const void* q, const void* k, const void* v, const void* o,
-                                const float* lse, const void* go, void* gq, void* gk, void* gv, float* ws,
-                                hipStream_t st) {
-    attn::BwdArgs a = attn::make_args(dtype == GDR_DTYPE_F32, B, Tq, Tk, Hq, Hkv, d, window, sinks, scale);
-    attn::set_workspace(a, ws);
-    auto* f = dtype == GDR_DTYPE_F32 ? (d == 64 ? attn::launch<float, 64> : attn::launch<float, 128>)
-                                     : (d == 64 ? attn::launch<bf16_t, 64> : attn::launch<bf16_t, 128>);
+hipError_t launch_attn_backward(int dtype, const attn::BwdArgs& a, const void* q, const void* k, const void* v, const void* o,
+                                const float* lse, const void* go, void* gq, void* gk, void* gv, hipStream_t st) {
+    auto* f = dtype == GDR_DTYPE_F32 ? (a.d == 64 ? attn::launch<float, 64> : attn::launch<float, 128>)
+                                     : (a.d == 64 ? attn::launch<bf16_t, 64> : attn::launch<bf16_t, 128>);
     return f(a, q, k, v, o, lse, go, gq, gk, gv, st);
 }
 

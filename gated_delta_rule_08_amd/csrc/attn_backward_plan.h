@@ -169,33 +169,53 @@ inline BwdArgs make_args(bool f32, int B, int Tq, int Tk, int Hq, int Hkv, int d
             rows_of(a, j * kKeys, (j + 1) * kKeys < Tk ? (j + 1) * kKeys - 1 : Tk - 1, lo, hi);
             return hi - lo;
         };
-        auto estimate = [&](int cut) {  // cut 0: no slices
-            long long total = 0, pieces = 0, parts = 0;
-            int longest = 0;
-            for (int j = 0; j < a.key_blocks; ++j) {
-                const int n = list(j), here = cut && n > cut ? (n - 1) / cut + 1 : 1;
-                total += n;
-                pieces += here;
-                if (here > 1) parts += here;
-                if (n > longest) longest = n;
-            }
-            const double most = cut && cut < longest ? cut : longest, even = static_cast<double>(total) * heads / 256 + most / 2;
+        // The lists that slices are cut from, as groups of neighbouring blocks each as
+        // long as its middle one's: at most 64 with sinks and 64 without, so that the
+        // search takes a few microseconds whatever the length (60000 keys under a window
+        // of 256: 3 us of the host, 18 block by block).
+        int len[128], of[128], groups_n = 0, longest[2] = {0, 0};  // longest: without and with sinks
+        auto time_of = [&](long long total, long long pieces, long long parts, int most_rows, int cut) {
+            const double most = cut && cut < most_rows ? cut : most_rows, even = static_cast<double>(total) * heads / 256 + most / 2;
             const double ends = cut ? 96.0 * pieces * heads / 256 : 96.0;
             const bool once = f32 && cut && pieces * heads <= 224;
             return row * ((most > even || once ? most : even) + ends) + (parts ? 4 + part * parts * heads : 0);
         };
-        double least = estimate(0);
+        long long total = 0;
+        for (int j = 0; j < a.key_blocks; ++j) {
+            const int n = list(j);
+            total += n;
+            if (n > longest[0]) longest[0] = n;
+        }
+        int best = 0;
+        double least = time_of(total, 0, 0, longest[0], 0);
         if (sunk) {  // the segments' kernel and join
             const double even = static_cast<double>(heads) * ((sinks + 31) / 32) * a.rows / 1024;
             least += 8 + 0.13 * (even > 128 ? even : 128) * (f32 ? 5 : 1);
         }
         a.sliced = true;
         if (window) a.long_blocks = (sinks + kKeys - 1) / kKeys;
-        int longest[2] = {0, 0}, best = 0;  // lists, of blocks without and with sinks
-        for (int j = 0; j < a.key_blocks; ++j) {
-            int& most = longest[j < a.long_blocks];
-            if (list(j) > most) most = list(j);
+        total = longest[0] = 0;
+        for (int sunken = 1; sunken >= 0; --sunken) {
+            const int from = sunken ? 0 : a.long_blocks, end = sunken ? a.long_blocks : a.key_blocks, step = (end - from + 63) / 64;
+            for (int j = from; j < end; j += step) {
+                const int here = step < end - j ? step : end - j, n = list(j + here / 2);
+                len[groups_n] = n;
+                of[groups_n++] = here;
+                total += static_cast<long long>(n) * here;
+            }
+            for (int j = from; j < end; ++j)
+                if (list(j) > longest[sunken]) longest[sunken] = list(j);
         }
+        const int most_rows = longest[0] > longest[1] ? longest[0] : longest[1];
+        auto estimate = [&](int cut) {
+            long long pieces = 0, parts = 0;
+            for (int i = 0; i < groups_n; ++i) {
+                const int here = len[i] > cut ? (len[i] - 1) / cut + 1 : 1;
+                pieces += here * of[i];
+                if (here > 1) parts += here * of[i];
+            }
+            return time_of(total, pieces, parts, most_rows, cut);
+        };
         auto set = [&](int cut) {
             a.slice_rows = cut;
             a.slices = longest[0] > cut ? (longest[0] - 1) / cut + 1 : 1;
@@ -203,7 +223,7 @@ inline BwdArgs make_args(bool f32, int B, int Tq, int Tk, int Hq, int Hkv, int d
             a.part_blocks = a.slices > 1 ? a.key_blocks : a.long_slices > 1 ? a.long_blocks : 0;
             a.head_parts = 4 * static_cast<size_t>(a.slots_before(a.part_blocks));
         };
-        for (int cut = 32; cut < longest[0] || cut < longest[1]; cut = (cut + cut / 4 + 31) / 32 * 32) {
+        for (int cut = 32; cut < most_rows; cut = (cut + cut / 4 + 31) / 32 * 32) {
             set(cut);
             if (heads * a.head_parts * 64 * d * sizeof(float) > kPartBytes) continue;
             const double t = estimate(cut);

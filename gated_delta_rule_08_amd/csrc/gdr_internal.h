@@ -138,11 +138,11 @@ hipError_t launch_attn_prefill(int dtype, int B, int Tq, int Tk, int Hq, int Hkv
                                float scale, const void* q, const void* k, const void* v, void* o, float* lse,
                                hipStream_t s, const AttnPacked& pk = AttnPacked());
 
-size_t attn_backward_workspace_floats(int dtype, int B, int Tq, int Tk, int Hq, int Hkv, int d, int window, int sinks);
-hipError_t launch_attn_backward(int dtype, int B, int Tq, int Tk, int Hq, int Hkv, int d, int window, int sinks,
-                                float scale, const void* q, const void* k, const void* v, const void* o,
-                                const float* lse, const void* go, void* gq, void* gk, void* gv, float* ws,
-                                hipStream_t s);
+namespace attn {
+struct BwdArgs;  // attn_backward_plan.h
+}
+hipError_t launch_attn_backward(int dtype, const attn::BwdArgs& plan, const void* q, const void* k, const void* v, const void* o,
+                                const float* lse, const void* go, void* gq, void* gk, void* gv, hipStream_t s);
 size_t attn_decode_workspace_floats(int Hq, int Hkv, int d, int page_size, int max_pages, int window, int sinks);
 hipError_t launch_attn_decode(int dtype, int B, int Hq, int Hkv, int d, int page_size, int num_pages, int max_pages,
                               int window, int sinks, float scale, const void* q, const void* k, const void* v,

@@ -8,6 +8,7 @@ It is built without device code, with UndefinedBehaviorSanitizer.
 import os
 import shutil
 import subprocess
+import time
 
 import pytest
 
@@ -49,3 +50,19 @@ def test_backward_workspace_is_bounded(lib, dtype, Hq, Hkv):
         for window in (0, 64, 4096):
             need = lib.gdr_attn_backward_workspace_bytes(dtype, 1, T, T, Hq, Hkv, 128, window, 0)
             assert 8 * T * Hq <= need <= 8 * (T * Hq + 4 * Hkv) + 2048 + (256 << 20), (T, window, need)
+
+
+def test_planning_does_not_grow_with_the_length(lib):
+    """The plan is formed on the host in every call: 469 key blocks take at most five times as long as 32 (twice
+    here; block by block eleven times)."""
+    def us(*shape):
+        times = []
+        for _ in range(40):
+            t0 = time.perf_counter()
+            for _ in range(25):
+                lib.gdr_attn_backward_workspace_bytes(*shape)
+            times.append(time.perf_counter() - t0)
+        return min(times) / 25 * 1e6
+
+    short, long = us(1, 1, 4096, 4096, 32, 8, 128, 0, 0), us(1, 1, 60000, 60000, 8, 1, 128, 256, 0)
+    assert long <= 5 * short, (short, long)
