@@ -79,10 +79,9 @@ int gdr_attn_prefill_varlen(int dtype, int N, int total_q, int total_k, int max_
                             const int* cu_k, void* o, float* lse, void* stream) {
     const int st = common_checks(dtype, Hq, Hkv, d, window, sinks);
     if (st != GDR_OK) return st;
-    if (N < 0 || total_q < 0 || total_k < 0 || max_q < 0 || !sizes_ok(1, total_q, Hq, d) ||
-        !sizes_ok(1, total_k, Hkv, d) || !sizes_ok(N, max_q, Hq, 1))
-        return GDR_ERR_BAD_SHAPE;
-    if (max_q > total_q) max_q = total_q;
+    if (N < 0 || total_q < 0 || total_k < 0 || max_q < 0) return GDR_ERR_BAD_SHAPE;
+    if (max_q > total_q) max_q = total_q;  // a bound may be loose
+    if (!sizes_ok(1, total_q, Hq, d) || !sizes_ok(1, total_k, Hkv, d) || !sizes_ok(N, max_q, Hq, 1)) return GDR_ERR_BAD_SHAPE;
     if (N == 0 || max_q == 0 || Hq == 0) return GDR_OK;
     if (!q || !o || !cu_q || !cu_k || (total_k > 0 && (!k || !v))) return GDR_ERR_NULL_PTR;
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(lse, 4) ||
