@@ -9,6 +9,7 @@ built, importing works but every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -517,6 +518,14 @@ def _attn_launch(dev: int, stream, fn, *args) -> None:
         _check(status)
 
 
+def _on_stream(dev: int, stream):
+    """The call's stream as the current one, for torch's own work on its tensors."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else
+                             torch.cuda.ExternalStream(int(stream), device=dev))
+
+
 def _attn_types(q, *ts) -> int:
     """The dtype code of q, which every other tensor shares."""
     dtype = q.dtype
@@ -584,7 +593,7 @@ def gdr_attn_prefill_varlen(q, k, v, cu_q, cu_k, o, lse=None, max_seqlen_q: Opti
     """:func:`gdr_attn_prefill` of packed sequences: q, o [total_q,Hq,d], k, v
     [total_k,Hkv,d], lse [total_q,Hq]; cu_q and cu_k [N+1] are int32 device
     offsets.  max_seqlen_q bounds every sequence's queries; if None it is read
-    from cu_q (one device-to-host copy)."""
+    from cu_q (one device-to-host copy on the call's stream)."""
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q must be [total_q,Hq,d], k and v [total_k,Hkv,d]")
     total_q, Hq, d = shape = q.shape
@@ -602,7 +611,8 @@ def gdr_attn_prefill_varlen(q, k, v, cu_q, cu_k, o, lse=None, max_seqlen_q: Opti
         raise ValueError("lse must be fp32 [total_q,Hq]")
     dev = _attn_device(q, k, v, cu_q, cu_k, o, lse)
     if max_seqlen_q is None:
-        cu = cu_q.cpu()
+        with _on_stream(dev, stream):  # cu_q may be this stream's work
+            cu = cu_q.cpu()
         max_seqlen_q = int((cu[1:] - cu[:-1]).max().clamp(min=0)) if N > 0 else 0
     _attn_launch(dev, stream, load_library().gdr_attn_prefill_varlen, code, N, total_q, total_k, max_seqlen_q, Hq, Hkv, d,
                  _attn_int(window), _attn_int(sinks), d ** -0.5 if scale is None else scale, q.data_ptr(), k.data_ptr(), v.data_ptr(),
