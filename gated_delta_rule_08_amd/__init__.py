@@ -544,8 +544,9 @@ def _attn_heads(Hq: int, Hkv: int) -> None:
 
 
 def _attn_int(x: int) -> int:
-    """A window or sink count as a C int: anything larger hides nothing either."""
-    return x if x < 0x7fffffff else 0x7fffffff
+    """x as a C int, of which ctypes would drop the bits above 32: a window, a sink count or a bound beyond it
+    says the same as the largest, a size beyond it is refused as that is, and anything negative as -1 is."""
+    return -1 if x < 0 else x if x < 0x7fffffff else 0x7fffffff
 
 
 def _int32(name, t, shape) -> None:
@@ -614,15 +615,15 @@ def gdr_attn_prefill_varlen(q, k, v, cu_q, cu_k, o, lse=None, max_seqlen_q: Opti
         with _on_stream(dev, stream):  # cu_q may be this stream's work
             cu = cu_q.cpu()
         max_seqlen_q = int((cu[1:] - cu[:-1]).max().clamp(min=0)) if N > 0 else 0
-    _attn_launch(dev, stream, load_library().gdr_attn_prefill_varlen, code, N, total_q, total_k, max_seqlen_q, Hq, Hkv, d,
+    _attn_launch(dev, stream, load_library().gdr_attn_prefill_varlen, code, N, total_q, total_k, _attn_int(max_seqlen_q), Hq, Hkv, d,
                  _attn_int(window), _attn_int(sinks), d ** -0.5 if scale is None else scale, q.data_ptr(), k.data_ptr(), v.data_ptr(),
                  cu_q.data_ptr(), cu_k.data_ptr(), o.data_ptr(), None if lse is None else lse.data_ptr())
 
 
 def gdr_attn_backward_workspace_bytes(dtype, B: int, Tq: int, Tk: int, Hq: int, Hkv: int, d: int, window: int = 0,
                                       sinks: int = 0) -> int:
-    return int(load_library().gdr_attn_backward_workspace_bytes(_DTYPES[dtype], B, Tq, Tk, Hq, Hkv, d,
-                                                                _attn_int(window), _attn_int(sinks)))
+    return int(load_library().gdr_attn_backward_workspace_bytes(
+        _DTYPES[dtype], *map(_attn_int, (B, Tq, Tk, Hq, Hkv, d, window, sinks))))
 
 
 def gdr_attn_backward(q, k, v, o, lse, grad_o, grad_q, grad_k, grad_v, window: int = 0, sinks: int = 0,
@@ -665,8 +666,8 @@ def _page_checks(k_pages, v_pages, page_table, Hkv, d, N):
 
 def gdr_attn_decode_workspace_bytes(dtype, B: int, Hq: int, Hkv: int, d: int, page_size: int, max_pages: int,
                                     window: int = 0, sinks: int = 0) -> int:
-    return int(load_library().gdr_attn_decode_workspace_bytes(_DTYPES[dtype], B, Hq, Hkv, d, page_size, max_pages,
-                                                              _attn_int(window), _attn_int(sinks)))
+    return int(load_library().gdr_attn_decode_workspace_bytes(
+        _DTYPES[dtype], *map(_attn_int, (B, Hq, Hkv, d, page_size, max_pages, window, sinks))))
 
 
 def gdr_attn_decode(q, k, v, k_pages, v_pages, page_table, lengths, o, window: int = 0, sinks: int = 0,

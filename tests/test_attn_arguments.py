@@ -4,6 +4,7 @@ import ctypes
 import os
 
 import pytest
+import torch
 
 import gated_delta_rule_08_amd as gdr
 
@@ -29,3 +30,41 @@ def test_a_loose_bound_of_the_queries_is_no_error(lib):
         assert call(mq) == NULL, mq  # past the sizes, at the missing q
         assert call(mq, tq=0) == OK, mq
     assert call(-1) == SHAPE and call(BIG, tq=BIG) == SHAPE
+
+
+def test_integers_beyond_32_bits_keep_their_meaning(lib):
+    """A window far beyond the keys is no window, one far below 0 is refused; neither becomes its low 32 bits."""
+    size = gdr.gdr_attn_backward_workspace_bytes
+    args = (torch.bfloat16, 1, 9000, 9000, 8, 2, 64)
+    full, narrow = size(*args), size(*args, 1000)
+    assert full > 0 and narrow > 0 and full != narrow
+    for window in (9000, BIG, 2 ** 32 + 1000, 2 ** 40):
+        assert size(*args, window) == full, window
+    for window in (-1, -2 ** 31, -2 ** 32, -2 ** 32 + 1000, -2 ** 40):
+        assert size(*args, window) == 0, window
+    assert size(*args, 1000, -2 ** 32) == 0
+    for i in range(1, 7):  # sizes
+        assert size(*args[:i], 2 ** 32 + args[i], *args[i + 1:]) == 0, i
+    pages = (torch.bfloat16, 2, 8, 2, 64, 16, 1024)
+    assert gdr.gdr_attn_decode_workspace_bytes(*pages) > 0
+    for i in range(1, 7):
+        assert gdr.gdr_attn_decode_workspace_bytes(*pages[:i], 2 ** 32 + pages[i], *pages[i + 1:]) == 0, i
+    assert gdr._attn_int(2 ** 32 + 5) == BIG and gdr._attn_int(-2 ** 32 + 5) == -1 and gdr._attn_int(5) == 5
+
+
+def test_calls_pass_their_integers_whole(monkeypatch):
+    """What the binding hands to the library for the window, the sinks and the bound of a packed call."""
+    seen = []
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *args: seen.append((name, args)) or 0
+
+    monkeypatch.setattr(gdr, "load_library", Lib)
+    monkeypatch.setattr(gdr, "_attn_device", lambda *ts: 0)
+    monkeypatch.setattr(gdr, "_attn_launch", lambda dev, stream, fn, *args: fn(*args))
+    q, k, o = torch.zeros(8, 4, 64), torch.zeros(8, 2, 64), torch.zeros(8, 4, 64)
+    cu = torch.tensor([0, 8], dtype=torch.int32)
+    gdr.gdr_attn_prefill_varlen(q, k, k, cu, cu, o, max_seqlen_q=2 ** 32 + 2, window=-2 ** 32, sinks=2 ** 33)
+    name, args = seen.pop()
+    assert name == "gdr_attn_prefill_varlen" and args[4] == BIG and args[8] == -1 and args[9] == BIG
