@@ -168,7 +168,7 @@ def _workspace(need: int, device, stream):
         return None
     ws = torch.empty(need, dtype=torch.uint8, device=device)
     if stream is not None:
-        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=device)
         if s.cuda_stream != torch.cuda.current_stream(device).cuda_stream:
             ws.record_stream(s)
     return ws

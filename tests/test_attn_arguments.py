@@ -68,3 +68,27 @@ def test_calls_pass_their_integers_whole(monkeypatch):
     gdr.gdr_attn_prefill_varlen(q, k, k, cu, cu, o, max_seqlen_q=2 ** 32 + 2, window=-2 ** 32, sinks=2 ** 33)
     name, args = seen.pop()
     assert name == "gdr_attn_prefill_varlen" and args[4] == BIG and args[8] == -1 and args[9] == BIG
+
+
+def test_a_workspace_is_recorded_on_the_stream_of_its_own_device(monkeypatch):
+    """A stream given as a handle belongs to the tensors' device, whichever device is current."""
+    made = []
+
+    class Stream:
+        cuda_stream = 77
+
+    class Tensor:
+        def record_stream(self, s):
+            made.append("recorded")
+
+    def external(handle, device=None):
+        made.append((handle, device))
+        return Stream()
+
+    current = type("Current", (), {"cuda_stream": 0})
+    monkeypatch.setattr(torch.cuda, "ExternalStream", external)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: current)
+    monkeypatch.setattr(torch, "empty", lambda *a, **kw: Tensor())
+    device = torch.device("cuda", 1)
+    gdr._workspace(16, device, 77)
+    assert made == [(77, device), "recorded"]
