@@ -510,12 +510,13 @@ size_t gdr_attn_decode_workspace_bytes(int dtype, int B, int Hq, int Hkv, int d,
  *
  *   k, v        [total, Hkv, d]   dtype
  *   cu_seqlens  [N + 1] int32, DEVICE: non-decreasing token offsets; tokens of
- *               no sequence are ignored
+ *               no sequence are ignored.  Out of order, a token goes to its
+ *               place in one of the sequences whose ranges hold it, or nowhere.
  *   lengths, page_table, pages as above (N sequences)
  *
  * A token of a sequence with a negative length, or whose position is beyond the
- * table row or on a page outside [0, num_pages), is not written.  Two tokens with the same place race.
- * Returns a GDR_* status.
+ * table row or on a page outside [0, num_pages), is not written.  Two tokens
+ * with the same place race.  Returns a GDR_* status.
  */
 int gdr_attn_append(int dtype, int N, int total, int Hkv, int d, int page_size, int num_pages, int max_pages,
                     const void* k, const void* v, const int* cu_seqlens, const int* lengths, void* k_pages,
