@@ -259,8 +259,10 @@ template <int D> struct ColRead<float, D> {
 // They are written as assembly because the compiler would wait for a copy
 // before any later LDS read that it cannot tell apart from it, which is every
 // read of the other buffer: the kernels wait themselves (vmcnt, before the
-// barrier or the read that needs the copy).  They return nothing in registers;
-// M0, the destination, serves no other instruction of these kernels.
+// barrier or the read that needs the copy).  They return nothing in registers.
+// M0, the destination, is a reserved register that the compiler takes no clobber
+// for; nothing else in these kernels uses it (tests/test_attn_m0.py reads the
+// compiled code).
 // lds: wave-uniform byte address in LDS (lds_addr).
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {
     return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const void*)p));
