@@ -115,8 +115,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && WAVES == 4 ? 2 : 1) v
                                                              const T* __restrict__ go, T* __restrict__ gk,
                                                              T* __restrict__ gv) {
     using C = DkdvCfg<T, D, WAVES>;
-    using L = Tile<T, D>;
-    constexpr int KS = D / 16, DT = D / 32, BM = C::BM, NM = BM / 32;
+    constexpr int KS = D / 16, DT = D / 32, BM = C::BM;
     constexpr bool kSeg = WAVES == 1;
     extern __shared__ unsigned char smem[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h2 = lane >> 5;
@@ -164,12 +163,12 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && WAVES == 4 ? 2 : 1) v
     const T *qp = q + low + from * qstep, *gp = go + low + from * qstep;
     auto fetch = [&](int i) {
         const uint32_t buf = lds_addr(smem) + (i & 1) * C::kBuf;
-        const uint32_t st = lds_addr(smem) + C::kStat + (i & 1) * C::kStatBuf + 256 * wave;
+        const uint32_t st = lds_addr(smem) + C::kStat + (i & 1) * C::kStatBuf;
         const int r0 = lo + BM * next;
         if (even && r0 + BM <= a.rows) {
             copy.run(buf, qp);
             copy.run(buf + C::kTile, gp);
-            if (wave < NM) copy_words(st, stat + r0, (again(lane) < 32 ? 0u : 4u * a.pitch) + 4u * (32 * wave + (again(lane) & 31)));  // lanes 0..31: lse2, 32..63: delta
+            if (wave == 0) copy_words(st, stat + r0, (again(lane) < 32 ? 0u : 4u * a.pitch) + 4u * (again(lane) & 31));  // lanes 0..31: lse2, 32..63: delta
         } else {
             auto row = [&](int r) {
                 r = min(r0 + r, a.rows - 1);
@@ -178,7 +177,7 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && WAVES == 4 ? 2 : 1) v
             };
             copy.gather(buf, [&](int r) { return q + row(r); });
             copy.gather(buf + C::kTile, [&](int r) { return go + row(r); });
-            if (wave < NM) copy_words(st, stat + r0, 4u * (h2 * a.pitch + min(32 * wave + (lane & 31), a.rows - 1 - r0)));
+            if (wave == 0) copy_words(st, stat + r0, 4u * (h2 * a.pitch + min(lane & 31, a.rows - 1 - r0)));
         }
         qp -= qstep;
         gp -= qstep;
@@ -206,65 +205,62 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && WAVES == 4 ? 2 : 1) v
         if (r0 + BM <= any_lo || r0 >= any_hi) continue;
         const float* st = reinterpret_cast<const float*>(smem + C::kStat + (i & 1) * C::kStatBuf) + 4 * h2;
         const bool whole = r0 >= whole_lo && r0 + BM <= whole_hi;
+        // P: registers of S as they stand are the B operand of dV
+        f32x16 s = zero16();
 #pragma unroll
-        for (int w = 0; w < NM; ++w) {
-            // P: registers of S as they stand are the B operand of dV
-            f32x16 s = zero16();
-#pragma unroll
-            for (int e = 0; e < KS; ++e) {
-                s = mma32(RowRead<T, D>::get(smem, rb, e, 32 * w * L::kRow), kf[e], s);
-                if (e % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // at most four fragments ahead: no spills
-            }
-#pragma unroll
-            for (int r = 0; r < 16; r += 4) {
-                const f32x4 ls = *reinterpret_cast<const f32x4*>(st + 64 * w + 2 * r);
-#pragma unroll
-                for (int y = 0; y < 4; ++y) s[r + y] = ex2(fmaf(s[r + y], c, -ls[y]));
-            }
-            if (!whole) {  // the lane's key is visible to rows [key_lo, key_hi)
-                const int mine = again(lane), at = j0 + (mine & 31);
-                const int key_lo = rows_to(at), key_hi = a.window == 0 || at < a.sinks ? hi : min(hi, rows_to(at + a.window));
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int row = r0 + 32 * w + row32(r, mine >> 5);
-                    if (row < key_lo || row >= key_hi) s[r] = 0.f;
-                }
-            }
-            __builtin_amdgcn_sched_barrier(0);
-            {
-                frag_t<T> pf[2] = {pack_regs<T>(s, 0), pack_regs<T>(s, 1)};
-#pragma unroll
-                for (int t = 0; t < DT; ++t)
-#pragma unroll
-                    for (int u = 0; u < 2; ++u)
-                        dv[t] = mma32(ColRead<T, D>::get(smem, cb + C::kTile, t, 2 * w + u), pf[u], dv[t]);
-            }
-            __builtin_amdgcn_sched_barrier(0);
-            f32x16 dp = zero16();
-            const int rb2 = again(rb), cb2 = again(cb);
-#pragma unroll
-            for (int e = 0; e < KS; ++e) {
-                dp = mma32(RowRead<T, D>::get(smem, rb2, e, C::kTile + 32 * w * L::kRow), vf[e], dp);
-                if (e % 4 == 3) __builtin_amdgcn_sched_barrier(0);
-            }
-            // dS is 0 where P is, unless dP - delta is not finite: then, as for dV, the
-            // sums become NaN and seen_keys tells hidden pairs from visible ones whose
-            // weight underflowed.
-#pragma unroll
-            for (int r = 0; r < 16; r += 4) {
-                const f32x4 de = *reinterpret_cast<const f32x4*>(st + 64 * w + 32 + 2 * r);
-#pragma unroll
-                for (int y = 0; y < 4; ++y) dp[r + y] = s[r + y] * (dp[r + y] - de[y]);
-            }
-            {
-                frag_t<T> df[2] = {pack_regs<T>(dp, 0), pack_regs<T>(dp, 1)};
-#pragma unroll
-                for (int t = 0; t < DT; ++t)
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) dk[t] = mma32(ColRead<T, D>::get(smem, cb2, t, 2 * w + u), df[u], dk[t]);
-            }
-            __builtin_amdgcn_sched_barrier(0);
+        for (int e = 0; e < KS; ++e) {
+            s = mma32(RowRead<T, D>::get(smem, rb, e, 0), kf[e], s);
+            if (e % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // at most four fragments ahead: no spills
         }
+#pragma unroll
+        for (int r = 0; r < 16; r += 4) {
+            const f32x4 ls = *reinterpret_cast<const f32x4*>(st + 2 * r);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) s[r + y] = ex2(fmaf(s[r + y], c, -ls[y]));
+        }
+        if (!whole) {  // the lane's key is visible to rows [key_lo, key_hi)
+            const int mine = again(lane), at = j0 + (mine & 31);
+            const int key_lo = rows_to(at), key_hi = a.window == 0 || at < a.sinks ? hi : min(hi, rows_to(at + a.window));
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int row = r0 + row32(r, mine >> 5);
+                if (row < key_lo || row >= key_hi) s[r] = 0.f;
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        {
+            frag_t<T> pf[2] = {pack_regs<T>(s, 0), pack_regs<T>(s, 1)};
+#pragma unroll
+            for (int t = 0; t < DT; ++t)
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+                    dv[t] = mma32(ColRead<T, D>::get(smem, cb + C::kTile, t, u), pf[u], dv[t]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        f32x16 dp = zero16();
+        const int rb2 = again(rb), cb2 = again(cb);
+#pragma unroll
+        for (int e = 0; e < KS; ++e) {
+            dp = mma32(RowRead<T, D>::get(smem, rb2, e, C::kTile), vf[e], dp);
+            if (e % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+        }
+        // dS is 0 where P is, unless dP - delta is not finite: then, as for dV, the
+        // sums become NaN and seen_keys tells hidden pairs from visible ones whose
+        // weight underflowed.
+#pragma unroll
+        for (int r = 0; r < 16; r += 4) {
+            const f32x4 de = *reinterpret_cast<const f32x4*>(st + 32 + 2 * r);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) dp[r + y] = s[r + y] * (dp[r + y] - de[y]);
+        }
+        {
+            frag_t<T> df[2] = {pack_regs<T>(dp, 0), pack_regs<T>(dp, 1)};
+#pragma unroll
+            for (int t = 0; t < DT; ++t)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) dk[t] = mma32(ColRead<T, D>::get(smem, cb2, t, u), df[u], dk[t]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
     }
     if (!wave_live) return;
 

@@ -29,12 +29,12 @@ struct BwdArgs {
     int long_slices, slices;  // the others into at most slices
     int sink_tiles, segs;     // not sliced: 32-key tiles that hold sinks, segments of each (at most)
     int seg_rows;
-    // Key tiles whose gradients may come in parts.  Not sliced: the sinks' tiles, room
-    // for 1 + segs parts each.  Sliced: those of the first part_blocks blocks, room for
-    // what each block's list needs; slot s of a block's four tiles lie side by side.
+    // Key tiles whose gradients may come in parts.  Not sliced: the sinks' tiles, 1 +
+    // segs parts each, slot by slot.  Sliced: those of the first part_blocks blocks,
+    // block by block with room for what its list needs, then slot by slot.
     int part_tiles, part_blocks;
-    int part_step;            // tiles from one part of a tile to its next
-    size_t head_parts;        // parts of a head
+    int part_step;            // parts from one of a tile to its next
+    int head_parts;           // parts of a head
     // The workspace: the row statistics, the slots, the parts.
     float* stats;             // [B Hkv, 2, pitch]: lse log2 e, then delta
     int* slots;               // sliced: [512], slots_before each block
@@ -49,9 +49,8 @@ struct BwdArgs {
         return static_cast<int>(rows_before(block) / slice_rows) + block;
     }
     __device__ __forceinline__ float* part_of(int head, int tile, int slot, int d) const {
-        const size_t at = sliced ? 4 * static_cast<size_t>(slots[tile >> 2] + slot) + (tile & 3)
-                                 : static_cast<size_t>(tile) * (1 + segs) + slot;
-        return part + (head * head_parts + at) * 64 * d;
+        const int at = (sliced ? 4 * slots[tile >> 2] : tile & ~3) + slot * part_step + (tile & 3);
+        return part + (static_cast<size_t>(head) * head_parts + at) * 64 * d;
     }
 };
 
@@ -221,11 +220,12 @@ inline BwdArgs make_args(bool f32, int B, int Tq, int Tk, int Hq, int Hkv, int d
             a.slices = longest[0] > cut ? (longest[0] - 1) / cut + 1 : 1;
             a.long_slices = longest[1] > cut ? (longest[1] - 1) / cut + 1 : 1;
             a.part_blocks = a.slices > 1 ? a.key_blocks : a.long_slices > 1 ? a.long_blocks : 0;
-            a.head_parts = 4 * static_cast<size_t>(a.slots_before(a.part_blocks));
+            const long long parts = 4 * (a.rows_before(a.part_blocks) / cut + a.part_blocks);
+            a.head_parts = static_cast<int>(parts < 0x7fffffff ? parts : 0x7fffffff);  // beyond kPartBytes
         };
         for (int cut = 32; cut < most_rows; cut = (cut + cut / 4 + 31) / 32 * 32) {
             set(cut);
-            if (heads * a.head_parts * 64 * d * sizeof(float) > kPartBytes) continue;
+            if (static_cast<size_t>(heads) * a.head_parts * 64 * d * sizeof(float) > kPartBytes) continue;
             const double t = estimate(cut);
             if (t < least) {
                 least = t;
@@ -250,8 +250,8 @@ inline BwdArgs make_args(bool f32, int B, int Tq, int Tk, int Hq, int Hkv, int d
         a.seg_rows = static_cast<int>(even < 128 ? 128 : even > a.rows ? a.rows : (even + 31) / 32 * 32);
         a.segs = (a.rows + a.seg_rows - 1) / a.seg_rows;
         a.part_tiles = a.sink_tiles;
-        a.part_step = 1;
-        a.head_parts = static_cast<size_t>(a.part_tiles) * (1 + a.segs);
+        a.part_step = a.part_tiles;
+        a.head_parts = a.part_tiles * (1 + a.segs);
     }
     return a;
 }

@@ -109,8 +109,8 @@ void check_parts(Case c) {
     std::vector<long long> used(heads * a.head_parts, -1);
     if (a.sliced && a.part_blocks > kSliced) fail(c, "slots of too many blocks");
     auto at_of = [&](int head, int tile, int slot) {  // as part_of has it
-        return static_cast<long long>(head * a.head_parts + (a.sliced ? 4 * static_cast<size_t>(a.slots_before(tile >> 2) + slot) + (tile & 3)
-                                                                      : static_cast<size_t>(tile) * (1 + a.segs) + slot));
+        return static_cast<long long>(head) * a.head_parts + (a.sliced ? 4 * a.slots_before(tile >> 2) : tile & ~3) +
+               static_cast<long long>(slot) * a.part_step + (tile & 3);
     };
     auto take = [&](int head, int tile, int slot, bool read) {
         const long long at = at_of(head, tile, slot);
