@@ -439,7 +439,8 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(T) == 2 ? 2 : 1) void dq_kernel
         for (int x = 0; x < 8; ++x) delta = fmaf(static_cast<float>(of[x]), static_cast<float>(gf[s][x]), delta);
     }
     delta += other_half(delta);
-    const float lse2 = lse[qrow] * kLog2e;
+    // a row without weight (no visible key, or none with a score above -infinity): P = 0, not 2^(.. + infinity)
+    const float lse2 = lse[qrow] == -INFINITY ? INFINITY : lse[qrow] * kLog2e;
     const float c = a.scale * kLog2e;
     const int rb0 = RowRead<T, D>::base(lane & 31, h2) + sub * Tile<T, D>::kRow;
     if (sizeof(T) == 2 && n > 0 && keys.count <= kFew) {  // delta as a sum over the keys

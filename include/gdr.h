@@ -386,8 +386,9 @@ size_t gdr_chunk_backward_workspace_bytes_ranged(int gate, int dtype, int B, int
  * i.e. full causal attention with window 0, else the last `window` positions
  * (its own included) and the first `sinks` keys.  For a query row i:
  *     s_ij = scale q_i . k_j over the visible keys, o_i = softmax(s_i) v.
- * A query that sees no key gets o = 0 and lse = -inf.  A hidden key has no
- * influence whatever its values (infinities and NaN included).
+ * A query that sees no key, or whose scores all are -inf, gets o = 0, lse =
+ * -inf and a zero gradient.  A hidden key has no influence whatever its values
+ * (infinities and NaN included).
  *
  * Query heads: Hq a multiple of Hkv, not 0 unless Hkv is; query head h reads
  * key head h / (Hq / Hkv).  d in {64, 128} for keys and values alike.  With dtype BF16
@@ -397,7 +398,8 @@ size_t gdr_chunk_backward_workspace_bytes_ranged(int gate, int dtype, int B, int
  * operation is fp32.  Every sum runs in a fixed order: repeated calls give
  * identical results.  Tensors as above: dense, row-major, 16-byte aligned
  * (int arrays and lse 4-byte), no output overlapping an input; at most 2^15
- * heads, and fewer than 2^29 rows (positions x heads) in one sequence.
+ * heads, and fewer than 2^29 rows (positions x heads) in one sequence, or in
+ * all of a packed batch.
  * ---------------------------------------------------------------------------
  */
 
