@@ -156,6 +156,13 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(int(stream))
 
 
+def _stream_object(stream, device):
+    """A stream argument as torch's object.  Handle 0 is the device's default stream (torch would make a new one)."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else torch.cuda.default_stream(device)
+
+
 def _workspace(need: int, device, stream):
     """A workspace of `need` bytes for one call launched on `stream`.
 
@@ -168,7 +175,7 @@ def _workspace(need: int, device, stream):
         return None
     ws = torch.empty(need, dtype=torch.uint8, device=device)
     if stream is not None:
-        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=device)
+        s = _stream_object(stream, device)
         if s.cuda_stream != torch.cuda.current_stream(device).cuda_stream:
             ws.record_stream(s)
     return ws
@@ -520,10 +527,7 @@ def _attn_launch(dev: int, stream, fn, *args) -> None:
 
 def _on_stream(dev: int, stream):
     """The call's stream as the current one, for torch's own work on its tensors."""
-    if stream is None:
-        return contextlib.nullcontext()
-    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else
-                             torch.cuda.ExternalStream(int(stream), device=dev))
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(_stream_object(stream, dev))
 
 
 def _attn_types(q, *ts) -> int:

@@ -92,3 +92,20 @@ def test_a_workspace_is_recorded_on_the_stream_of_its_own_device(monkeypatch):
     device = torch.device("cuda", 1)
     gdr._workspace(16, device, 77)
     assert made == [(77, device), "recorded"]
+
+
+def test_handle_0_is_the_default_stream(monkeypatch):
+    """The workspace of a call on handle 0 is recorded on the default stream where another one is current."""
+    recorded = []
+
+    class Tensor:
+        def record_stream(self, s):
+            recorded.append(s)
+
+    default, current = (type("Stream", (), {"cuda_stream": n}) for n in (0, 9))
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: default)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: current)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: type("Pool", (), {"cuda_stream": 5}))
+    monkeypatch.setattr(torch, "empty", lambda *a, **kw: Tensor())
+    gdr._workspace(16, torch.device("cuda", 0), 0)
+    assert recorded == [default]

@@ -55,3 +55,25 @@ def test_a_bad_offset_leaves_the_other_sequences_without_a_bound():
     gdr.gdr_attn_prefill_varlen(q, k, k, dev([0, 20, 40, 60]), dev([0, 20, 40, 60]), good)
     gdr.gdr_attn_prefill_varlen(q, k, k, dev([0, 20, 40, 2 ** 31 - 1]), dev([0, 20, 40, 60]), o)
     assert torch.equal(o[:40], good[:40]) and (o[40:] == 7).all()
+
+
+def test_offsets_written_on_the_default_stream_given_as_handle_0():
+    """Handle 0 is the default stream, also while another stream is current."""
+    announce("attn offsets, handle 0")
+    q, k, v = make(1, 90, 4, 64), make(2, 90, 2, 64), make(3, 90, 2, 64)
+    x = [t.cuda() for t in (q, k, v)]
+    o = torch.full_like(x[0], 7.0)
+    late, ready = torch.zeros(3, dtype=torch.int32, device="cuda"), torch.tensor([0, 20, 90], dtype=torch.int32, device="cuda")
+    work = torch.randn(8192, 8192, device="cuda")
+    out = torch.empty_like(work)
+    torch.mm(work, work, out=out)
+    torch.cuda.synchronize()
+    for _ in range(30):
+        torch.mm(work, work, out=out)
+    late.copy_(ready)
+    assert torch.cuda.default_stream().cuda_stream == 0
+    with torch.cuda.stream(torch.cuda.Stream()):
+        gdr.gdr_attn_prefill_varlen(*x, late, late, o, stream=0)
+    torch.cuda.synchronize()
+    for a, b in ((0, 20), (20, 90)):
+        check("o", o[a:b], *attend(q[a:b], k[a:b], v[a:b], 0, 0, 0.125, torch.bfloat16)["o"])
