@@ -23,8 +23,9 @@
 //
 // Bound by the products and the vector work between them at two waves per SIMD
 // (dK and dV of 32 keys are 128 accumulators of a lane at d=128): T=8192, window
-// 1024, 4 sinks, 32 query on 8 key heads: dq 235 us (41% matrix cores busy, 6 d
-// flops per pair), dkdv 304 (41%, 8 d), segments 30, join 5.
+// 1024, 4 sinks, 32 query on 8 key heads: dq 228 us (40% matrix cores busy, 6 d
+// flops per pair), dkdv 298 (41%, 8 d), segments 29, join 5.  fp32 with d=128 runs
+// one wave per SIMD, and its sink segments (WAVES = 1) keep 18 registers in scratch.
 #include "attn_backward_plan.h"
 #include "attn_common.h"
 

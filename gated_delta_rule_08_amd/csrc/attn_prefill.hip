@@ -17,10 +17,11 @@
 // ColRead).  O stays in registers.
 //
 // Bound by the matrix cores and the softmax's vector work together: full causal
-// T=8192, 32 query on 8 key heads, d=128: 536 us, 1.03 PFLOP/s, matrix cores 50%
+// T=8192, 32 query on 8 key heads, d=128: 535 us, 1.03 PFLOP/s, matrix cores 51%
 // and vector ALUs 48% busy, no LDS bank conflicts; two workgroups per CU (64 KB of
-// LDS, up to 256 registers each), whose waves fill each other's gaps.  Eight waves
-// per workgroup: 522 us there, but 208 against 184 with 32 key heads (T=4096).
+// LDS, 174 registers), whose waves fill each other's gaps.  Eight waves per
+// workgroup: 538 us there and 173 against 186 with 32 key heads (T=4096), but 967
+// against 951 under a window of 4096 (T=16384) and 336 against 305 at d=64.
 #include "attn_common.h"
 
 namespace gdr {
@@ -196,8 +197,9 @@ __global__ __launch_bounds__(64 * kWaves, (PrefillCfg<T, D, SPLIT>::kBufs)) void
 
         // The other wave of the SIMD is in another phase: a wave in its products
         // goes first, the exponentials of the other fill the gaps.  With d = 128
-        // only in the second product (T=8192: 520 us, both products 541, neither
-        // 540), with d = 64 in both (B=2 T=4096: 86 us, second 93, neither 88).
+        // only in the second product (T=8192, 32/8 heads: 535 us, both products 562,
+        // neither 558), with d = 64 in both (305 us, second 314, neither 316; 8/8 heads
+        // 121 / 119 / 128).
         if (D == 64) __builtin_amdgcn_s_setprio(1);
         f32x16 s[NS];
 #pragma unroll
