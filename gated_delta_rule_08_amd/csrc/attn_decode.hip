@@ -14,14 +14,9 @@
 // 163 us and 6 for the join, 6.0 TB/s of the whole call; one of 32768: 24 + 5 us.
 //
 // The visible keys of a sequence are a list (the sinks, then the window) in
-// blocks of 128.  Sequences differ in length, so it is not they that are dealt
-// out but the blocks: the blocks of all (sequence, key head) units in a row are
-// cut into equal shares, one per workgroup, whatever the lengths are.  A
-// workgroup finds its share from the lengths alone (a scan over the batch),
-// writes the units it holds whole, and leaves (m, l, O) of the at most two it
-// shares with others to a second kernel, which joins them in order.  Lengths
-// of at most 512 keys take one workgroup per unit and no join.
-#include "attn_common.h"
+// blocks of 128, dealt out and joined as attn_deal.h has it.  Lengths of at
+// most 512 keys take one workgroup per unit and no join.
+#include "attn_deal.h"
 
 namespace gdr {
 namespace attn {
@@ -40,6 +35,14 @@ struct DecodeArgs {
     float scale;
     int shares;  // workgroups the blocks are dealt to; 0: one workgroup per unit
     int heads;   // query heads of a unit: min(16, G)
+
+    __host__ __device__ __forceinline__ int per() const { return Hkv * head_tiles; }
+    __device__ __forceinline__ int blocks(int len) const;
+    __device__ __forceinline__ bool skipped(int b, int len, const int* __restrict__ table) const;
+    __device__ __forceinline__ JoinRow row(int r) const {
+        const int b = r / Hq, hq = r - b * Hq, hk = hq / G, g = hq - hk * G;
+        return JoinRow{b, hk * head_tiles + g / 16, g & 15};
+    }
 };
 
 // What one sequence's step covers, from its length alone (the same in every
@@ -67,56 +70,9 @@ __device__ __forceinline__ bool has_page(const DecodeArgs& a, int b, int p, cons
     return page >= 0 && page < a.num_pages;
 }
 
-// The blocks of the batch in a row: sequence by sequence, within one unit by
-// unit (key head, 16 query heads), `per` units each.  A wave sums them 256
-// sequences at a time, four to a lane, so that their lengths come together.
-__device__ __forceinline__ int scan64(int x, int lane) {  // inclusive
-#pragma unroll
-    for (int s = 1; s < 64; s <<= 1) {
-        const int y = __shfl_up(x, s);
-        if (lane >= s) x += y;
-    }
-    return x;
-}
-struct Blocks4 {
-    int each[4], upto;  // of sequences at + 4 lane .. + 3; blocks of at .. and these
-};
-__device__ __forceinline__ Blocks4 blocks_of(const DecodeArgs& a, int at, const int* __restrict__ lengths, int lane) {
-    Blocks4 r;
-    int sum = 0, len[4];
-#pragma unroll
-    for (int x = 0; x < 4; ++x) len[x] = at + 4 * lane + x < a.B ? lengths[at + 4 * lane + x] : -1;
-#pragma unroll
-    for (int x = 0; x < 4; ++x) sum += r.each[x] = span_of(a, len[x]).blocks;
-    r.upto = scan64(sum, lane);
-    return r;
-}
-// Blocks of one unit per sequence: of the whole batch, and of the sequences before b.
-__device__ __forceinline__ long long all_blocks(const DecodeArgs& a, const int* lengths, int lane, int b, long long& before) {
-    long long sum = 0;
-    before = 0;
-    for (int at = 0; at < a.B; at += 256) {
-        const Blocks4 r = blocks_of(a, at, lengths, lane);
-        if (b >= at && b < at + 256) {
-            const int x = b - at, rest = x & 3;
-            int mine = r.upto;  // up to and with this lane's four, less those not before b
-#pragma unroll
-            for (int y = 0; y < 4; ++y)
-                if (y >= rest) mine -= r.each[y];
-            before = sum + __shfl(mine, x >> 2);
-        }
-        sum += __shfl(r.upto, 63);
-    }
-    return sum;
-}
-
-// Shares in use: no share is empty, so a unit's parts are consecutive shares.
-__device__ __forceinline__ int shares_of(const DecodeArgs& a, long long n) {
-    return static_cast<int>(n < a.shares ? n : a.shares);
-}
-// The share that holds block g of n, share w being blocks [w n / W, (w+1) n / W).
-__device__ __forceinline__ int owner(long long g, long long n, int W) {
-    return static_cast<int>(((g + 1) * W - 1) / n);
+__device__ __forceinline__ int DecodeArgs::blocks(int len) const { return span_of(*this, len).blocks; }
+__device__ __forceinline__ bool DecodeArgs::skipped(int b, int len, const int* __restrict__ table) const {
+    return !has_page(*this, b, len, table);
 }
 
 template <typename T, int D> struct DecodeCfg {
@@ -208,55 +164,17 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(T) * D <= 256 ? 2 : 1) void dec
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int c16 = lane & 15, h4 = lane >> 4;
 
-    const int slot_mask = (1 << a.page_shift) - 1, per = a.Hkv * a.head_tiles;
+    const int slot_mask = (1 << a.page_shift) - 1, per = a.per();
     // a scale of 0 as one that no score survives: c -inf of a hidden key stays -inf
     const float c = fmaxf(fabsf(a.scale) * kLog2e, 1e-37f);
     unsigned char *kt = smem + wave * C::kWave, *vt = kt + C::kTile, *tt = vt + C::kTile;
     const uint32_t kt_at = lds_addr(kt), vt_at = lds_addr(vt), tt_at = lds_addr(tt);
     const int kb = RowRead16<T, D>::base(lane), vb = ColRead16<T, D>::base(lane);
 
-    // this workgroup's blocks: [at_block, at_block + left) of unit `unit` of sequence b and on
-    int b, unit, at_block, left;
-    Span sp;
-    if (a.shares == 0) {
-        b = blockIdx.x / per;
-        unit = blockIdx.x - b * per;
-        sp = span_of(a, lengths[b]);
-        at_block = 0;
-        left = sp.blocks;
-    } else {
-        long long before;
-        const long long n = per * all_blocks(a, lengths, lane, -1, before);
-        const int W = shares_of(a, n);
-        if (static_cast<int>(blockIdx.x) >= W) return;
-        const long long lo = n * blockIdx.x / W, hi = n * (blockIdx.x + 1) / W;
-        left = __builtin_amdgcn_readfirstlane(static_cast<int>(hi - lo));
-        before = 0;  // per unit
-        for (b = 0; b < a.B; b += 256) {  // the first sequence that ends after lo
-            const Blocks4 r = blocks_of(a, b, lengths, lane);
-            const uint64_t past = __ballot((before + r.upto) * per > lo);
-            if (past) {
-                int x = 0, upto = r.upto - r.each[0] - r.each[1] - r.each[2] - r.each[3];
-#pragma unroll
-                for (int y = 0; y < 3; ++y)
-                    if (x == y && (before + upto + r.each[y]) * per <= lo) {
-                        upto += r.each[y];
-                        ++x;
-                    }
-                const int from = __builtin_ctzll(past);
-                before += __shfl(upto, from);
-                b += 4 * from + __shfl(x, from);
-                break;
-            }
-            before += __shfl(r.upto, 63);
-        }
-        b = __builtin_amdgcn_readfirstlane(b);
-        if (b >= a.B) return;  // not reached unless the lengths change under the call
-        sp = span_of(a, lengths[b]);
-        const long long in = lo - before * per;
-        unit = __builtin_amdgcn_readfirstlane(static_cast<int>(in / max(1, sp.blocks)));
-        at_block = __builtin_amdgcn_readfirstlane(static_cast<int>(in - static_cast<long long>(unit) * sp.blocks));
-    }
+    Share share;
+    if (!find_share(a, lengths, lane, blockIdx.x, share)) return;
+    int b = share.b, unit = share.unit, at_block = share.at_block, left = share.left;
+    Span sp = span_of(a, lengths[b]);
 
 #pragma unroll 1
     while (left > 0) {
@@ -474,113 +392,27 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(T) * D <= 256 ? 2 : 1) void dec
     }
 }
 
-// Joins the parts of a shared unit, W waves per query head: part 0 is slot 1 of
-// the unit's first share, the others slot 0 of the shares after it.  16 W parts
-// at a time, lane s holding part s's weight 2^(m_s - max m); a wave adds every
-// W-th part, the channels over its lanes, and the waves' sums are added in order.
-template <typename T, int D, int W>
-__global__ __launch_bounds__(256) void join_kernel(DecodeArgs a, const int* __restrict__ table,
-                                                   const int* __restrict__ lengths,
-                                                   const float* __restrict__ part_o,
-                                                   const float* __restrict__ part_ml, T* __restrict__ o) {
-    constexpr int N = D / 64, kEach = 16;
-    __shared__ float sums[W > 1 ? W - 1 : 1][D];
-    const int lane = threadIdx.x & 63, every = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = every % W;
-    const int at = blockIdx.x * (4 / W) + every / W, b = at / a.Hq, hq = at - b * a.Hq;
-    if (b >= a.B) return;
-    const Span sp = span_of(a, lengths[b]);
-    if (sp.blocks == 0 || !has_page(a, b, sp.pos, table)) return;
-    const int per = a.Hkv * a.head_tiles, hk = hq / a.G, g = hq - hk * a.G;
-    long long before;
-    const long long n = per * all_blocks(a, lengths, lane, b, before);
-    const long long lo = per * before + static_cast<long long>(hk * a.head_tiles + g / 16) * sp.blocks;
-    const int used = shares_of(a, n), w0 = owner(lo, n, used), parts = owner(lo + sp.blocks - 1, n, used) - w0 + 1;
-    if (parts == 1) return;  // written whole
-    auto slot = [&](int s) { return (static_cast<size_t>(w0 + s) * 2 + (s == 0)) * a.heads + (g & 15); };
-    float M = -INFINITY, total = 0.f, acc[N] = {};
-    for (int s0 = 0; s0 < parts; s0 += kEach * W) {
-        float m = -INFINITY, l = 0.f;
-        if (lane < kEach * W && s0 + lane < parts) {
-            m = part_ml[slot(s0 + lane) * 2];
-            l = part_ml[slot(s0 + lane) * 2 + 1];
-        }
-        float x[kEach][N];
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) {  // all loads before the first use
-            const int s = s0 + W * i + wave;
-#pragma unroll
-            for (int e = 0; e < N; ++e) x[i][e] = s < parts ? part_o[slot(s) * D + N * lane + e] : 0.f;
-        }
-        float mx = m;
-#pragma unroll
-        for (int s = 1; s < 64; s <<= 1) mx = fmaxf(mx, __shfl_xor(mx, s));
-        mx = fmaxf(M, mx);
-        const float old = M == -INFINITY ? 0.f : ex2(M - mx), w = m == -INFINITY ? 0.f : ex2(m - mx);
-        M = mx;
-        float add = l * w;
-#pragma unroll
-        for (int s = 1; s < 64; s <<= 1) add += __shfl_xor(add, s);
-        total = total * old + add;
-#pragma unroll
-        for (int e = 0; e < N; ++e) acc[e] *= old;
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-            const float ws = __shfl(w, W * i + wave);
-#pragma unroll
-            for (int e = 0; e < N; ++e) acc[e] = fmaf(ws, x[i][e], acc[e]);
-        }
-    }
-    if constexpr (W > 1) {
-        if (wave > 0) {
-#pragma unroll
-            for (int e = 0; e < N; ++e) sums[wave - 1][N * lane + e] = acc[e];
-        }
-        __syncthreads();
-        if (wave > 0) return;
-    }
-    const float inv = total == 0.f ? 0.f : 1.f / total;
-    const size_t row = static_cast<size_t>(b) * a.Hq + hq;
-#pragma unroll
-    for (int e = 0; e < N; ++e) {
-#pragma unroll
-        for (int s = 0; s < W - 1; ++s) acc[e] += sums[s][N * lane + e];
-        Elem<T>::store(o + row * D + N * lane + e, acc[e] * inv);
-    }
-}
-
 template <typename T, int D>
 hipError_t launch_decode_t(const DecodeArgs& a, const void* q, const void* k, const void* v, void* k_pages,
                            void* v_pages, const int* table, const int* lengths, void* o, float* ws, hipStream_t st) {
     using C = DecodeCfg<T, D>;
-    const unsigned long long blocks =
-        a.shares ? a.shares : static_cast<unsigned long long>(a.B) * a.Hkv * a.head_tiles;
-    const unsigned long long rows = static_cast<unsigned long long>(a.B) * a.Hq;
-    // a share's blocks have to fit an int, and so have those of one scan's sequences
-    const unsigned long long most = (static_cast<unsigned long long>(a.max_pages) << a.page_shift) / kBlock + 1;
-    if (a.shares && (static_cast<unsigned long long>(a.B) * a.Hkv * a.head_tiles * most / a.shares > 0x7fffffffull ||
-                     (a.B < 256 ? a.B : 256) * most > 0x7fffffffull))
-        return hipErrorInvalidConfiguration;
-    if (!grid_fits(blocks, 64 * kWaves) || !grid_fits(rows, 256)) return hipErrorInvalidConfiguration;
     auto* f = decode_kernel<T, D>;
-    if (C::kLds > 64 * 1024) {
-        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(f),
-                                                 hipFuncAttributeMaxDynamicSharedMemorySize, C::kLds);
-        if (e != hipSuccess) return e;
-    }
-    float* part_o = ws;
-    float* part_ml = ws ? ws + static_cast<size_t>(a.shares) * 2 * a.heads * D : nullptr;
-    hipLaunchKernelGGL(f, dim3(static_cast<unsigned>(blocks)), dim3(64 * kWaves), C::kLds, st, a,
-                       static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v),
-                       static_cast<T*>(k_pages), static_cast<T*>(v_pages), table, lengths, static_cast<T*>(o),
-                       part_o, part_ml);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || a.shares == 0) return e;
-    // Many heads have few parts each and take a wave (64 sequences of 32: 5.7 against 10.9 us), few heads four.
-    const bool many = rows >= 1024;
-    auto* join = many ? join_kernel<T, D, 1> : join_kernel<T, D, 4>;
-    hipLaunchKernelGGL(join, dim3(static_cast<unsigned>(many ? (rows + 3) / 4 : rows)), dim3(256), 0, st, a, table, lengths,
-                       part_o, part_ml, static_cast<T*>(o));
-    return hipGetLastError();
+    const unsigned long long most = (static_cast<unsigned long long>(a.max_pages) << a.page_shift) / kBlock + 1;
+    return launch_dealt<T, D>(a, static_cast<unsigned long long>(a.B) * a.Hq, most, 64 * kWaves, table, lengths, o, ws, st,
+                              [&](unsigned blocks, float* part_o, float* part_ml) {
+                                  if (C::kLds > 64 * 1024) {
+                                      const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(f),
+                                                                               hipFuncAttributeMaxDynamicSharedMemorySize,
+                                                                               C::kLds);
+                                      if (e != hipSuccess) return e;
+                                  }
+                                  hipLaunchKernelGGL(f, dim3(blocks), dim3(64 * kWaves), C::kLds, st, a,
+                                                     static_cast<const T*>(q), static_cast<const T*>(k),
+                                                     static_cast<const T*>(v), static_cast<T*>(k_pages),
+                                                     static_cast<T*>(v_pages), table, lengths, static_cast<T*>(o),
+                                                     part_o, part_ml);
+                                  return hipGetLastError();
+                              });
 }
 
 // Append: a workgroup copies 1024 consecutive 16-byte units of the new keys and
