@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import math
 import os
 from typing import Optional
 
@@ -26,6 +27,9 @@ __all__ = [
     "gdr_decode_multi_ex", "gdr_chunk_prefill_varlen_ex", "SCHED_FUSED", "SCHED_SPLIT",
     "gdr_chunk_prefill_noalloc", "gdr_attn_prefill", "gdr_attn_prefill_varlen", "gdr_attn_backward",
     "gdr_attn_backward_workspace_bytes", "gdr_attn_decode", "gdr_attn_decode_workspace_bytes", "gdr_attn_append",
+    "gdr_attn_norm_rope", "gdr_attn_norm_rope_backward", "gdr_attn_norm_rope_backward_workspace_bytes",
+    "gdr_attn_plan_pages", "gdr_attn_append_mx4", "gdr_attn_read_mx4", "gdr_attn_decode_mx4",
+    "gdr_attn_decode_mx4_workspace_bytes",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -51,7 +55,11 @@ EXPORTED_SYMBOLS = ("gdr_decode_step", "gdr_decode_step_ex", "gdr_chunk_prefill_
                     "gdr_abi_version",
                     "gdr_attn_prefill", "gdr_attn_prefill_varlen", "gdr_attn_backward",
                     "gdr_attn_backward_workspace_bytes", "gdr_attn_decode",
-                    "gdr_attn_decode_workspace_bytes", "gdr_attn_append")
+                    "gdr_attn_decode_workspace_bytes", "gdr_attn_append",
+                    "gdr_attn_norm_rope", "gdr_attn_norm_rope_backward",
+                    "gdr_attn_norm_rope_backward_workspace_bytes", "gdr_attn_plan_pages",
+                    "gdr_attn_append_mx4", "gdr_attn_read_mx4", "gdr_attn_decode_mx4",
+                    "gdr_attn_decode_mx4_workspace_bytes")
 CHUNK = 64
 _lib = None
 
@@ -76,7 +84,7 @@ def load_library():
         raise GdrError(-100, "libgdr.so is not built (%s); run "
                        "`python -m gated_delta_rule_08_amd.build`" % path)
     lib = ctypes.CDLL(path)
-    vp, i, f = ctypes.c_void_p, ctypes.c_int, ctypes.c_float
+    vp, i, f, ll = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_longlong
     lib.gdr_decode_step.argtypes = [i, i, i, i, i, i, f] + [vp] * 8
     lib.gdr_decode_step.restype = i
     lib.gdr_decode_step_ex.argtypes = [i] * 7 + [f] + [vp] * 8
@@ -123,6 +131,22 @@ def load_library():
     lib.gdr_attn_decode_workspace_bytes.restype = ctypes.c_size_t
     lib.gdr_attn_append.argtypes = [i] * 8 + [vp] * 8
     lib.gdr_attn_append.restype = i
+    lib.gdr_attn_norm_rope.argtypes = [i] * 7 + [f, ll, ll] + [vp] * 9
+    lib.gdr_attn_norm_rope.restype = i
+    lib.gdr_attn_norm_rope_backward.argtypes = [i] * 7 + [f] + [ll] * 4 + [vp] * 13 + [ctypes.c_size_t, vp]
+    lib.gdr_attn_norm_rope_backward.restype = i
+    lib.gdr_attn_norm_rope_backward_workspace_bytes.argtypes = [i] * 5
+    lib.gdr_attn_norm_rope_backward_workspace_bytes.restype = ctypes.c_size_t
+    lib.gdr_attn_plan_pages.argtypes = [i] * 5 + [vp] * 11
+    lib.gdr_attn_plan_pages.restype = i
+    lib.gdr_attn_append_mx4.argtypes = [i] * 8 + [vp] * 10
+    lib.gdr_attn_append_mx4.restype = i
+    lib.gdr_attn_read_mx4.argtypes = [i] * 8 + [vp] * 10
+    lib.gdr_attn_read_mx4.restype = i
+    lib.gdr_attn_decode_mx4.argtypes = [i] * 11 + [f] + [vp] * 9 + [ctypes.c_size_t, vp]
+    lib.gdr_attn_decode_mx4.restype = i
+    lib.gdr_attn_decode_mx4_workspace_bytes.argtypes = [i] * 10
+    lib.gdr_attn_decode_mx4_workspace_bytes.restype = ctypes.c_size_t
     lib.gdr_status_string.argtypes = [i]
     lib.gdr_status_string.restype = ctypes.c_char_p
     lib.gdr_abi_version.argtypes = []
@@ -724,3 +748,260 @@ def gdr_attn_append(k, v, cu_seqlens, lengths, k_pages, v_pages, page_table, str
     _attn_launch(dev, stream, load_library().gdr_attn_append, code, N, total, Hkv, d, page, num_pages, max_pages,
                  k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), lengths.data_ptr(), k_pages.data_ptr(),
                  v_pages.data_ptr(), page_table.data_ptr())
+
+
+# ---- around the attention layers: norm and rotation, page plan, 4-bit cache
+
+
+def _token_stride(name, t, tokens: int, H: int, d: int) -> int:
+    """Elements from token to token of t [..., H, d], whose heads are dense and whose tokens are evenly apart."""
+    size, step = t.shape, t.stride()
+    if t.is_contiguous() or t.numel() == 0:
+        return H * d
+    if step[-1] != 1 or (H > 1 and step[-2] != d):
+        raise ValueError("%s: the heads of a token must be dense" % name)
+    apart = None  # of the innermost token axis that has one
+    expect = 0
+    for n, s in zip(reversed(size[:-2]), reversed(step[:-2])):
+        if n == 1:
+            continue
+        if apart is None:
+            apart = s
+        elif s != expect:
+            raise ValueError("%s: the tokens must be evenly apart" % name)
+        expect = s * n
+    return H * d if apart is None else apart
+
+
+def _rope_rows(q, k, positions, inv_freq):
+    """(tokens, Hq, Hkv, d, rot) of a norm and rotation."""
+    if q.dim() < 2 or q.dim() != k.dim():
+        raise ValueError("q must be [...,Hq,d], k [...,Hkv,d]")
+    lead, (Hq, d) = q.shape[:-2], q.shape[-2:]
+    if k.shape[:-2] != lead or k.shape[-1] != d:
+        raise ValueError("q and k must agree in their tokens and channels")
+    if inv_freq.dim() != 1 or inv_freq.dtype != torch.float32:
+        raise ValueError("inv_freq must be fp32 [rot / 2]")
+    rot = 2 * inv_freq.shape[0]
+    if rot:
+        _int32("positions", positions, lead)
+    return math.prod(lead), Hq, k.shape[-2], d, rot
+
+
+def _on_device(dev, *ts) -> None:
+    """Each tensor (None ones apart) is on device number dev; its strides are the caller's to check."""
+    for t in ts:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("all tensors must be on the GPU" if t.get_device() < 0 else "all tensors must be on one device")
+
+
+def _rope_weights(d, *ws) -> None:
+    for w in ws:
+        if w is not None and (w.shape != (d,) or w.dtype != torch.float32):
+            raise ValueError("weights and their gradients must be fp32 [d]")
+
+
+def gdr_attn_norm_rope(q, k, positions, inv_freq, q_out, k_out, w_q=None, w_k=None, eps: float = 1e-6, norm: bool = True,
+                       interleaved: bool = False, stream=None) -> None:
+    """RMS norm of each head of queries and keys (``norm``) and the rotation of
+    their first ``2 * len(inv_freq)`` channels by ``positions * inv_freq``.
+
+    q [...,Hq,d] and k [...,Hkv,d] share a dtype (fp32 or bf16) and their
+    leading (token) axes; their heads are dense, their tokens evenly apart, so
+    both may be views of a fused projection.  q_out and k_out are dense and may
+    be q and k themselves where those are.  positions is int32 of the token
+    axes, inv_freq fp32, w_q and w_k fp32 [d] (None: ones).  The pairs are
+    channels (i, i + rot / 2), or (2i, 2i + 1) if ``interleaved``.
+    """
+    tokens, Hq, Hkv, d, rot = _rope_rows(q, k, positions, inv_freq)
+    if q_out.shape != q.shape or k_out.shape != k.shape:
+        raise ValueError("q_out and k_out must have the shapes of q and k")
+    code = _attn_types(q, k, q_out, k_out)
+    _rope_weights(d, w_q, w_k)
+    dev = _attn_device(q_out, k_out, w_q, w_k, inv_freq, positions if rot else None)
+    _on_device(dev, q, k)
+    sq, sk = _token_stride("q", q, tokens, Hq, d), _token_stride("k", k, tokens, Hkv, d)
+    _attn_launch(dev, stream, load_library().gdr_attn_norm_rope, code, (1 if interleaved else 0) | (0 if norm else 2), _attn_int(tokens),
+                 Hq, Hkv, d, rot, eps, sq, sk, q.data_ptr(), k.data_ptr(), None if w_q is None else w_q.data_ptr(),
+                 None if w_k is None else w_k.data_ptr(), positions.data_ptr() if rot else None,
+                 inv_freq.data_ptr() if rot else None, q_out.data_ptr(), k_out.data_ptr())
+
+
+def gdr_attn_norm_rope_backward_workspace_bytes(dtype, tokens: int, Hq: int, Hkv: int, d: int) -> int:
+    return int(load_library().gdr_attn_norm_rope_backward_workspace_bytes(_DTYPES[dtype], *map(_attn_int, (tokens, Hq, Hkv, d))))
+
+
+def gdr_attn_norm_rope_backward(q, k, positions, inv_freq, grad_q_out, grad_k_out, grad_q, grad_k, w_q=None, w_k=None,
+                                grad_w_q=None, grad_w_k=None, eps: float = 1e-6, norm: bool = True, interleaved: bool = False,
+                                workspace=None, stream=None) -> None:
+    """Gradients of sum(grad_q_out * q_out) + sum(grad_k_out * k_out) through
+    :func:`gdr_attn_norm_rope` for the same arguments, written into grad_q and
+    grad_k (which may lie as q and k do, or be the incoming gradients
+    themselves) and, where given, grad_w_q and grad_w_k (fp32 [d], overwritten).
+    workspace: a device tensor of at least
+    gdr_attn_norm_rope_backward_workspace_bytes bytes, or None to have one
+    allocated for this call."""
+    tokens, Hq, Hkv, d, rot = _rope_rows(q, k, positions, inv_freq)
+    for x, g, h in ((q, grad_q_out, grad_q), (k, grad_k_out, grad_k)):
+        if g.shape != x.shape or h.shape != x.shape:
+            raise ValueError("gradient shapes must match the inputs")
+    code = _attn_types(q, k, grad_q_out, grad_k_out, grad_q, grad_k)
+    _rope_weights(d, w_q, w_k, grad_w_q, grad_w_k)
+    dev = _attn_device(grad_q_out, grad_k_out, w_q, w_k, grad_w_q, grad_w_k, inv_freq, positions if rot else None, workspace)
+    _on_device(dev, q, k, grad_q, grad_k)
+    strides = [_token_stride(n, t, tokens, H, d) for n, t, H in (
+        ("q", q, Hq), ("k", k, Hkv), ("grad_q", grad_q, Hq), ("grad_k", grad_k, Hkv))]
+    weights = grad_w_q is not None or grad_w_k is not None
+    need = 0 if workspace is not None or not weights else gdr_attn_norm_rope_backward_workspace_bytes(q.dtype, tokens, Hq, Hkv, d)
+    ws, ws_bytes, workspace = _attn_workspace(workspace, need, dev, stream)
+    _attn_launch(dev, stream, load_library().gdr_attn_norm_rope_backward, code, (1 if interleaved else 0) | (0 if norm else 2),
+                 _attn_int(tokens), Hq, Hkv, d, rot, eps, *strides, q.data_ptr(), k.data_ptr(),
+                 None if w_q is None else w_q.data_ptr(), None if w_k is None else w_k.data_ptr(),
+                 positions.data_ptr() if rot else None, inv_freq.data_ptr() if rot else None, grad_q_out.data_ptr(),
+                 grad_k_out.data_ptr(), grad_q.data_ptr(), grad_k.data_ptr(),
+                 None if grad_w_q is None else grad_w_q.data_ptr(), None if grad_w_k is None else grad_w_k.data_ptr(), ws, ws_bytes)
+
+
+def gdr_attn_plan_pages(lengths, add, free_pages, n_free, page_table, page_size: int, cu_seqlens, added, lengths_out,
+                        n_free_out, slots=None, max_tokens: Optional[int] = None, stream=None) -> None:
+    """The page plan of a serving step: requests that hold ``lengths`` [N]
+    tokens are to add ``add`` [N].
+
+    New pages come from the top of the stack free_pages [F], of which n_free [1]
+    are there, and go into page_table [N,max_pages].  Requests are served in
+    order up to the first that the pages, or ``max_tokens`` in all (slots' size,
+    or no limit), do not suffice for; it and those after it add 0.  Written:
+    cu_seqlens [N+1] (packed offsets of the added tokens), added [N],
+    lengths_out [N] = lengths + added, n_free_out [1] and, if given, slots
+    [max_tokens]: each token's page * page_size + position % page_size.  added,
+    lengths_out and n_free_out may be add, lengths and n_free.  All int32;
+    page_size a power of two.
+    """
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [N,max_pages]")
+    N, max_pages = page_table.shape
+    for name, t, shape in (("lengths", lengths, (N,)), ("add", add, (N,)), ("page_table", page_table, (N, max_pages)),
+                           ("free_pages", free_pages, (free_pages.numel(),)), ("n_free", n_free, (1,)),
+                           ("cu_seqlens", cu_seqlens, (N + 1,)), ("added", added, (N,)), ("lengths_out", lengths_out, (N,)),
+                           ("n_free_out", n_free_out, (1,))):
+        _int32(name, t, shape)
+    if slots is not None:
+        _int32("slots", slots, (slots.numel(),))
+        if max_tokens is None or max_tokens > slots.numel():
+            max_tokens = slots.numel()
+    dev = _attn_device(lengths, add, free_pages, n_free, page_table, cu_seqlens, added, lengths_out, n_free_out, slots)
+    _attn_launch(dev, stream, load_library().gdr_attn_plan_pages, N, _attn_int(page_size), max_pages, _attn_int(free_pages.numel()),
+                 0x7fffffff if max_tokens is None else _attn_int(max_tokens), lengths.data_ptr(), add.data_ptr(),
+                 free_pages.data_ptr(), n_free.data_ptr(), page_table.data_ptr(), cu_seqlens.data_ptr(), added.data_ptr(),
+                 lengths_out.data_ptr(), None if slots is None else slots.data_ptr(), n_free_out.data_ptr())
+
+
+def _mx4_checks(k_codes, k_scales, v_codes, v_scales, page_table, Hkv, d, N):
+    """(page_size, num_pages, max_pages) of a 4-bit cache."""
+    if k_codes.dim() != 4 or page_table.dim() != 2:
+        raise ValueError("k_codes must be [num_pages,Hkv,page_size,d/2], page_table [sequences,max_pages]")
+    num_pages, _, page, _ = k_codes.shape
+    if (k_codes.shape != (num_pages, Hkv, page, d // 2) or v_codes.shape != (num_pages, Hkv, page // 32, d, 16)
+            or k_scales.shape != (num_pages, Hkv, page, d // 32) or v_scales.shape != k_scales.shape):
+        raise ValueError("k_codes must be [num_pages,Hkv,page_size,d/2], v_codes [num_pages,Hkv,page_size/32,d,16], "
+                         "k_scales and v_scales [num_pages,Hkv,page_size,d/32]")
+    for t in (k_codes, k_scales, v_codes, v_scales):
+        if t.dtype != torch.uint8:
+            raise ValueError("codes and scales must be uint8")
+    max_pages = page_table.shape[1]
+    _int32("page_table", page_table, (N, max_pages))
+    return page, num_pages, max_pages
+
+
+def gdr_attn_append_mx4(k, v, cu_seqlens, lengths, k_codes, k_scales, v_codes, v_scales, page_table, stream=None) -> None:
+    """Quantises packed keys and values k, v [total,Hkv,d] into the pages of a
+    4-bit cache: token i of sequence n (cu_seqlens [N+1], int32) goes to
+    position lengths[n] + i.
+
+    Blocks of 32 channels share a power of two, of which each value is a 4-bit
+    multiple (0, 1/2, 1, 3/2, 2, 3, 4, 6 with a sign): k_codes
+    [num_pages,Hkv,page_size,d/2], v_codes [num_pages,Hkv,page_size/32,d,16],
+    k_scales and v_scales [num_pages,Hkv,page_size,d/32], all uint8; page_size a
+    power of two from 32.  page_table [N,max_pages] and lengths [N] as in
+    :func:`gdr_attn_append`; lengths are not advanced."""
+    if k.dim() != 3:
+        raise ValueError("k and v must be [total,Hkv,d]")
+    total, Hkv, d = shape = k.shape
+    if v.shape != shape:
+        raise ValueError("k and v shapes disagree")
+    code = _attn_types(k, v)
+    N = lengths.numel()
+    _int32("lengths", lengths, (N,))
+    _int32("cu_seqlens", cu_seqlens, (N + 1,))
+    page, num_pages, max_pages = _mx4_checks(k_codes, k_scales, v_codes, v_scales, page_table, Hkv, d, N)
+    dev = _attn_device(k, v, cu_seqlens, lengths, k_codes, k_scales, v_codes, v_scales, page_table)
+    _attn_launch(dev, stream, load_library().gdr_attn_append_mx4, code, N, _attn_int(total), Hkv, d, page, num_pages, max_pages,
+                 k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), lengths.data_ptr(), k_codes.data_ptr(),
+                 k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), page_table.data_ptr())
+
+
+def gdr_attn_read_mx4(k_codes, k_scales, v_codes, v_scales, page_table, cu_seqlens, k, v, first=None, stream=None) -> None:
+    """What the pages of a 4-bit cache stand for, as packed dense k, v
+    [total,Hkv,d] (fp32 or bf16, exact in both): positions first[n] and on
+    (first [N] int32; None: from 0) of each sequence, cu_seqlens[n+1] -
+    cu_seqlens[n] of them.  The context of a prompt's next part for
+    :func:`gdr_attn_prefill_varlen`.  The cache as in
+    :func:`gdr_attn_append_mx4`."""
+    if k.dim() != 3:
+        raise ValueError("k and v must be [total,Hkv,d]")
+    total, Hkv, d = shape = k.shape
+    if v.shape != shape:
+        raise ValueError("k and v shapes disagree")
+    code = _attn_types(k, v)
+    N = page_table.shape[0]
+    _int32("cu_seqlens", cu_seqlens, (N + 1,))
+    if first is not None:
+        _int32("first", first, (N,))
+    page, num_pages, max_pages = _mx4_checks(k_codes, k_scales, v_codes, v_scales, page_table, Hkv, d, N)
+    dev = _attn_device(k, v, cu_seqlens, first, k_codes, k_scales, v_codes, v_scales, page_table)
+    _attn_launch(dev, stream, load_library().gdr_attn_read_mx4, code, N, _attn_int(total), Hkv, d, page, num_pages, max_pages,
+                 k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), page_table.data_ptr(),
+                 cu_seqlens.data_ptr(), None if first is None else first.data_ptr(), k.data_ptr(), v.data_ptr())
+
+
+def gdr_attn_decode_mx4_workspace_bytes(dtype, B: int, Tq: int, Hq: int, Hkv: int, d: int, page_size: int, max_pages: int,
+                                        window: int = 0, sinks: int = 0) -> int:
+    return int(load_library().gdr_attn_decode_mx4_workspace_bytes(
+        _DTYPES[dtype], *map(_attn_int, (B, Tq, Hq, Hkv, d, page_size, max_pages, window, sinks))))
+
+
+def gdr_attn_decode_mx4(q, k_codes, k_scales, v_codes, v_scales, page_table, lengths, o, window: int = 0, sinks: int = 0,
+                        scale: Optional[float] = None, workspace=None, stream=None) -> None:
+    """Attention of each sequence's last position, or last Tq of them (up to 64:
+    a draft to verify), over a 4-bit cache that holds them already: q, o
+    [B,Hq,d] or [B,Tq,Hq,d], query i of sequence b at position lengths[b] - Tq + i,
+    the mask as in :func:`gdr_attn_prefill`.
+
+    The cache as in :func:`gdr_attn_append_mx4`; page_table [B,max_pages] and
+    lengths [B] are int32 device tensors.  workspace: a device tensor of at
+    least gdr_attn_decode_mx4_workspace_bytes bytes, or None to have one
+    allocated for this call.
+    """
+    if q.dim() == 3:
+        (B, Hq, d), Tq = q.shape, 1
+    elif q.dim() == 4:
+        B, Tq, Hq, d = q.shape
+    else:
+        raise ValueError("q must be [B,Hq,d] or [B,Tq,Hq,d]")
+    if o.shape != q.shape:
+        raise ValueError("q and o shapes disagree")
+    if k_codes.dim() != 4:
+        raise ValueError("k_codes must be [num_pages,Hkv,page_size,d/2]")
+    Hkv = k_codes.shape[1]
+    _attn_heads(Hq, Hkv)
+    code = _attn_types(q, o)
+    page, num_pages, max_pages = _mx4_checks(k_codes, k_scales, v_codes, v_scales, page_table, Hkv, d, B)
+    _int32("lengths", lengths, (B,))
+    dev = _attn_device(q, k_codes, k_scales, v_codes, v_scales, page_table, lengths, o, workspace)
+    need = 0 if workspace is not None else gdr_attn_decode_mx4_workspace_bytes(q.dtype, B, Tq, Hq, Hkv, d, page, max_pages, window,
+                                                                               sinks)
+    ws, ws_bytes, workspace = _attn_workspace(workspace, need, dev, stream)
+    _attn_launch(dev, stream, load_library().gdr_attn_decode_mx4, code, B, Tq, Hq, Hkv, d, page, num_pages, max_pages,
+                 _attn_int(window), _attn_int(sinks), d ** -0.5 if scale is None else scale, q.data_ptr(), k_codes.data_ptr(),
+                 k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), page_table.data_ptr(), lengths.data_ptr(),
+                 o.data_ptr(), ws, ws_bytes)

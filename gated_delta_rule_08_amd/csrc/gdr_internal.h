@@ -152,6 +152,34 @@ hipError_t launch_attn_append(int dtype, int N, int total, int Hkv, int d, int p
                               int max_pages, const void* k, const void* v, const int* cu, const int* lengths,
                               void* k_pages, void* v_pages, const int* table, hipStream_t s);
 
+// Around the attention layers: norm and rotation (attn_rope.hip), the page plan
+// (attn_pages.hip) and the 4-bit cache (attn_mx4.hip).  Strides in elements.
+hipError_t launch_attn_rope(int dtype, int tokens, int Hq, int Hkv, int d, int rot, int interleaved, int norm, float eps,
+                            long long q_stride, long long k_stride, const void* q, const void* k, const float* w_q,
+                            const float* w_k, const int* positions, const float* inv_freq, void* q_out, void* k_out,
+                            hipStream_t s);
+size_t attn_rope_backward_workspace_floats(int tokens, int Hq, int Hkv, int d);
+// ws may be null where neither weight's gradient is wanted; tokens == 0: those are zeroed
+hipError_t launch_attn_rope_backward(int dtype, int tokens, int Hq, int Hkv, int d, int rot, int interleaved, int norm,
+                                     float eps, long long q_stride, long long k_stride, long long gq_stride,
+                                     long long gk_stride, const void* q, const void* k, const float* w_q, const float* w_k,
+                                     const int* positions, const float* inv_freq, const void* g_q_out, const void* g_k_out,
+                                     void* g_q, void* g_k, float* g_w_q, float* g_w_k, float* ws, hipStream_t s);
+hipError_t launch_attn_plan_pages(int N, int page_size, int max_pages, int n_stack, int max_tokens, const int* lengths,
+                                  const int* add, const int* free_pages, const int* n_free, int* table, int* cu, int* added,
+                                  int* lengths_out, int* slots, int* n_free_out, hipStream_t s);
+hipError_t launch_attn_append_mx4(int dtype, int N, int total, int Hkv, int d, int page_size, int num_pages, int max_pages,
+                                  const void* k, const void* v, const int* cu, const int* lengths, void* k_codes,
+                                  void* k_scales, void* v_codes, void* v_scales, const int* table, hipStream_t s);
+hipError_t launch_attn_read_mx4(int dtype, int N, int total, int Hkv, int d, int page_size, int num_pages, int max_pages,
+                                const void* k_codes, const void* k_scales, const void* v_codes, const void* v_scales,
+                                const int* table, const int* cu, const int* first, void* k, void* v, hipStream_t s);
+size_t attn_decode_mx4_workspace_floats(int Tq, int Hq, int Hkv, int d, int page_size, int max_pages, int window, int sinks);
+hipError_t launch_attn_decode_mx4(int dtype, int B, int Tq, int Hq, int Hkv, int d, int page_size, int num_pages,
+                                  int max_pages, int window, int sinks, float scale, const void* q, const void* k_codes,
+                                  const void* k_scales, const void* v_codes, const void* v_scales, const int* table,
+                                  const int* lengths, void* o, float* ws, hipStream_t s);
+
 // state_out <- state_in (or zeros when state_in is NULL), n floats.
 hipError_t launch_state_copy(const float* state_in, float* state_out, size_t n, hipStream_t s);
 

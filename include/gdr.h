@@ -524,6 +524,167 @@ int gdr_attn_append(int dtype, int N, int total, int Hkv, int d, int page_size, 
                     const void* k, const void* v, const int* cu_seqlens, const int* lengths, void* k_pages,
                     void* v_pages, const int* page_table, void* stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Around the attention layers: what stands between a layer's projection and its
+ * attention, and a paged cache that holds keys and values in 4 bits.  Types, heads,
+ * d, alignment and device data as in the attention calls above; fp32 arithmetic
+ * throughout, outputs rounded once.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * Flags of gdr_attn_norm_rope and its backward (bitwise OR; others return
+ * GDR_ERR_BAD_ENUM):
+ *   GDR_ROPE_INTERLEAVED  the turned pairs are channels (2i, 2i + 1), not (i, i + rot / 2)
+ *   GDR_ROPE_NO_NORM      rotation only (w_q, w_k and their gradients NULL, else GDR_ERR_UNSUPPORTED)
+ */
+enum { GDR_ROPE_INTERLEAVED = 1, GDR_ROPE_NO_NORM = 2 };
+
+/*
+ * RMS norm of every head of queries and keys, and the rotation of their first rot
+ * channels by the token's position, in one pass: with x one head's d channels,
+ *     y = x / sqrt(mean(x^2) + eps) * w,
+ *     (y_a, y_b) <- (y_a cos t - y_b sin t, y_b cos t + y_a sin t),
+ * t = positions[token] * inv_freq[i] for pair i of rot / 2.
+ *
+ *   q      [tokens, Hq, d]    dtype, token after token q_stride elements apart (a
+ *   k      [tokens, Hkv, d]   view of a fused projection; k_stride likewise); the
+ *                             strides are multiples of 16 bytes
+ *   q_out, k_out              the same, dense
+ *   w_q, w_k   [d] fp32, or NULL: ones
+ *   positions  [tokens] int32;  inv_freq [rot / 2] fp32 (both NULL if rot is 0)
+ *
+ * rot is a multiple of 16 up to d.  The angle is formed in double, so a position
+ * may be any int32.  Hq and Hkv are independent here, and either may be 0.  q_out
+ * may be q, and k_out k, where these are dense (GDR_ERR_ALIAS otherwise).  tokens *
+ * (Hq + Hkv) must stay below 2^29.  Returns a GDR_* status.
+ */
+int gdr_attn_norm_rope(int dtype, int flags, int tokens, int Hq, int Hkv, int d, int rot, float eps, long long q_stride,
+                       long long k_stride, const void* q, const void* k, const float* w_q, const float* w_k,
+                       const int* positions, const float* inv_freq, void* q_out, void* k_out, void* stream);
+
+/*
+ * Backward pass of gdr_attn_norm_rope for the same arguments: gradients of
+ * L = sum(grad_q_out * q_out) + sum(grad_k_out * k_out).
+ *
+ *   grad_q_out, grad_k_out  as q_out and k_out, dense
+ *   grad_q, grad_k          as q and k, tokens grad_q_stride and grad_k_stride
+ *                           elements apart; grad_q may be grad_q_out if it is dense
+ *   grad_w_q, grad_w_k      [d] fp32 or NULL (not wanted): sums over every token and
+ *                           head, in a fixed order (repeated calls agree)
+ *   workspace  at least gdr_attn_norm_rope_backward_workspace_bytes(...) bytes where
+ *              grad_w_q or grad_w_k is wanted
+ *
+ * q and k are not read with GDR_ROPE_NO_NORM.  Without tokens or heads grad_w_q and
+ * grad_w_k are zeroed.  Returns a GDR_* status.
+ */
+int gdr_attn_norm_rope_backward(int dtype, int flags, int tokens, int Hq, int Hkv, int d, int rot, float eps,
+                                long long q_stride, long long k_stride, long long grad_q_stride, long long grad_k_stride,
+                                const void* q, const void* k, const float* w_q, const float* w_k, const int* positions,
+                                const float* inv_freq, const void* grad_q_out, const void* grad_k_out, void* grad_q,
+                                void* grad_k, float* grad_w_q, float* grad_w_k, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
+/* Bytes of workspace gdr_attn_norm_rope_backward needs for the weights'
+ * gradients (0 when the arguments are invalid or there are no rows). */
+size_t gdr_attn_norm_rope_backward_workspace_bytes(int dtype, int tokens, int Hq, int Hkv, int d);
+
+/*
+ * The page plan of a serving step: N requests that hold lengths[n] tokens each are
+ * to add add[n].  A request needs ceil((lengths + add) / page_size) -
+ * ceil(lengths / page_size) new pages, taken one by one from the top of a stack.
+ * Requests are served in order up to the first that the stack or max_tokens (the
+ * step's tokens in all) does not suffice for; it and those after it add nothing.
+ * A request with a negative length or addition, or one that would outgrow its row
+ * of the table, adds nothing and holds no one up.
+ *
+ *   lengths, add  [N] int32
+ *   free_pages    [n_stack] int32, the top at n_free[0] - 1 (n_free is taken as
+ *                 within 0 .. n_stack); not changed
+ *   page_table    [N, max_pages] int32: the entries of new pages are written, the
+ *                 others are left
+ *   cu_seqlens    [N + 1] int32 out: offsets of the step's tokens, packed (what the
+ *                 append and the prefill take)
+ *   added         [N] int32 out: add[n], or 0; may be add
+ *   lengths_out   [N] int32 out: lengths + added; may be lengths
+ *   slots         [max_tokens] int32 out, or NULL: page * page_size + position %
+ *                 page_size of every token, -1 where that page is negative; left as
+ *                 it was behind the last token
+ *   n_free_out    [1] int32 out: pages left; may be n_free
+ *
+ * All device data, and nothing is read on the host.  page_size a power of two up to
+ * 65536.  N == 0 writes cu_seqlens[0] and n_free_out.  Returns a GDR_* status.
+ */
+int gdr_attn_plan_pages(int N, int page_size, int max_pages, int n_stack, int max_tokens, const int* lengths, const int* add,
+                        const int* free_pages, const int* n_free, int* page_table, int* cu_seqlens, int* added,
+                        int* lengths_out, int* slots, int* n_free_out, void* stream);
+
+/*
+ * The 4-bit cache.  32 consecutive channels of one position and head are a block:
+ * a scale byte b and 32 codes, each a sign (8) and one of 0, 1/2, 1, 3/2, 2, 3, 4, 6
+ * (0 .. 7), standing for code * 2^(b - 127).  The append takes the least scale
+ * with max |x| <= 7 * 2^(b - 127), b within 1 .. 252, and the nearest code, ties to
+ * the even one (6 from there on).  A block that holds an infinity or NaN stands for
+ * NaN: b = 255 with codes 0.
+ *
+ *   k_codes   [num_pages, Hkv, page_size, d / 2]       uint8: the even channel in the low half
+ *   v_codes   [num_pages, Hkv, page_size / 32, d, 16]  uint8: a channel's 32 positions, the
+ *                                                      even in the low half
+ *   k_scales, v_scales [num_pages, Hkv, page_size, d / 32] uint8
+ *   page_table [sequences, max_pages] int32, as in the paged cache above; page_size a
+ *             power of two from 32 to 65536
+ *
+ * All four 16-byte aligned.  What the calls were not asked to write is left as it was.
+ */
+
+/*
+ * Quantises the keys and values of N packed sequences into their pages: token i of
+ * sequence n goes to position lengths[n] + i.  Arguments, and what is not written, as
+ * in gdr_attn_append; sequences of one call must not share a block of 32 positions that
+ * is written.  Returns a GDR_* status.
+ */
+int gdr_attn_append_mx4(int dtype, int N, int total, int Hkv, int d, int page_size, int num_pages, int max_pages,
+                        const void* k, const void* v, const int* cu_seqlens, const int* lengths, void* k_codes, void* k_scales,
+                        void* v_codes, void* v_scales, const int* page_table, void* stream);
+
+/*
+ * The way back, for the prefill of a prompt's next part: positions first[n] ..
+ * first[n] + cu_seqlens[n + 1] - cu_seqlens[n] - 1 of each sequence (first NULL: from 0)
+ * into packed k, v [total, Hkv, d], exactly.  Tokens of no sequence, and those beyond
+ * the table row or on a page outside the pool, are left as they were.  Returns a
+ * GDR_* status.
+ */
+int gdr_attn_read_mx4(int dtype, int N, int total, int Hkv, int d, int page_size, int num_pages, int max_pages,
+                      const void* k_codes, const void* k_scales, const void* v_codes, const void* v_scales,
+                      const int* page_table, const int* cu_seqlens, const int* first, void* k, void* v, void* stream);
+
+/*
+ * Attention of the last Tq positions (up to 64: 1 for a decode step, more to verify
+ * a draft) of B sequences over the 4-bit cache; the mask is the attention calls'.
+ * The new tokens' keys and values are in the cache already (gdr_attn_append_mx4).
+ *
+ *   q, o      [B, Tq, Hq, d]   dtype
+ *   lengths   [B] int32: positions the cache holds, the Tq new ones included: query i
+ *             is at position lengths[b] - Tq + i
+ *   workspace at least gdr_attn_decode_mx4_workspace_bytes(...) bytes (NULL if 0)
+ *
+ * A sequence whose length is negative or beyond its table row is skipped (o stays as
+ * it was); positions of a page outside the pool are hidden; a query that sees no key (one before the first
+ * position, or of an empty sequence) gets 0.  A block that stands for NaN makes the rows that see it NaN, and so does
+ * a query with an infinity.  With dtype BF16 the weights enter the second product rounded to bf16.  With num_pages or
+ * max_pages 0 nothing is written.  Returns a GDR_* status.
+ */
+int gdr_attn_decode_mx4(int dtype, int B, int Tq, int Hq, int Hkv, int d, int page_size, int num_pages, int max_pages,
+                        int window, int sinks, float scale, const void* q, const void* k_codes, const void* k_scales,
+                        const void* v_codes, const void* v_scales, const int* page_table, const int* lengths, void* o,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace gdr_attn_decode_mx4 needs (0 when the arguments are
+ * invalid or none is needed). */
+size_t gdr_attn_decode_mx4_workspace_bytes(int dtype, int B, int Tq, int Hq, int Hkv, int d, int page_size, int max_pages,
+                                           int window, int sinks);
+
 /* Static, NUL-terminated description of a status code (never NULL). */
 const char* gdr_status_string(int status);
 
