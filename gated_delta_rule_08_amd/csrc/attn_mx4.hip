@@ -24,6 +24,11 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kMxWaves = 4;
 constexpr int kQuad = 4 * kMxRows;  // positions of a wave's step: 4 blocks of 32
+// A unit's steps are dealt out as if it had four more at its beginning: its first
+// loads wait for one another (length, page, keys) for as long as four waves take for
+// a step each.  64 sequences of 16 .. 8000 tokens, whose shortest come in dozens to a
+// workgroup: 83 us without, 61 with (2: 67, 6 and 8: 61 and 62).
+constexpr int kUnitCost = 4;
 
 // At query position p a key j is visible if j <= p and (window == 0 or j > p - window or j < sinks).
 struct Mx4Args {
@@ -33,6 +38,7 @@ struct Mx4Args {
     float scale;
     int shares;  // workgroups the blocks are dealt to; 0: one workgroup per unit
     int heads;   // rows of a unit: min(16, Tq * G)
+    FastDiv by_group, by_tiles;  // by G and by head_tiles
 
     __host__ __device__ __forceinline__ int per() const { return Hkv * head_tiles; }
     __device__ __forceinline__ int blocks(int len) const;
@@ -48,7 +54,7 @@ struct Mx4Args {
 struct MxSpan {
     int p0, p1;         // positions of the first and the last query
     int sinks, jump;    // blocks 0 .. sinks-1 come first; entry x >= sinks is block x + jump
-    int entries, steps; // steps of four entries; 0: the length is out of range
+    int entries, steps; // steps of four entries and kUnitCost; 0: the length is out of range
 };
 __device__ __forceinline__ MxSpan mx_span(const Mx4Args& a, int n) {
     MxSpan s;
@@ -59,7 +65,7 @@ __device__ __forceinline__ MxSpan mx_span(const Mx4Args& a, int n) {
     s.jump = lo / kMxRows - s.sinks;
     s.entries = n > 0 ? s.p1 / kMxRows - s.jump + 1 : 0;
     const bool fits = n >= 0 && (s.p1 >> a.page_shift) < a.max_pages;
-    s.steps = fits ? max(1, (s.entries + 3) / 4) : 0;  // without keys one step, which writes the zeros
+    s.steps = fits ? (s.entries + 3) / 4 + kUnitCost : 0;
     return s;
 }
 __device__ __forceinline__ int Mx4Args::blocks(int len) const { return mx_span(*this, len).steps; }
@@ -81,6 +87,72 @@ template <int NP> __device__ __forceinline__ void split8(const float (&x)[8], bf
     }
 }
 
+// LDS of the decode step: for each wave the keys, values and scales of one step.
+// Keys are read 16 (d = 64: 8) bytes a lane, four positions of each of the four
+// blocks at a time.  d = 128: odd blocks have their 16-byte units swapped in
+// pairs; d = 64: these too, and the blocks 2 and 3 lie 128 bytes further.  Either
+// way the lanes that share a cycle read different banks.
+template <int D> struct Mx4Lds {
+    static constexpr int kBlock = kMxRows * D / 2;  // bytes of a block's codes
+    static constexpr int kScales = kMxRows * D / 32;
+    static constexpr int kGap = D == 64 ? 128 : 0;
+    static constexpr int kValues = 4 * kBlock + kGap, kKeyScales = kValues + 4 * kBlock;
+    static constexpr int kValueScales = kKeyScales + 4 * kScales;
+    static constexpr int kWave = kValueScales + 4 * kScales;
+    static constexpr int kPitch = D + 4;  // floats of a joined row
+    static constexpr int kJoin = kMxWaves * 16 * (kPitch + 2) * 4;
+    static constexpr int kBytes = kMxWaves * kWave > kJoin ? kMxWaves * kWave : kJoin;
+    static constexpr int kKeyCopies = 4 * kBlock / 1024, kScaleCopies = 4 * kScales / 256;
+    __device__ __forceinline__ static int keys(int block) { return block * kBlock + (block >> 1) * kGap; }
+};
+
+// At most n of this wave's latest loads and copies are still on their way.
+template <int N> __device__ __forceinline__ void mx4_wait() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0f70 | (N & 15) | ((N >> 4) << 14));
+    asm volatile("" ::: "memory");
+}
+// This wave's LDS reads have returned: what they read may be overwritten.
+__device__ __forceinline__ void mx4_wait_lds() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xc07f);
+    asm volatile("" ::: "memory");
+}
+// Copies to LDS, base + off in memory: 16 bytes a lane, not to be kept in the
+// caches, or 4.
+__device__ __forceinline__ void mx4_copy16(uint32_t lds, const void* base, uint32_t off) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 nt" ::"s"(lds), "v"(off), "s"(base)
+                 : "memory");
+}
+
+// v in the lanes where `mine` holds, else zero.
+__device__ __forceinline__ bf16x8v of_copy(const bf16x8v& v, bool mine) {
+    const u32x4 u = __builtin_bit_cast(u32x4, v);
+    return __builtin_bit_cast(bf16x8v, u32x4{mine ? u[0] : 0u, mine ? u[1] : 0u, mine ? u[2] : 0u, mine ? u[3] : 0u});
+}
+// v as a value the compiler knows nothing about: it is kept, not formed again.
+__device__ __forceinline__ bf16x8v kept(const bf16x8v& v) {
+    u32x4 u = __builtin_bit_cast(u32x4, v);
+    asm volatile("" : "+v"(u));
+    return __builtin_bit_cast(bf16x8v, u);
+}
+// The sum or maximum over the X copies of a row (16 / X lanes apart in its 16), and
+// over the four blocks (the lanes 16 and 32 apart), in every lane.
+template <int N> __device__ __forceinline__ float rotated(float v) {  // of the lane N further in its 16
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x120 + N, 0xf, 0xf, true));
+}
+template <int X, typename F> __device__ __forceinline__ float over_copies(float v, F f) {
+    if constexpr (X == 4) v = f(v, rotated<4>(v));
+    if constexpr (X >= 2) v = f(v, rotated<8>(v));
+    return v;
+}
+template <typename F> __device__ __forceinline__ float over_blocks(float v, F f) {
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = f(__uint_as_float(a[0]), __uint_as_float(a[1]));
+    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return f(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+
 // One decode step.  A wave takes 128 positions at a time: block h of the four goes
 // with the lanes 16 h .. 16 h + 15.
 //
@@ -90,75 +162,159 @@ template <int NP> __device__ __forceinline__ void split8(const float (&x)[8], bf
 //  O^T = V^T P^T: the lane's 8 weights of positions 8 i .. 8 i + 7 are the operand as
 //  they stand, and the other is word i of a channel's 16 bytes.
 //
+// A unit of few rows leaves most of the 16 columns idle, and with them most of the
+// lanes' softmax.  So there are X = 4 copies of up to 4 rows, or 2 of up to 8: copy x
+// takes positions 32 x / X .. of each block.  Of the keys' tiles each meets the query
+// in its own copy's columns only, zero in the others, so that X tiles share an
+// accumulator, and a lane has 32 / X positions; of the weights each product takes
+// one copy's, and the copies' sums are added at the end.  (X = 1: 960 vector
+// instructions a step, X = 4: 600.)
+//
 // The keys' scales are applied by the conversion to bf16, which is exact.  The
 // values' scales differ along the summed axis and are multiplied into the weights:
 // one set of weights for every 32 channels.  bf16: the weights are rounded to bf16
-// before the power of two, or after it, which is the same.  fp32: queries and
+// after the power of two, which is the same as before it.  fp32: queries and
 // weights go in as three bf16 pieces, 24 bits, and no bit of the codes is lost.
-template <typename T, int D>
+//
+// Bound by HBM and, at half its time, by the vector ALUs.  Everything that is read
+// goes through LDS, straight from memory in whole lines: fetched into the registers
+// of the lanes that need it, each line of the keys and scales is asked for by
+// several of them while it is on its way, and the L1 cache stalls on that (64
+// sequences of 16 .. 8000 tokens, 280 MB: 89 us with the loads a step ahead in
+// registers).  Keys are refilled as soon as the scores are formed, values as soon as
+// they are summed, no barrier until the end.
+template <typename T, int D, int X>
 __global__ __launch_bounds__(64 * kMxWaves, 2) void mx4_decode_kernel(
     Mx4Args a, const T* __restrict__ q, const uint8_t* __restrict__ k_codes, const uint8_t* __restrict__ k_scales,
     const uint8_t* __restrict__ v_codes, const uint8_t* __restrict__ v_scales, const int* __restrict__ table,
     const int* __restrict__ lengths, T* __restrict__ o, float* __restrict__ part_o, float* __restrict__ part_ml) {
-    constexpr int NP = Pieces<T>::n, KS = D / 32, DT = D / 16, CB = D / 32;
-    constexpr int kLane = D / 8;      // bytes of a key in one lane
-    constexpr int kPitch = D + 4;     // floats of a joined row
-    constexpr int kWords = CB * 8;    // words of a block's 32 x CB scales
-    __shared__ __align__(16) float jo[kMxWaves * 16 * kPitch];
-    __shared__ float jm[kMxWaves * 16 * 2];
+    using C = Mx4Lds<D>;
+    constexpr int NP = Pieces<T>::n, KS = D / 32, DT = D / 16, CB = D / 32, kPitch = C::kPitch;
+    constexpr int kCopies = C::kKeyCopies + C::kScaleCopies;  // of a step's keys, and of its values
+    constexpr int kRows = 16 / X, kMine = 32 / X;              // rows of a unit; positions of a lane in each block
+    extern __shared__ __align__(16) unsigned char smem[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int c16 = lane & 15, h4 = lane >> 4;
+    const int c16 = lane & 15, h4 = lane >> 4, x = c16 / kRows;
     const int per = a.per(), slot_mask = (1 << a.page_shift) - 1;
     // a scale of 0 as one that no score survives: c -inf of a hidden key stays -inf
     const float c = fmaxf(fabsf(a.scale) * kLog2e, 1e-37f);
+    unsigned char* mine_lds = smem + wave * C::kWave;
+    const uint32_t lds_at = lds_addr(mine_lds);
+    // where this lane reads its keys, their scales, its values and theirs
+    const unsigned char* kp = mine_lds + C::keys(c16 >> 2) + (c16 & 3) * (D / 2) +
+                              (D == 128 ? 16 * (h4 ^ ((c16 >> 2) & 1)) : 8 * (h4 ^ (((c16 >> 2) & 1) << 1)));
+    const unsigned char* ksp = mine_lds + C::kKeyScales + (c16 >> 2) * C::kScales + (c16 & 3) * CB + (h4 * CB) / 4;
+    const unsigned char* vp = mine_lds + C::kValues + h4 * C::kBlock + 16 * c16;
+    const unsigned char* vsp = mine_lds + C::kValueScales + h4 * C::kScales + x * kMine * CB;
+    // and the unit it copies, from the start of 1024 bytes of keys: even and odd blocks
+    const uint32_t unit = 16 * lane, swapped = 16 * (lane ^ 1);
 
     Share share;
     if (!find_share(a, lengths, lane, blockIdx.x, share)) return;
-    int b = share.b, unit = share.unit, at_block = share.at_block, left = share.left;
-    MxSpan sp = mx_span(a, lengths[b]);
+    int b = __builtin_amdgcn_readfirstlane(share.b), unit_at = __builtin_amdgcn_readfirstlane(share.unit);
+    int at_block = __builtin_amdgcn_readfirstlane(share.at_block), left = __builtin_amdgcn_readfirstlane(share.left);
+    auto span = [&](int b) { return mx_span(a, __builtin_amdgcn_readfirstlane(lengths[b])); };
+    MxSpan sp = span(b);
 
 #pragma unroll 1
     while (left > 0) {
-        if (unit >= per || sp.steps == 0) {  // the next sequence that is not skipped
+        if (unit_at >= per || sp.steps == 0) {  // the next sequence that is not skipped
             if (++b >= a.B) return;
-            unit = 0;
-            sp = mx_span(a, lengths[b]);
+            unit_at = 0;
+            sp = span(b);
             continue;
         }
         const int take = min(left, sp.steps - at_block);
-        const int hk = unit / a.head_tiles, ht = unit - hk * a.head_tiles;
-        const int* trow = table + static_cast<size_t>(b) * a.max_pages;
+        const int hk = __builtin_amdgcn_readfirstlane(a.by_tiles(unit_at)), ht = unit_at - hk * a.head_tiles;
+        // the table does not change under the call: scalar loads, counted apart from the copies
+        typedef const int __attribute__((address_space(4))) * ConstInts;
+        const ConstInts trow = (ConstInts)(table + static_cast<size_t>(b) * a.max_pages);
 
         // this lane's query row: query i, head g of the group
         const int rows = min(16, a.Tq * a.G - ht * 16);
-        const int mine = ht * 16 + min(c16, rows - 1), qi = mine / a.G;
+        const int mine = ht * 16 + min(c16 % kRows, rows - 1), qi = a.by_group(mine);
         const int pos = sp.p0 + qi;
         const size_t orow = (static_cast<size_t>(b) * a.Tq + qi) * a.Hq + hk * a.G + mine - qi * a.G;
-        bf16x8v qf[KS][NP];
+
+        // Entry e of the list: its first position; and from the page there the row of its
+        // first position in the page tensors, or -1 where there is none (past the list, or
+        // on a page outside the pool).
+        auto start_of = [&](int e) { return (e < sp.sinks ? e : e + sp.jump) * kMxRows; };
+        auto page_of = [&](int e) { return trow[start_of(max(min(e, sp.entries - 1), 0)) >> a.page_shift]; };
+        auto row_of = [&](int e, int page) {
+            if (e >= sp.entries || page < 0 || page >= a.num_pages) return -1;
+            return ((page * a.Hkv + hk) << a.page_shift) + (start_of(e) & slot_mask);
+        };
+        auto copy_scales = [&](uint32_t lds, const uint8_t* scales, const int (&row)[4]) {  // 256 bytes at a time
+            constexpr int kEach = 256 / C::kScales;  // blocks of a copy
+#pragma unroll
+            for (int j = 0; j < C::kScaleCopies; ++j) {
+                int r = row[kEach * j];
+#pragma unroll
+                for (int x = 1; x < kEach; ++x)
+                    if (lane >= x * (64 / kEach)) r = row[kEach * j + x];
+                const size_t from = static_cast<size_t>(max(r, 0)) * CB + 4 * (lane & (64 / kEach - 1));
+                gather_words(lds + 256 * j, scales + from);
+            }
+        };
+        auto copy_keys = [&](const int (&row)[4]) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const uint8_t* p = k_codes + static_cast<size_t>(max(row[x], 0)) * (D / 2);
+#pragma unroll
+                for (int j = 0; j < C::kBlock / 1024; ++j)
+                    mx4_copy16(lds_at + C::keys(x) + 1024 * j, p + 1024 * j, x & 1 ? swapped : unit);
+            }
+            copy_scales(lds_at + C::kKeyScales, k_scales, row);
+        };
+        auto copy_values = [&](const int (&row)[4]) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const uint8_t* p = v_codes + static_cast<size_t>(max(row[x], 0)) * (D / 2);
+#pragma unroll
+                for (int j = 0; j < C::kBlock / 1024; ++j)
+                    mx4_copy16(lds_at + C::kValues + C::kBlock * x + 1024 * j, p + 1024 * j, unit);
+            }
+            copy_scales(lds_at + C::kValueScales, v_scales, row);
+        };
+
+        // The query and the pages of two steps come together, then the first copies.
+        const int end = max(0, at_block + take - kUnitCost);
+        int step = max(0, at_block - kUnitCost) + wave, row[4], page[4], next[4];
+        bf16x8v qf[X][KS][NP];  // copy by copy: the others' columns are zero
         {
             const T* qp = q + orow * D + (D / 4) * h4;
+            frag_t<T> raw[KS];
+#pragma unroll
+            for (int s = 0; s < KS; ++s) raw[s] = load8(qp + 8 * s);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                page[x] = page_of(4 * step + x);
+                next[x] = page_of(4 * (step + kMxWaves) + x);
+            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                row[x] = row_of(4 * step + x, page[x]);
+                page[x] = next[x];
+            }
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
-                float x[8];
+                float f[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = Elem<T>::load(qp + 8 * s + i);
-                if (a.scale < 0.f) {
+                for (int i = 0; i < 8; ++i) f[i] = a.scale < 0.f ? -static_cast<float>(raw[s][i]) : static_cast<float>(raw[s][i]);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = -x[i];
+                for (int y = 0; y < X; ++y) {
+                    split8<NP>(f, qf[y][s]);
+#pragma unroll
+                    for (int p = 0; p < NP; ++p) qf[y][s][p] = X > 1 ? kept(of_copy(qf[y][s][p], x == y)) : qf[y][s][p];
                 }
-                split8<NP>(x, qf[s]);
             }
         }
-
-        // Entry e of the list: the row of its first position in the page tensors, or
-        // -1 where there is none (past the list, or on a page outside the pool).
-        auto row_of = [&](int e) {
-            if (e >= sp.entries) return -1;
-            const int first = (e < sp.sinks ? e : e + sp.jump) * kMxRows;
-            const int page = trow[first >> a.page_shift];
-            if (page < 0 || page >= a.num_pages) return -1;
-            return ((page * a.Hkv + hk) << a.page_shift) + (first & slot_mask);
-        };
+        if (step < end) {
+            copy_keys(row);
+            copy_values(row);
+        }
 
         f32x4 acc[DT];
 #pragma unroll
@@ -166,92 +322,102 @@ __global__ __launch_bounds__(64 * kMxWaves, 2) void mx4_decode_kernel(
         float m = -INFINITY, l = 0.f;
 
 #pragma unroll 1
-        for (int step = at_block + wave; step < at_block + take; step += kMxWaves) {
-            const int krow = row_of(4 * step + (c16 >> 2)), vrow = row_of(4 * step + h4);
-            // keys: lane (c, h) has channels D/4 h .. of position 4 t + c % 4 of block c / 4
-            uint32_t kf[8][KS];
-            uint32_t ks[8];
-            {
-                const size_t first = static_cast<size_t>(max(krow, 0)) + (c16 & 3);
-                const uint8_t* p = k_codes + first * (D / 2) + kLane * h4;
-                const uint8_t* s = k_scales + first * CB + (h4 * CB) / 4;
+        for (; step < end; step += kMxWaves) {
+            const bool more = step + kMxWaves < end;
+            int shown = 0;  // blocks that exist
 #pragma unroll
-                for (int t = 0; t < 8; ++t) {
+            for (int x = 0; x < 4; ++x) shown |= (row[x] >= 0) << x;
+            mx4_wait<kCopies>();  // the keys; the values may still come
+            // The byte 255 gives an infinite scale, which no code but 0 comes with: the scores are
+            // NaN.  Where tiles share an accumulator such a key would reach the other copies'
+            // scores too: it goes in as a finite one, and its own score is set afterwards.
+            uint32_t kb[8];
+#pragma unroll
+            for (int t = 0; t < 8; ++t) kb[t] = ksp[t * 4 * CB];
+            bool odd = false;
+            if constexpr (X > 1) {
+                uint32_t top = 0;
+#pragma unroll
+                for (int t = 0; t < 8; ++t) top = max(top, kb[t]);
+                odd = __any(top == kMxNan);
+                if (odd) {
+#pragma unroll
+                    for (int t = 0; t < 8; ++t)
+                        if (kb[t] == kMxNan) kb[t] = 1;
+                }
+            }
+            f32x4 s[8 / X];
+#pragma unroll
+            for (int j = 0; j < 8 / X; ++j) {
+                s[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int y = 0; y < X; ++y) {
+                    const int t = y * (8 / X) + j;
+                    uint32_t k[KS];
                     if constexpr (D == 128) {
-                        const u32x4 x = *reinterpret_cast<const u32x4*>(p + t * 4 * (D / 2));
+                        const u32x4 u = *reinterpret_cast<const u32x4*>(kp + t * 4 * (D / 2));
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) kf[t][i] = x[i];
+                        for (int i = 0; i < 4; ++i) k[i] = u[i];
                     } else {
-                        const u32x2 x = *reinterpret_cast<const u32x2*>(p + t * 4 * (D / 2));
+                        const u32x2 u = *reinterpret_cast<const u32x2*>(kp + t * 4 * (D / 2));
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) kf[t][i] = x[i];
+                        for (int i = 0; i < 2; ++i) k[i] = u[i];
                     }
-                    ks[t] = s[t * 4 * CB];
+                    const float scale = mx_float(kb[t]);
+#pragma unroll
+                    for (int e = 0; e < KS; ++e) {
+                        const bf16x8v kv = mx_bf16(k[e], scale);
+#pragma unroll
+                        for (int p = 0; p < NP; ++p) s[j] = mma16(kv, qf[y][e][p], s[j]);
+                    }
                 }
             }
-            // values: lane (c, h) has channel 16 t + c of block h; scales: all of block h
-            u32x4 vf[DT];
-            uint32_t vs[kWords];
-            {
-                const size_t first = max(vrow, 0);
-                const uint8_t* p = v_codes + first * (D / 2) + 16 * c16;
-                const u32x4* s = reinterpret_cast<const u32x4*>(v_scales + first * CB);
+            if (odd) {
+                const unsigned char* own = mine_lds + C::kKeyScales + h4 * C::kScales + x * kMine * CB;
 #pragma unroll
-                for (int t = 0; t < DT; ++t) vf[t] = *reinterpret_cast<const u32x4*>(p + t * 256);
+                for (int j = 0; j < kMine; ++j) {
+                    bool nan = false;
 #pragma unroll
-                for (int t = 0; t < kWords / 4; ++t) {
-                    const u32x4 x = s[t];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) vs[4 * t + i] = x[i];
+                    for (int cb = 0; cb < CB; ++cb) nan |= own[j * CB + cb] == kMxNan;
+                    if (nan) s[j >> 2][j & 3] = NAN;
                 }
             }
-
-            f32x4 s[8];
+            if (more) {
 #pragma unroll
-            for (int t = 0; t < 8; ++t) {
-                s[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-                // the byte 255 gives an infinite scale, which no code but 0 comes with: the scores are NaN
-                const float scale = mx_float(ks[t]);
+                for (int x = 0; x < 4; ++x) row[x] = row_of(4 * (step + kMxWaves) + x, page[x]);
 #pragma unroll
-                for (int e = 0; e < KS; ++e) {
-                    const bf16x8v x = mx_bf16(kf[t][e], scale);
-#pragma unroll
-                    for (int p = 0; p < NP; ++p) s[t] = mma16(x, qf[e][p], s[t]);
-                }
+                for (int x = 0; x < 4; ++x) page[x] = page_of(4 * (step + 2 * kMxWaves) + x);
+                mx4_wait_lds();
+                copy_keys(row);
             }
 
             // Which of its 32 positions the lane's query sees.  A hidden position's weight is
             // 0, and so is its scale: what it holds has no influence whatever it is.
-            const int e0 = 4 * step + h4, first = (e0 < sp.sinks ? e0 : e0 + sp.jump) * kMxRows;
-            const bool whole = vrow >= 0 && first + kMxRows - 1 <= sp.p0 &&
+            const int first = start_of(4 * step + h4);
+            const bool exists = (shown >> h4) & 1;
+            const bool whole = exists && first + kMxRows - 1 <= sp.p0 &&
                                (a.window == 0 || first > sp.p1 - a.window || first + kMxRows <= a.sinks);
-            if (!__all(whole)) {
-                uint32_t seen = 0;
-                if (vrow >= 0) {
-                    const int before = min(max(pos + 1 - first, 0), 32);  // j <= pos
-                    seen = before == 32 ? 0xffffffffu : (1u << before) - 1;
-                    if (a.window) {
-                        const int out = min(max(pos - a.window + 1 - first, 0), 32), sink = min(max(a.sinks - first, 0), 32);
-                        seen &= (out == 32 ? 0u : 0xffffffffu << out) | (sink == 32 ? 0xffffffffu : (1u << sink) - 1);
-                    }
+            const bool all = __all(whole);
+            uint32_t seen = 0xffffffffu;
+            if (!all) {
+                const int before = min(max(pos + 1 - first, 0), 32);  // j <= pos
+                seen = before == 32 ? 0xffffffffu : (1u << before) - 1;
+                if (a.window) {
+                    const int out = min(max(pos - a.window + 1 - first, 0), 32), sink = min(max(a.sinks - first, 0), 32);
+                    seen &= (out == 32 ? 0u : 0xffffffffu << out) | (sink == 32 ? 0xffffffffu : (1u << sink) - 1);
                 }
+                if (!exists) seen = 0;
+                seen >>= x * kMine;
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    const bool see = (seen >> j) & 1;
-                    if (!see) s[j >> 2][j & 3] = -INFINITY;
-                    if constexpr (D == 128) {
-                        if (!see) vs[j] = 0;
-                    } else {
-                        if (!see) vs[j >> 1] &= j & 1 ? 0xffffu : 0xffff0000u;
-                    }
-                }
+                for (int j = 0; j < kMine; ++j)
+                    if (!((seen >> j) & 1)) s[j >> 2][j & 3] = -INFINITY;
             }
 
             float mx = s[0][0];
 #pragma unroll
-            for (int j = 1; j < 32; ++j) mx = fmaxf(mx, s[j >> 2][j & 3]);
-            mx = fmaxf(mx, __shfl_xor(mx, 16));
-            mx = fmaxf(m, fmaxf(mx, __shfl_xor(mx, 32)));
+            for (int j = 1; j < kMine; ++j) mx = fmaxf(mx, s[j >> 2][j & 3]);
+            auto larger = [](float u, float v) { return fmaxf(u, v); };
+            mx = fmaxf(m, over_blocks(over_copies<X>(mx, larger), larger));
             const float mc = mx == -INFINITY ? 0.f : mx * c;
             if (__any(mx > m)) {
                 const float alpha = m == -INFINITY ? 0.f : ex2(m * c - mc);
@@ -260,8 +426,28 @@ __global__ __launch_bounds__(64 * kMxWaves, 2) void mx4_decode_kernel(
                 for (int t = 0; t < DT; ++t) acc[t] *= alpha;
                 m = mx;
             }
+            if (more)
+                mx4_wait<kCopies>();  // the values; the next keys may still come
+            else
+                mx4_wait<0>();
+            u32x4 vf[DT], vs[kMine * CB / 16];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int t = 0; t < kMine * CB / 16; ++t) vs[t] = *reinterpret_cast<const u32x4*>(vsp + 16 * t);
+#pragma unroll
+            for (int t = 0; t < DT; ++t) vf[t] = *reinterpret_cast<const u32x4*>(vp + 256 * t);
+            if (!all) {
+#pragma unroll
+                for (int j = 0; j < kMine; ++j) {  // 4 positions to 16 bytes (d = 64: 8)
+                    if (!((seen >> j) & 1)) vs[j * CB >> 4][(j * CB >> 2) & 3] &= D == 128 ? 0u : j & 1 ? 0xffffu : 0xffff0000u;
+                }
+            }
+            if (more) {
+                mx4_wait_lds();
+                copy_values(row);
+            }
+#pragma unroll
+            for (int i = 0; i < 4 / X; ++i) {  // 8 of this lane's positions
+                __builtin_amdgcn_sched_barrier(0);
                 float w[8];
 #pragma unroll
                 for (int y = 0; y < 8; ++y) {
@@ -270,28 +456,40 @@ __global__ __launch_bounds__(64 * kMxWaves, 2) void mx4_decode_kernel(
                 }
 #pragma unroll
                 for (int cb = 0; cb < CB; ++cb) {
-                    float x[8];
+                    float f[8];
 #pragma unroll
                     for (int y = 0; y < 8; ++y) {
                         const int byte = (8 * i + y) * CB + cb;
-                        x[y] = w[y] * mx_float((vs[byte >> 2] >> (8 * (byte & 3))) & 255u);
+                        f[y] = w[y] * mx_float((vs[byte >> 4][(byte >> 2) & 3] >> (8 * (byte & 3))) & 255u);
                     }
                     bf16x8v pf[NP];
-                    split8<NP>(x, pf);
+                    split8<NP>(f, pf);
 #pragma unroll
-                    for (int t = 2 * cb; t < 2 * cb + 2; ++t) {
-                        const bf16x8v v = mx_bf16(vf[t][i], 1.f);
+                    for (int y = 0; y < X; ++y) {
+                        bf16x8v py[NP];
 #pragma unroll
-                        for (int p = 0; p < NP; ++p) acc[t] = mma16(v, pf[p], acc[t]);
+                        for (int p = 0; p < NP; ++p) py[p] = X > 1 ? of_copy(pf[p], x == y) : pf[p];
+#pragma unroll
+                        for (int t = 2 * cb; t < 2 * cb + 2; ++t) {
+                            const bf16x8v v = mx_bf16(vf[t][y * (4 / X) + i], 1.f);
+#pragma unroll
+                            for (int p = 0; p < NP; ++p) acc[t] = mma16(v, py[p], acc[t]);
+                        }
                     }
                 }
             }
         }
-        l += __shfl_xor(l, 16);
-        l += __shfl_xor(l, 32);
+        auto plus = [](float u, float v) { return u + v; };
+        l = over_blocks(over_copies<X>(l, plus), plus);
+#pragma unroll
+        for (int t = 0; t < DT; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[t][r] = over_copies<X>(acc[t][r], plus);
 
         // the four waves' parts, joined in LDS in wave order
         __syncthreads();
+        float* jo = reinterpret_cast<float*>(smem);
+        float* jm = jo + kMxWaves * 16 * kPitch;
         {
             float* dst = jo + (wave * 16 + c16) * kPitch + 4 * h4;
 #pragma unroll
@@ -302,33 +500,33 @@ __global__ __launch_bounds__(64 * kMxWaves, 2) void mx4_decode_kernel(
             }
         }
         __syncthreads();
-        const int row = threadIdx.x >> 4;
+        const int mr = threadIdx.x >> 4;
         const bool whole = take == sp.steps;
-        if (row < rows) {
+        if (mr < rows) {
             float mw[kMxWaves], M = -INFINITY;
 #pragma unroll
             for (int x = 0; x < kMxWaves; ++x) {
-                mw[x] = jm[(x * 16 + row) * 2];
+                mw[x] = jm[(x * 16 + mr) * 2];
                 M = fmaxf(M, mw[x]);
             }
             float lt = 0.f;
 #pragma unroll
             for (int x = 0; x < kMxWaves; ++x) {
                 mw[x] = mw[x] == -INFINITY ? 0.f : ex2((mw[x] - M) * c);
-                lt = fmaf(jm[(x * 16 + row) * 2 + 1], mw[x], lt);
+                lt = fmaf(jm[(x * 16 + mr) * 2 + 1], mw[x], lt);
             }
-            const int r = ht * 16 + row, i = r / a.G;
+            const int r = ht * 16 + mr, i = a.by_group(r);
             const size_t out = (static_cast<size_t>(b) * a.Tq + i) * a.Hq + hk * a.G + r - i * a.G;
             const float inv = lt == 0.f ? 0.f : 1.f / lt;
             // a shared unit's part: slot 1 holds its beginning, slot 0 what does not begin here
-            const size_t prow = (static_cast<size_t>(blockIdx.x) * 2 + (at_block == 0)) * a.heads + row;
+            const size_t prow = (static_cast<size_t>(blockIdx.x) * 2 + (at_block == 0)) * a.heads + mr;
 #pragma unroll
             for (int e = 0; e < D / 64; ++e) {
                 const int d = 64 * e + 4 * (threadIdx.x & 15);
                 f32x4 sum = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int x = 0; x < kMxWaves; ++x)  // a wave without keys holds zeros; one whose weight underflows may hold a NaN
-                    sum += *reinterpret_cast<const f32x4*>(jo + (x * 16 + row) * kPitch + d) * mw[x];
+                    sum += *reinterpret_cast<const f32x4*>(jo + (x * 16 + mr) * kPitch + d) * mw[x];
                 if (whole)
                     store4<T>(o + out * D + d, sum[0] * inv, sum[1] * inv, sum[2] * inv, sum[3] * inv);
                 else
@@ -341,7 +539,7 @@ __global__ __launch_bounds__(64 * kMxWaves, 2) void mx4_decode_kernel(
         }
         left -= take;
         at_block = 0;
-        ++unit;
+        ++unit_at;
         if (left > 0) __syncthreads();  // LDS is free for the next unit
     }
 }
@@ -628,18 +826,27 @@ Mx4Args mx4_args(int B, int Tq, int Hq, int Hkv, int page_size, int num_pages, i
     a.scale = scale;
     a.shares = mx4_shares(page_size, max_pages, window, sinks, Tq);
     a.heads = Tq * a.G < 16 ? Tq * a.G : 16;
+    a.by_group = FastDiv(a.G);
+    a.by_tiles = FastDiv(a.head_tiles);
     return a;
 }
 
-template <typename T, int D>
+template <typename T, int D, int X>
 hipError_t launch_mx4_decode_t(const Mx4Args& a, const void* q, const void* k_codes, const void* k_scales,
                                const void* v_codes, const void* v_scales, const int* table, const int* lengths, void* o,
                                float* ws, hipStream_t st) {
     const unsigned long long rows = static_cast<unsigned long long>(a.B) * a.Tq * a.Hq;
-    const unsigned long long most = (static_cast<unsigned long long>(a.max_pages) << a.page_shift) / kQuad + 2;
+    const unsigned long long most = (static_cast<unsigned long long>(a.max_pages) << a.page_shift) / kQuad + 2 + kUnitCost;
     return launch_dealt<T, D>(a, rows, most, 64 * kMxWaves, table, lengths, o, ws, st,
                               [&](unsigned blocks, float* part_o, float* part_ml) {
-                                  hipLaunchKernelGGL((mx4_decode_kernel<T, D>), dim3(blocks), dim3(64 * kMxWaves), 0, st, a,
+                                  auto* f = mx4_decode_kernel<T, D, X>;
+                                  constexpr int lds = Mx4Lds<D>::kBytes;
+                                  if (lds > 64 * 1024) {
+                                      const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(f),
+                                                                               hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+                                      if (e != hipSuccess) return e;
+                                  }
+                                  hipLaunchKernelGGL(f, dim3(blocks), dim3(64 * kMxWaves), lds, st, a,
                                                      static_cast<const T*>(q), static_cast<const uint8_t*>(k_codes),
                                                      static_cast<const uint8_t*>(k_scales),
                                                      static_cast<const uint8_t*>(v_codes),
@@ -661,9 +868,15 @@ hipError_t launch_attn_decode_mx4(int dtype, int B, int Tq, int Hq, int Hkv, int
                                   const void* k_scales, const void* v_codes, const void* v_scales, const int* table,
                                   const int* lengths, void* o, float* ws, hipStream_t st) {
     const attn::Mx4Args a = attn::mx4_args(B, Tq, Hq, Hkv, page_size, num_pages, max_pages, window, sinks, scale);
-    auto* f = dtype == GDR_DTYPE_F32
-                  ? (d == 64 ? attn::launch_mx4_decode_t<float, 64> : attn::launch_mx4_decode_t<float, 128>)
-                  : (d == 64 ? attn::launch_mx4_decode_t<bf16_t, 64> : attn::launch_mx4_decode_t<bf16_t, 128>);
+    auto* f = d == 64 ? attn::launch_mx4_decode_t<float, 64, 1> : attn::launch_mx4_decode_t<float, 128, 1>;
+    if (dtype == GDR_DTYPE_BF16) {
+        if (a.heads <= 4)
+            f = d == 64 ? attn::launch_mx4_decode_t<bf16_t, 64, 4> : attn::launch_mx4_decode_t<bf16_t, 128, 4>;
+        else if (a.heads <= 8)
+            f = d == 64 ? attn::launch_mx4_decode_t<bf16_t, 64, 2> : attn::launch_mx4_decode_t<bf16_t, 128, 2>;
+        else
+            f = d == 64 ? attn::launch_mx4_decode_t<bf16_t, 64, 1> : attn::launch_mx4_decode_t<bf16_t, 128, 1>;
+    }
     return f(a, q, k_codes, k_scales, v_codes, v_scales, table, lengths, o, ws, st);
 }
 
