@@ -27,44 +27,50 @@ struct JoinRow {
 // The blocks of the batch in a row: sequence by sequence, within one unit by
 // unit, per() units each.  A wave sums them 256
 // sequences at a time, four to a lane, so that their lengths come together.
-__device__ __forceinline__ int scan64(int x, int lane) {  // inclusive
-#pragma unroll
-    for (int s = 1; s < 64; s <<= 1) {
-        const int y = __shfl_up(x, s);
-        if (lane >= s) x += y;
-    }
+// The sums are formed in registers (shifts inside 16 lanes, then the sums of the
+// 16 and 32 lanes before).
+__device__ __forceinline__ int scan64(int x) {  // inclusive
+    x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);
     return x;
 }
 struct Blocks4 {
-    int each[4], upto;  // of sequences at + 4 lane .. + 3; blocks of at .. and these
+    int len[4], each[4], upto;  // of sequences at + 4 lane .. + 3; blocks of at .. and these
 };
 template <typename A>
 __device__ __forceinline__ Blocks4 blocks_of(const A& a, int at, const int* __restrict__ lengths, int lane) {
     Blocks4 r;
-    int sum = 0, len[4];
+    int sum = 0;
 #pragma unroll
-    for (int x = 0; x < 4; ++x) len[x] = at + 4 * lane + x < a.B ? lengths[at + 4 * lane + x] : -1;
+    for (int x = 0; x < 4; ++x) r.len[x] = at + 4 * lane + x < a.B ? lengths[at + 4 * lane + x] : -1;
 #pragma unroll
-    for (int x = 0; x < 4; ++x) sum += r.each[x] = a.blocks(len[x]);
-    r.upto = scan64(sum, lane);
+    for (int x = 0; x < 4; ++x) sum += r.each[x] = a.blocks(r.len[x]);
+    r.upto = scan64(sum);
     return r;
 }
-// Blocks of one unit per sequence: of the whole batch, and of the sequences before b.
+__device__ __forceinline__ int of4(const int (&v)[4], int x) { return x == 0 ? v[0] : x == 1 ? v[1] : x == 2 ? v[2] : v[3]; }
+// Blocks of one unit per sequence: of the whole batch; of the sequences before b, of b itself, and b's length.
 template <typename A>
-__device__ __forceinline__ long long all_blocks(const A& a, const int* lengths, int lane, int b, long long& before) {
+__device__ __forceinline__ long long all_blocks(const A& a, const int* lengths, int lane, int b, long long& before, int& mine,
+                                                int& len) {
     long long sum = 0;
-    before = 0;
     for (int at = 0; at < a.B; at += 256) {
         const Blocks4 r = blocks_of(a, at, lengths, lane);
         if (b >= at && b < at + 256) {
             const int x = b - at, rest = x & 3;
-            int mine = r.upto;  // up to and with this lane's four, less those not before b
+            int upto = r.upto;  // up to and with this lane's four, less those not before b
 #pragma unroll
             for (int y = 0; y < 4; ++y)
-                if (y >= rest) mine -= r.each[y];
-            before = sum + __shfl(mine, x >> 2);
+                if (y >= rest) upto -= r.each[y];
+            before = sum + __builtin_amdgcn_readlane(upto, x >> 2);
+            mine = __builtin_amdgcn_readlane(of4(r.each, rest), x >> 2);
+            len = __builtin_amdgcn_readlane(of4(r.len, rest), x >> 2);
         }
-        sum += __shfl(r.upto, 63);
+        sum += __builtin_amdgcn_readlane(r.upto, 63);
     }
     return sum;
 }
@@ -83,9 +89,9 @@ __device__ __forceinline__ int owner(long long g, long long n, int W) {
     return static_cast<int>(divide((g + 1) * W - 1, n));
 }
 
-// A workgroup's blocks: [at_block, at_block + left) of unit `unit` of sequence b and on.
+// A workgroup's blocks: [at_block, at_block + left) of unit `unit` of sequence b (of length len) and on.
 struct Share {
-    int b, unit, at_block, left;
+    int b, len, unit, at_block, left;
 };
 // The share of workgroup `bid`; false: it has none.
 template <typename A>
@@ -93,21 +99,26 @@ __device__ __forceinline__ bool find_share(const A& a, const int* __restrict__ l
     const int per = a.per();
     if (a.shares == 0) {
         s.b = bid / per;
+        s.len = __builtin_amdgcn_readfirstlane(lengths[s.b]);
         s.unit = bid - s.b * per;
         s.at_block = 0;
-        s.left = a.blocks(lengths[s.b]);
+        s.left = a.blocks(s.len);
         return true;
     }
-    long long before;
-    const long long n = per * all_blocks(a, lengths, lane, -1, before);
+    long long n = 0;
+    Blocks4 r;
+    for (int at = 0; at < a.B; at += 256) {
+        r = blocks_of(a, at, lengths, lane);
+        n += __builtin_amdgcn_readlane(r.upto, 63);
+    }
+    n *= per;
     const int W = shares_of(a, n);
     if (bid >= W) return false;
     const long long lo = divide(n * bid, W), hi = divide(n * (bid + 1), W);
-    s.left = __builtin_amdgcn_readfirstlane(static_cast<int>(hi - lo));
-    before = 0;  // per unit
-    int b;
-    for (b = 0; b < a.B; b += 256) {  // the first sequence that ends after lo
-        const Blocks4 r = blocks_of(a, b, lengths, lane);
+    s.left = static_cast<int>(hi - lo);
+    long long before = 0;  // per unit
+    for (int b = 0; b < a.B; b += 256) {  // the first sequence that ends after lo
+        if (a.B > 256) r = blocks_of(a, b, lengths, lane);
         const uint64_t past = __ballot((before + r.upto) * per > lo);
         if (past) {
             int x = 0, upto = r.upto - r.each[0] - r.each[1] - r.each[2] - r.each[3];
@@ -118,19 +129,18 @@ __device__ __forceinline__ bool find_share(const A& a, const int* __restrict__ l
                     ++x;
                 }
             const int from = __builtin_ctzll(past);
-            before += __shfl(upto, from);
-            b += 4 * from + __shfl(x, from);
-            break;
+            before += __builtin_amdgcn_readlane(upto, from);
+            s.b = b + 4 * from + __builtin_amdgcn_readlane(x, from);
+            s.len = __builtin_amdgcn_readlane(of4(r.len, x), from);
+            const int blocks = __builtin_amdgcn_readlane(of4(r.each, x), from);
+            const long long in = lo - before * per;
+            s.unit = static_cast<int>(divide(in, max(1, blocks)));
+            s.at_block = static_cast<int>(in - static_cast<long long>(s.unit) * blocks);
+            return true;
         }
-        before += __shfl(r.upto, 63);
+        before += __builtin_amdgcn_readlane(r.upto, 63);
     }
-    s.b = b = __builtin_amdgcn_readfirstlane(b);
-    if (b >= a.B) return false;  // not reached unless the lengths change under the call
-    const int blocks = a.blocks(lengths[b]);
-    const long long in = lo - before * per;
-    s.unit = __builtin_amdgcn_readfirstlane(static_cast<int>(divide(in, max(1, blocks))));
-    s.at_block = __builtin_amdgcn_readfirstlane(static_cast<int>(in - static_cast<long long>(s.unit) * blocks));
-    return true;
+    return false;  // not reached unless the lengths change under the call
 }
 
 // Joins the parts of a shared unit, W waves per query head: part 0 is slot 1 of
@@ -148,11 +158,11 @@ __global__ __launch_bounds__(256) void join_kernel(A a, int rows, const int* __r
     const int at = blockIdx.x * (4 / W) + every / W;
     if (at >= rows) return;
     const JoinRow jr = a.row(at);
-    const int len = lengths[jr.b], blocks = a.blocks(len);
-    if (blocks == 0 || a.skipped(jr.b, len, table)) return;
     const int per = a.per();
-    long long before;
-    const long long n = per * all_blocks(a, lengths, lane, jr.b, before);
+    long long before = 0;
+    int blocks = 0, len = -1;
+    const long long n = per * all_blocks(a, lengths, lane, jr.b, before, blocks, len);
+    if (blocks == 0 || a.skipped(jr.b, len, table)) return;
     const long long lo = per * before + static_cast<long long>(jr.unit) * blocks;
     const int used = shares_of(a, n), w0 = owner(lo, n, used), parts = owner(lo + blocks - 1, n, used) - w0 + 1;
     if (parts == 1) return;  // written whole

@@ -174,7 +174,7 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(T) * D <= 256 ? 2 : 1) void dec
     Share share;
     if (!find_share(a, lengths, lane, blockIdx.x, share)) return;
     int b = share.b, unit = share.unit, at_block = share.at_block, left = share.left;
-    Span sp = span_of(a, lengths[b]);
+    Span sp = span_of(a, share.len);
 
 #pragma unroll 1
     while (left > 0) {

@@ -211,17 +211,15 @@ __global__ __launch_bounds__(64 * kMxWaves, 2) void mx4_decode_kernel(
 
     Share share;
     if (!find_share(a, lengths, lane, blockIdx.x, share)) return;
-    int b = __builtin_amdgcn_readfirstlane(share.b), unit_at = __builtin_amdgcn_readfirstlane(share.unit);
-    int at_block = __builtin_amdgcn_readfirstlane(share.at_block), left = __builtin_amdgcn_readfirstlane(share.left);
-    auto span = [&](int b) { return mx_span(a, __builtin_amdgcn_readfirstlane(lengths[b])); };
-    MxSpan sp = span(b);
+    int b = share.b, unit_at = share.unit, at_block = share.at_block, left = share.left;
+    MxSpan sp = mx_span(a, share.len);
 
 #pragma unroll 1
     while (left > 0) {
         if (unit_at >= per || sp.steps == 0) {  // the next sequence that is not skipped
             if (++b >= a.B) return;
             unit_at = 0;
-            sp = span(b);
+            sp = mx_span(a, __builtin_amdgcn_readfirstlane(lengths[b]));
             continue;
         }
         const int take = min(left, sp.steps - at_block);
@@ -298,6 +296,11 @@ __global__ __launch_bounds__(64 * kMxWaves, 2) void mx4_decode_kernel(
                 row[x] = row_of(4 * step + x, page[x]);
                 page[x] = next[x];
             }
+            if (step < end) {
+                copy_keys(row);
+                copy_values(row);
+            }
+            // (waiting for the query, the compiler waits for the copies too, once a unit)
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
                 float f[8];
@@ -310,10 +313,6 @@ __global__ __launch_bounds__(64 * kMxWaves, 2) void mx4_decode_kernel(
                     for (int p = 0; p < NP; ++p) qf[y][s][p] = X > 1 ? kept(of_copy(qf[y][s][p], x == y)) : qf[y][s][p];
                 }
             }
-        }
-        if (step < end) {
-            copy_keys(row);
-            copy_values(row);
         }
 
         f32x4 acc[DT];
