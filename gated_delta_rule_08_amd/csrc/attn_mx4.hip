@@ -566,19 +566,23 @@ struct MxRun {
 // token of a sequence, or one at the start of a block.  So no block is written
 // from two places, except where sequences share a page.
 template <typename F> __device__ __forceinline__ void for_runs(const MxPlace& pl, int wave_range, int lane, F f) {
-    const int t = wave_range * pl.range + lane;
+    const int t0 = wave_range * pl.range, t = t0 + lane;
     bool lead = false;
     int count = 0, slot = 0;
     int row = 0;
+    // The last sequence that starts at or before t0: 64 of the offsets at a time, then
+    // what is left between two of them.
+    int s0 = 0;
+    for (int n = pl.N; n > 0;) {
+        const int step = (n + 63) / 64, at = lane * step;
+        const uint64_t upto = __ballot(at < n && pl.cu[s0 + min(at, n - 1)] <= t0);
+        const int k = max((upto == ~0ull ? 64 : __builtin_ctzll(~upto)) - 1, 0);
+        s0 += k * step;
+        n = step == 1 ? 0 : min(step, n - k * step);
+    }
     if (lane < pl.range && t < pl.total) {
-        int s = 0;  // the last sequence that starts at or before t
-        for (int hi = pl.N; hi - s > 1;) {
-            const int mid = (s + hi) >> 1;
-            if (pl.cu[mid] <= t)
-                s = mid;
-            else
-                hi = mid;
-        }
+        int s = s0;
+        while (s + 1 < pl.N && pl.cu[s + 1] <= t) ++s;
         const int begin = pl.cu[s], end = min(pl.cu[s + 1], pl.total), from = pl.first ? pl.first[s] : 0;
         const long long pos = static_cast<long long>(from) + (static_cast<long long>(t) - begin);
         slot = static_cast<int>(pos & (kMxRows - 1));
@@ -603,189 +607,267 @@ template <typename F> __device__ __forceinline__ void for_runs(const MxPlace& pl
     }
 }
 
-// The largest magnitude's bits over the lanes that share a block: 32 / N lanes of N channels each.
-template <int N> __device__ __forceinline__ uint32_t block_max(uint32_t x) {
-#pragma unroll
-    for (int s = 1; s < kMxBlock / N; s <<= 1) x = max(x, static_cast<uint32_t>(__shfl_xor(static_cast<int>(x), s)));
-    return x;
-}
+// How the append and the read go through a run: lane (u, r), u = lane % 16, has 8
+// channels of the positions 8 r .. 8 r + 7 of the block, 128 channels in all: one
+// head's, or with d = 64 two heads'.  Rows of the dense tensors are then read and
+// written 16 bytes (fp32: 32) a lane, whole lines together.  Keys are 4 bytes a
+// lane and position as they lie in the cache.  Values have the lane's 8 x 8 codes
+// transposed, and 8 words of a channel each exchanged between the four r, so that
+// each has all 16 bytes of two of the 8 channels.
 
-// N consecutive elements as fp32.
-template <int N> __device__ __forceinline__ void load_f32(const bf16_t* p, float (&x)[N]) {
-    if constexpr (N == 2) {
-        const uint32_t u = *reinterpret_cast<const uint32_t*>(p);
-        x[0] = __uint_as_float(u << 16);
-        x[1] = __uint_as_float(u & 0xffff0000u);
-    } else {
-        x[0] = bf16_to_f32(*p);
-    }
-}
-template <int N> __device__ __forceinline__ void load_f32(const float* p, float (&x)[N]) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = p[i];
-}
-
-// 32 elements as fp32 (16-byte aligned).
-__device__ __forceinline__ void load32(const bf16_t* p, float (&x)[32]) {
+// w[i] nibble k <-> w[k] nibble i.
+__device__ __forceinline__ void transpose8(uint32_t (&w)[8]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const u32x4 u = *reinterpret_cast<const u32x4*>(p + 8 * i);
+        const uint32_t a = w[i], b = w[i + 4];
+        w[i] = __builtin_amdgcn_perm(b, a, 0x05040100);
+        w[i + 4] = __builtin_amdgcn_perm(b, a, 0x07060302);
+    }
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-            x[8 * i + 2 * y] = __uint_as_float(u[y] << 16);
-            x[8 * i + 2 * y + 1] = __uint_as_float(u[y] & 0xffff0000u);
-        }
+    for (int j = 0; j < 4; ++j) {
+        const int i = (j & 1) | (j & 2) << 1;
+        const uint32_t a = w[i], b = w[i + 2];
+        w[i] = __builtin_amdgcn_perm(b, a, 0x06020400);
+        w[i + 2] = __builtin_amdgcn_perm(b, a, 0x07030501);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        const uint32_t a = w[i], b = w[i + 1];
+        w[i] = (a & 0x0f0f0f0fu) | (b & 0x0f0f0f0fu) << 4;
+        w[i + 1] = (a >> 4 & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u);
     }
 }
-__device__ __forceinline__ void load32(const float* p, float (&x)[32]) {
+__device__ __forceinline__ void swap32(uint32_t& a, uint32_t& b) {  // a's upper half lanes with b's lower
+    const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+    a = r[0];
+    b = r[1];
+}
+__device__ __forceinline__ void swap16(uint32_t& a, uint32_t& b) {  // a's odd 16 lanes with b's even
+    const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+    a = r[0];
+    b = r[1];
+}
+// The words of 8 channels for this lane's 8 positions, to and from all 32 positions
+// of channels 2 r and 2 r + 1.
+__device__ __forceinline__ void gather_channels(uint32_t (&w)[8], u32x4 (&c)[2]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const f32x4 u = *reinterpret_cast<const f32x4*>(p + 4 * i);
+    for (int k = 0; k < 4; ++k) swap32(w[k], w[k + 4]);
 #pragma unroll
-        for (int y = 0; y < 4; ++y) x[4 * i + y] = u[y];
+    for (int k = 0; k < 2; ++k) {
+        swap16(w[k], w[k + 2]);
+        swap16(w[k + 4], w[k + 6]);
+        c[k] = u32x4{w[k], w[k + 2], w[k + 4], w[k + 6]};
     }
+}
+__device__ __forceinline__ void spread_channels(const u32x4 (&c)[2], uint32_t (&w)[8]) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        w[k] = c[k][0];
+        w[k + 2] = c[k][1];
+        w[k + 4] = c[k][2];
+        w[k + 6] = c[k][3];
+        swap16(w[k], w[k + 2]);
+        swap16(w[k + 4], w[k + 6]);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) swap32(w[k], w[k + 4]);
 }
 
-// Append: a wave per (range of tokens, head).  Keys: a lane quantises 32 channels
-// of a position by itself.  Values: a lane has 1 or 2 channels and goes through
-// the positions, so that it ends with the 16 bytes of its channels; a block that
-// the run covers in part keeps its other positions.
+// The 8 codes of x, and the scale of the block of 32 that it shares with the three
+// lanes beside it.
+__device__ __forceinline__ uint32_t quantise8(const float (&x)[8], uint32_t& scale) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, magnitude(x[i]));
+    top = max(top, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(top), 0xB1, 0xf, 0xf, true)));
+    top = max(top, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(top), 0x4E, 0xf, 0xf, true)));
+    scale = mx_scale(top);
+    const float inv = mx_inverse(scale);
+    uint32_t w = 0;
+    w = mx_put<0>(w, x[0] * inv, x[1] * inv);
+    w = mx_put<1>(w, x[2] * inv, x[3] * inv);
+    w = mx_put<2>(w, x[4] * inv, x[5] * inv);
+    w = mx_put<3>(w, x[6] * inv, x[7] * inv);
+    return scale == kMxNan ? 0 : w;
+}
+
+// A lane's place in a run.
+template <int D> struct MxLane {
+    static constexpr int kHeads = 128 / D;  // of a wave
+    int u, r;
+    bool live;    // its head exists
+    int head;     // its head (one that exists)
+    int channel;  // its first channel in the head
+    __device__ __forceinline__ MxLane(int lane, int group, int Hkv) {
+        u = lane & 15;
+        r = lane >> 4;
+        const int h = group * kHeads + u / (D / 8);
+        live = h < Hkv;
+        head = min(h, Hkv - 1);
+        channel = 8 * (u % (D / 8));
+    }
+};
+
+// Append: a wave per (range of tokens, 128 channels).  A block that the run covers
+// in part keeps its other positions.  The values are loaded once the keys' registers
+// are free, which leaves room for four waves a SIMD (both at once: 142 registers
+// and 2 us more).  Bound by HBM: 8 prompts of 1000 .. 4096 tokens, 8 heads of 128,
+// 105 MB, 25 us; the read of the same and 100 tokens more each, 109 MB, 22 us.
 template <typename T, int D>
-__global__ __launch_bounds__(256) void mx4_append_kernel(MxPlace pl, FastDiv heads, int waves, const T* __restrict__ k,
+__global__ __launch_bounds__(256) void mx4_append_kernel(MxPlace pl, FastDiv groups, int waves, const T* __restrict__ k,
                                                          const T* __restrict__ v, uint8_t* __restrict__ k_codes,
                                                          uint8_t* __restrict__ k_scales, uint8_t* __restrict__ v_codes,
                                                          uint8_t* __restrict__ v_scales) {
-    constexpr int CB = D / 32, N = D / 64;
+    constexpr int CB = D / 32;
     const int lane = threadIdx.x & 63, id = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
     if (id >= waves) return;
-    const int range = heads(id), hk = id - range * heads.d;
+    const int range = groups(id);
+    const MxLane<D> ln(lane, id - range * groups.d, pl.Hkv);
     for_runs(pl, range, lane, [&](const MxRun& r) {
-        const size_t row = r.row + (static_cast<size_t>(hk) << pl.page_shift);
-        const size_t stride = static_cast<size_t>(pl.Hkv) * D;
-        const size_t from = static_cast<size_t>(r.token) * stride + static_cast<size_t>(hk) * D;
-        // keys
-#pragma unroll 1
-        for (int j = lane / CB; j < r.count; j += 64 / CB) {
-            const int cb = lane % CB;
-            float x[32];
-            load32(k + from + j * stride + 32 * cb, x);
-            uint32_t top = 0;
+        const size_t row = r.row + (static_cast<size_t>(ln.head) << pl.page_shift);
+        // the run's tokens: 32-bit offsets from its first
+        const uint32_t stride = static_cast<uint32_t>(pl.Hkv) * D, mine = static_cast<uint32_t>(ln.head) * D + ln.channel;
+        const T *kt = k + static_cast<size_t>(r.token) * stride, *vt = v + static_cast<size_t>(r.token) * stride;
+        const bool all = r.count == kMxRows;
+        auto token = [&](int i) { return min(max(8 * ln.r + i - r.slot, 0), r.count - 1); };  // outside the run: its first or last
+        auto within = [&](int i) { return ln.live && 8 * ln.r + i >= r.slot && 8 * ln.r + i < r.slot + r.count; };
+        frag_t<T> x[2][8];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) top = max(top, magnitude(x[i]));
-            const uint32_t e = mx_scale(top);
-            const float inv = mx_inverse(e);
-            u32x4 w = {0, 0, 0, 0};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                w[i] = mx_put<0>(w[i], x[8 * i] * inv, x[8 * i + 1] * inv);
-                w[i] = mx_put<1>(w[i], x[8 * i + 2] * inv, x[8 * i + 3] * inv);
-                w[i] = mx_put<2>(w[i], x[8 * i + 4] * inv, x[8 * i + 5] * inv);
-                w[i] = mx_put<3>(w[i], x[8 * i + 6] * inv, x[8 * i + 7] * inv);
-                if (e == kMxNan) w[i] = 0;
-            }
-            const size_t to = row + r.slot + j;
-            *reinterpret_cast<u32x4*>(k_codes + to * (D / 2) + 16 * cb) = w;
-            k_scales[to * CB + cb] = static_cast<uint8_t>(e);
+        for (int i = 0; i < 8; ++i) x[0][i] = load8(kt + (token(i) * stride + mine));
+        u32x4* at = reinterpret_cast<u32x4*>(v_codes + row * (D / 2) + static_cast<size_t>(ln.channel + 2 * ln.r) * 16);
+        u32x4 old[2] = {};
+        if (!all) {
+            old[0] = at[0];
+            old[1] = at[1];
         }
-        // values
-        u32x4* at = reinterpret_cast<u32x4*>(v_codes + row * (D / 2) + static_cast<size_t>(lane) * N * 16);
-        u32x4 w[N];
+        uint32_t w[8], e[8];
+        auto quantise = [&](const frag_t<T> (&x)[8]) {
 #pragma unroll
-        for (int n = 0; n < N; ++n) w[n] = r.count < kMxRows ? at[n] : u32x4{0, 0, 0, 0};
-        const int sub = lane % (kMxBlock / N);  // of the lanes of a block of channels
+            for (int i = 0; i < 8; ++i) {
+                float f[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float x[8][N];
-#pragma unroll
-            for (int y = 0; y < 8; ++y) {  // positions outside the run repeat its first or last
-                const int j = min(max(8 * i + y - r.slot, 0), r.count - 1);
-                load_f32<N>(v + from + j * stride + lane * N, x[y]);
+                for (int y = 0; y < 8; ++y) f[y] = static_cast<float>(x[i][y]);
+                w[i] = quantise8(f, e[i]);
             }
+        };
+        // a head's scales of a position in one word (d = 64: half), from the lanes that have its blocks
+        auto put_scales = [&](uint8_t* scales) {
 #pragma unroll
-            for (int y = 0; y < 8; ++y) {
-                const int j = 8 * i + y;
-                uint32_t top = magnitude(x[y][0]);
-                if constexpr (N == 2) top = max(top, magnitude(x[y][1]));
-                const uint32_t e = mx_scale(block_max<N>(top));
-                const float inv = mx_inverse(e);
-                uint32_t code = mx_put<0>(0, x[y][0] * inv, x[y][N - 1] * inv);  // a channel a half
-                if (e == kMxNan) code = 0;
-                if (j >= r.slot && j < r.slot + r.count) {
-                    const uint32_t keep = ~(15u << (4 * y));
-                    w[0][i] = (w[0][i] & keep) | ((code & 15u) << (4 * y));
-                    if constexpr (N == 2) w[1][i] = (w[1][i] & keep) | ((code >> 4) << (4 * y));
-                    if (sub == j % (kMxBlock / N)) v_scales[(row + j) * CB + lane * N / kMxBlock] = static_cast<uint8_t>(e);
+            for (int i = 0; i < 8; ++i) {
+                uint32_t s = e[i];
+                s |= static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(e[i]), 0x104, 0xf, 0xf, true)) << 8;
+                if constexpr (CB == 4) {
+                    s |= static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(s), 0x108, 0xf, 0xf, true)) << 16;
+                }
+                e[i] = s;
+            }
+            if (ln.channel != 0 || !ln.live) return;
+            uint8_t* p = scales + (row + 8 * ln.r) * CB;
+            if (all) {
+                if constexpr (CB == 4) {
+                    reinterpret_cast<u32x4*>(p)[0] = u32x4{e[0], e[1], e[2], e[3]};
+                    reinterpret_cast<u32x4*>(p)[1] = u32x4{e[4], e[5], e[6], e[7]};
+                } else {
+                    u32x4 t;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) t[i] = (e[2 * i] & 0xffffu) | e[2 * i + 1] << 16;
+                    reinterpret_cast<u32x4*>(p)[0] = t;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if (!within(i)) continue;
+                    if constexpr (CB == 4)
+                        reinterpret_cast<uint32_t*>(p)[i] = e[i];
+                    else
+                        reinterpret_cast<uint16_t*>(p)[i] = static_cast<uint16_t>(e[i]);
                 }
             }
-        }
+        };
+        quantise(x[0]);
 #pragma unroll
-        for (int n = 0; n < N; ++n) at[n] = w[n];
+        for (int i = 0; i < 8; ++i)
+            if (within(i)) *reinterpret_cast<uint32_t*>(k_codes + (row + 8 * ln.r + i) * (D / 2) + ln.channel / 2) = w[i];
+        put_scales(k_scales);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[1][i] = load8(vt + (token(i) * stride + mine));
+        quantise(x[1]);
+        put_scales(v_scales);
+        transpose8(w);
+        u32x4 c[2];
+        gather_channels(w, c);
+        if (!all) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {  // 8 positions a word
+                const int lo = min(max(r.slot - 8 * i, 0), 8), hi = min(max(r.slot + r.count - 8 * i, 0), 8);
+                const uint32_t mask = (hi == 8 ? 0xffffffffu : (1u << 4 * hi) - 1) & ~(lo == 8 ? 0xffffffffu : (1u << 4 * lo) - 1);
+#pragma unroll
+                for (int n = 0; n < 2; ++n) c[n][i] = (c[n][i] & mask) | (old[n][i] & ~mask);
+            }
+        }
+        if (ln.live) {
+            at[0] = c[0];
+            at[1] = c[1];
+        }
     });
 }
 
-__device__ __forceinline__ void store_f32(bf16_t* p, float a, float b) {
-    *reinterpret_cast<uint32_t*>(p) = f32_to_bf16(a) | static_cast<uint32_t>(f32_to_bf16(b)) << 16;
+// The 8 codes of a word times the scale of byte b, exactly, 16 bytes aligned.
+__device__ __forceinline__ void store8(bf16_t* p, uint32_t w, uint32_t b) {
+    u32x4 x = __builtin_bit_cast(u32x4, mx_bf16(w, mx_float(b)));
+    if (b == kMxNan) x = u32x4{0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u};
+    *reinterpret_cast<u32x4*>(p) = x;
 }
-__device__ __forceinline__ void store_f32(float* p, float a, float b) {
-    p[0] = a;
-    p[1] = b;
+__device__ __forceinline__ void store8(float* p, uint32_t w, uint32_t b) {
+    const bf16x8v x = mx_bf16(w, 1.f);
+    const float f = b == kMxNan ? NAN : mx_float(b);
+    f32x4 lo, hi;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        lo[i] = static_cast<float>(x[i]) * f;
+        hi[i] = static_cast<float>(x[4 + i]) * f;
+    }
+    reinterpret_cast<f32x4*>(p)[0] = lo;
+    reinterpret_cast<f32x4*>(p)[1] = hi;
 }
 
-// Code c (4 bits) times the scale of byte b; NaN where b is 255.
-__device__ __forceinline__ float mx_value(uint32_t c, uint32_t b) {
-    typedef float f32x2v __attribute__((ext_vector_type(2)));
-    const f32x2v x = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.f, 0);
-    return b == kMxNan ? NAN : x[0] * mx_float(b);
-}
-
-// Read: the same runs, the other way.  Every value is exact in both types.
+// Read: the same runs, the other way.
 template <typename T, int D>
-__global__ __launch_bounds__(256) void mx4_read_kernel(MxPlace pl, FastDiv heads, int waves,
+__global__ __launch_bounds__(256) void mx4_read_kernel(MxPlace pl, FastDiv groups, int waves,
                                                        const uint8_t* __restrict__ k_codes,
                                                        const uint8_t* __restrict__ k_scales,
                                                        const uint8_t* __restrict__ v_codes,
                                                        const uint8_t* __restrict__ v_scales, T* __restrict__ k,
                                                        T* __restrict__ v) {
-    constexpr int CB = D / 32, N = D / 64;
+    constexpr int CB = D / 32;
     const int lane = threadIdx.x & 63, id = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
     if (id >= waves) return;
-    const int range = heads(id), hk = id - range * heads.d;
+    const int range = groups(id);
+    const MxLane<D> ln(lane, id - range * groups.d, pl.Hkv);
     for_runs(pl, range, lane, [&](const MxRun& r) {
-        const size_t row = r.row + (static_cast<size_t>(hk) << pl.page_shift);
-        const size_t stride = static_cast<size_t>(pl.Hkv) * D;
-        const size_t to = static_cast<size_t>(r.token) * stride + static_cast<size_t>(hk) * D;
-        // keys
-#pragma unroll 1
-        for (int j = lane / CB; j < r.count; j += 64 / CB) {
-            const int cb = lane % CB;
-            const size_t from = row + r.slot + j;
-            const u32x4 w = *reinterpret_cast<const u32x4*>(k_codes + from * (D / 2) + 16 * cb);
-            const uint32_t e = k_scales[from * CB + cb];
-            T* p = k + to + j * stride + 32 * cb;
+        const size_t row = r.row + (static_cast<size_t>(ln.head) << pl.page_shift) + 8 * ln.r;
+        const uint32_t stride = static_cast<uint32_t>(pl.Hkv) * D, mine = static_cast<uint32_t>(ln.head) * D + ln.channel;
+        T *kt = k + static_cast<size_t>(r.token) * stride, *vt = v + static_cast<size_t>(r.token) * stride;
+        auto within = [&](int i) { return ln.live && 8 * ln.r + i >= r.slot && 8 * ln.r + i < r.slot + r.count; };
+        uint32_t w[2][8], e[2][8];
+        u32x4 c[2];
+        const u32x4* at = reinterpret_cast<const u32x4*>(v_codes + (row - 8 * ln.r) * (D / 2) +
+                                                         static_cast<size_t>(ln.channel + 2 * ln.r) * 16);
+        c[0] = at[0];
+        c[1] = at[1];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                float x[4];
-#pragma unroll
-                for (int y = 0; y < 4; ++y) x[y] = mx_value((w[i >> 1] >> (16 * (i & 1) + 4 * y)) & 15u, e);
-                store4<T>(p + 4 * i, x[0], x[1], x[2], x[3]);
-            }
+        for (int i = 0; i < 8; ++i) {
+            w[0][i] = *reinterpret_cast<const uint32_t*>(k_codes + (row + i) * (D / 2) + ln.channel / 2);
+            e[0][i] = k_scales[(row + i) * CB + ln.channel / 32];
+            e[1][i] = v_scales[(row + i) * CB + ln.channel / 32];
         }
-        // values
-        const u32x4* at = reinterpret_cast<const u32x4*>(v_codes + row * (D / 2) + static_cast<size_t>(lane) * N * 16);
-        u32x4 w[N];
+        spread_channels(c, w[1]);
+        transpose8(w[1]);
 #pragma unroll
-        for (int n = 0; n < N; ++n) w[n] = at[n];
+        for (int n = 0; n < 2; ++n)
 #pragma unroll
-        for (int j = 0; j < kMxRows; ++j) {
-            if (j < r.slot || j >= r.slot + r.count) continue;
-            const uint32_t e = v_scales[(row + j) * CB + lane * N / kMxBlock];
-            const float a = mx_value((w[0][j >> 3] >> (4 * (j & 7))) & 15u, e);
-            T* p = v + to + (j - r.slot) * stride + lane * N;
-            if constexpr (N == 2)
-                store_f32(p, a, mx_value((w[1][j >> 3] >> (4 * (j & 7))) & 15u, e));
-            else
-                Elem<T>::store(p, a);
-        }
+            for (int i = 0; i < 8; ++i)
+                if (within(i)) store8((n ? vt : kt) + (static_cast<uint32_t>(8 * ln.r + i - r.slot) * stride + mine), w[n][i], e[n][i]);
     });
 }
 
@@ -796,9 +878,14 @@ int log2_of(int x) {
 }
 
 MxPlace place_of(int N, int total, int Hkv, int page_size, int num_pages, int max_pages, const int* cu, const int* first,
-                 const int* table, unsigned long long& waves) {
-    MxPlace pl{N, total, Hkv, log2_of(page_size), num_pages, max_pages, 32, cu, first, table};
-    waves = (static_cast<unsigned long long>(total) + pl.range - 1) / pl.range * Hkv;
+                 const int* table, int d, int& groups, unsigned long long& waves) {
+    // A wave goes through its runs one after another: a range holds about as many
+    // tokens as a run does.
+    const int mean = total / N;
+    const int range = mean >= 32 ? 32 : mean >= 8 ? 8 : 2;
+    MxPlace pl{N, total, Hkv, log2_of(page_size), num_pages, max_pages, range, cu, first, table};
+    groups = d == 64 ? (Hkv + 1) / 2 : Hkv;
+    waves = (static_cast<unsigned long long>(total) + range - 1) / range * groups;
     return pl;
 }
 
@@ -883,13 +970,14 @@ hipError_t launch_attn_append_mx4(int dtype, int N, int total, int Hkv, int d, i
                                   const void* k, const void* v, const int* cu, const int* lengths, void* k_codes,
                                   void* k_scales, void* v_codes, void* v_scales, const int* table, hipStream_t st) {
     unsigned long long waves;
-    const attn::MxPlace pl = attn::place_of(N, total, Hkv, page_size, num_pages, max_pages, cu, lengths, table, waves);
+    int groups;
+    const attn::MxPlace pl = attn::place_of(N, total, Hkv, page_size, num_pages, max_pages, cu, lengths, table, d, groups, waves);
     const unsigned long long blocks = (waves + 3) / 4;
     if (!grid_fits(blocks, 256)) return hipErrorInvalidConfiguration;
     auto go = [&](auto t, auto dd) {
         using T = decltype(t);
         hipLaunchKernelGGL((attn::mx4_append_kernel<T, decltype(dd)::value>), dim3(static_cast<unsigned>(blocks)), dim3(256),
-                           0, st, pl, attn::FastDiv(Hkv), static_cast<int>(waves), static_cast<const T*>(k),
+                           0, st, pl, attn::FastDiv(groups), static_cast<int>(waves), static_cast<const T*>(k),
                            static_cast<const T*>(v), static_cast<uint8_t*>(k_codes), static_cast<uint8_t*>(k_scales),
                            static_cast<uint8_t*>(v_codes), static_cast<uint8_t*>(v_scales));
         return hipGetLastError();
@@ -904,13 +992,14 @@ hipError_t launch_attn_read_mx4(int dtype, int N, int total, int Hkv, int d, int
                                 const void* k_codes, const void* k_scales, const void* v_codes, const void* v_scales,
                                 const int* table, const int* cu, const int* first, void* k, void* v, hipStream_t st) {
     unsigned long long waves;
-    const attn::MxPlace pl = attn::place_of(N, total, Hkv, page_size, num_pages, max_pages, cu, first, table, waves);
+    int groups;
+    const attn::MxPlace pl = attn::place_of(N, total, Hkv, page_size, num_pages, max_pages, cu, first, table, d, groups, waves);
     const unsigned long long blocks = (waves + 3) / 4;
     if (!grid_fits(blocks, 256)) return hipErrorInvalidConfiguration;
     auto go = [&](auto t, auto dd) {
         using T = decltype(t);
         hipLaunchKernelGGL((attn::mx4_read_kernel<T, decltype(dd)::value>), dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
-                           st, pl, attn::FastDiv(Hkv), static_cast<int>(waves), static_cast<const uint8_t*>(k_codes),
+                           st, pl, attn::FastDiv(groups), static_cast<int>(waves), static_cast<const uint8_t*>(k_codes),
                            static_cast<const uint8_t*>(k_scales), static_cast<const uint8_t*>(v_codes),
                            static_cast<const uint8_t*>(v_scales), static_cast<T*>(k), static_cast<T*>(v));
         return hipGetLastError();
