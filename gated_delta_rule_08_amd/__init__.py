@@ -753,39 +753,40 @@ def gdr_attn_append(k, v, cu_seqlens, lengths, k_pages, v_pages, page_table, str
 # ---- around the attention layers: norm and rotation, page plan, 4-bit cache
 
 
-def _token_stride(name, t, tokens: int, H: int, d: int) -> int:
+def _token_stride(name, t, H: int, d: int) -> int:
     """Elements from token to token of t [..., H, d], whose heads are dense and whose tokens are evenly apart."""
-    size, step = t.shape, t.stride()
-    if t.is_contiguous() or t.numel() == 0:
+    if t.is_contiguous():
         return H * d
+    size, step = t.shape, t.stride()
     if step[-1] != 1 or (H > 1 and step[-2] != d):
         raise ValueError("%s: the heads of a token must be dense" % name)
     apart = None  # of the innermost token axis that has one
     expect = 0
-    for n, s in zip(reversed(size[:-2]), reversed(step[:-2])):
-        if n == 1:
-            continue
-        if apart is None:
-            apart = s
-        elif s != expect:
-            raise ValueError("%s: the tokens must be evenly apart" % name)
-        expect = s * n
+    for i in range(len(size) - 3, -1, -1):
+        n = size[i]
+        if n != 1:
+            if apart is None:
+                apart = step[i]
+            elif step[i] != expect:
+                raise ValueError("%s: the tokens must be evenly apart" % name)
+            expect = step[i] * n
     return H * d if apart is None else apart
 
 
 def _rope_rows(q, k, positions, inv_freq):
     """(tokens, Hq, Hkv, d, rot) of a norm and rotation."""
-    if q.dim() < 2 or q.dim() != k.dim():
+    qs, ks = q.shape, k.shape
+    if len(qs) < 2 or len(qs) != len(ks):
         raise ValueError("q must be [...,Hq,d], k [...,Hkv,d]")
-    lead, (Hq, d) = q.shape[:-2], q.shape[-2:]
-    if k.shape[:-2] != lead or k.shape[-1] != d:
+    lead, d = qs[:-2], qs[-1]
+    if ks[:-2] != lead or ks[-1] != d:
         raise ValueError("q and k must agree in their tokens and channels")
     if inv_freq.dim() != 1 or inv_freq.dtype != torch.float32:
         raise ValueError("inv_freq must be fp32 [rot / 2]")
     rot = 2 * inv_freq.shape[0]
     if rot:
         _int32("positions", positions, lead)
-    return math.prod(lead), Hq, k.shape[-2], d, rot
+    return math.prod(lead), qs[-2], ks[-2], d, rot
 
 
 def _on_device(dev, *ts) -> None:
@@ -820,7 +821,7 @@ def gdr_attn_norm_rope(q, k, positions, inv_freq, q_out, k_out, w_q=None, w_k=No
     _rope_weights(d, w_q, w_k)
     dev = _attn_device(q_out, k_out, w_q, w_k, inv_freq, positions if rot else None)
     _on_device(dev, q, k)
-    sq, sk = _token_stride("q", q, tokens, Hq, d), _token_stride("k", k, tokens, Hkv, d)
+    sq, sk = _token_stride("q", q, Hq, d), _token_stride("k", k, Hkv, d)
     _attn_launch(dev, stream, load_library().gdr_attn_norm_rope, code, (1 if interleaved else 0) | (0 if norm else 2), _attn_int(tokens),
                  Hq, Hkv, d, rot, eps, sq, sk, q.data_ptr(), k.data_ptr(), None if w_q is None else w_q.data_ptr(),
                  None if w_k is None else w_k.data_ptr(), positions.data_ptr() if rot else None,
@@ -849,8 +850,8 @@ def gdr_attn_norm_rope_backward(q, k, positions, inv_freq, grad_q_out, grad_k_ou
     _rope_weights(d, w_q, w_k, grad_w_q, grad_w_k)
     dev = _attn_device(grad_q_out, grad_k_out, w_q, w_k, grad_w_q, grad_w_k, inv_freq, positions if rot else None, workspace)
     _on_device(dev, q, k, grad_q, grad_k)
-    strides = [_token_stride(n, t, tokens, H, d) for n, t, H in (
-        ("q", q, Hq), ("k", k, Hkv), ("grad_q", grad_q, Hq), ("grad_k", grad_k, Hkv))]
+    strides = (_token_stride("q", q, Hq, d), _token_stride("k", k, Hkv, d), _token_stride("grad_q", grad_q, Hq, d),
+               _token_stride("grad_k", grad_k, Hkv, d))
     weights = grad_w_q is not None or grad_w_k is not None
     need = 0 if workspace is not None or not weights else gdr_attn_norm_rope_backward_workspace_bytes(q.dtype, tokens, Hq, Hkv, d)
     ws, ws_bytes, workspace = _attn_workspace(workspace, need, dev, stream)

@@ -212,12 +212,12 @@ def test_token_strides():
     """Views whose tokens are evenly apart pass their stride; others are refused."""
     s = gdr._token_stride
     qkv = torch.zeros(3, 5, 8, 64)
-    assert s("q", qkv[:, :, :4], 15, 4, 64) == 512
-    assert s("q", qkv[:, :, 4:6], 15, 2, 64) == 512
-    assert s("q", qkv, 15, 8, 64) == 512
-    assert s("q", qkv[:, :1, :4], 3, 4, 64) == 5 * 512  # one token of each sequence
-    assert s("q", qkv[1:2, 2:3, :4], 1, 4, 64) == 256
-    assert s("q", torch.zeros(0, 4, 64), 0, 4, 64) == 256
+    assert s("q", qkv[:, :, :4], 4, 64) == 512
+    assert s("q", qkv[:, :, 4:6], 2, 64) == 512
+    assert s("q", qkv, 8, 64) == 512
+    assert s("q", qkv[:, :1, :4], 4, 64) == 5 * 512  # one token of each sequence
+    assert s("q", qkv[1:2, 2:3, :4], 4, 64) == 256
+    assert s("q", torch.zeros(0, 4, 64), 4, 64) == 256
     for bad in (qkv[:, :4, :4], qkv[:, ::2, :4], qkv.transpose(1, 2)[:, :4], qkv[..., ::2], qkv[:, :, ::2], qkv.transpose(0, 1)):
         with pytest.raises(ValueError):
-            s("q", bad, 1, bad.shape[-2], bad.shape[-1])
+            s("q", bad, bad.shape[-2], bad.shape[-1])
