@@ -7,8 +7,8 @@
 // writes the units it holds whole, and leaves (m, l, O) of the at most two it
 // shares with others to join_kernel, which joins them in order.
 //
-// A describes the step: B sequences, `shares` workgroups (0: one per unit and no
-// join), `heads` rows of a part, and
+// A describes the step: B sequences, `shares` workgroups (0: units that are not
+// shared, and no join), `heads` rows of a part, and
 //   int per()                    units of a sequence
 //   int blocks(int len)          blocks of a unit, 0 where the sequence is skipped by its length
 //   bool skipped(b, len, table)  skipped for another reason (its blocks count all the same)
@@ -25,10 +25,9 @@ struct JoinRow {
 };
 
 // The blocks of the batch in a row: sequence by sequence, within one unit by
-// unit, per() units each.  A wave sums them 256
-// sequences at a time, four to a lane, so that their lengths come together.
-// The sums are formed in registers (shifts inside 16 lanes, then the sums of the
-// 16 and 32 lanes before).
+// unit, per() units each.  A wave sums them 256 sequences at a time, four to a
+// lane, so that their lengths come together.  The sums are formed in registers
+// (shifts inside 16 lanes, then the sums of the 16 and 32 lanes before).
 __device__ __forceinline__ int scan64(int x) {  // inclusive
     x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false);
     x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false);
@@ -93,7 +92,7 @@ __device__ __forceinline__ int owner(long long g, long long n, int W) {
 struct Share {
     int b, len, unit, at_block, left;
 };
-// The share of workgroup `bid`; false: it has none.
+// The share of workgroup `bid` (shares == 0: the unit `bid`); false: it has none.
 template <typename A>
 __device__ __forceinline__ bool find_share(const A& a, const int* __restrict__ lengths, int lane, int bid, Share& s) {
     const int per = a.per();
@@ -221,13 +220,12 @@ __global__ __launch_bounds__(256) void join_kernel(A a, int rows, const int* __r
 // Parts in the workspace: O of every share's two slots, then (m, l).
 template <typename A> size_t part_floats(const A& a, int d) { return static_cast<size_t>(a.shares) * 2 * a.heads * (d + 2); }
 
-// The launch of `step` (a decode kernel) and of the join behind it.  `rows` output rows; `most`
-// blocks that a unit can have at most.
+// The launch of `step` (a decode kernel of `blocks` workgroups) and of the join behind it.
+// `rows` output rows; `most` blocks that a unit can have at most.
 template <typename T, int D, typename A, typename F>
-hipError_t launch_dealt(const A& a, unsigned long long rows, unsigned long long most, int threads, const int* table,
-                        const int* lengths, void* o, float* ws, hipStream_t st, F step) {
+hipError_t launch_dealt(const A& a, unsigned long long blocks, unsigned long long rows, unsigned long long most, int threads,
+                        const int* table, const int* lengths, void* o, float* ws, hipStream_t st, F step) {
     const unsigned long long units = static_cast<unsigned long long>(a.B) * a.per();
-    const unsigned long long blocks = a.shares ? a.shares : units;
     // a share's blocks have to fit an int, and so have those of one scan's sequences
     if (a.shares && (units * most / a.shares > 0x7fffffffull || (a.B < 256 ? a.B : 256) * most > 0x7fffffffull))
         return hipErrorInvalidConfiguration;

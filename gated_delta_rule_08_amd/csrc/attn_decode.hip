@@ -398,7 +398,8 @@ hipError_t launch_decode_t(const DecodeArgs& a, const void* q, const void* k, co
     using C = DecodeCfg<T, D>;
     auto* f = decode_kernel<T, D>;
     const unsigned long long most = (static_cast<unsigned long long>(a.max_pages) << a.page_shift) / kBlock + 1;
-    return launch_dealt<T, D>(a, static_cast<unsigned long long>(a.B) * a.Hq, most, 64 * kWaves, table, lengths, o, ws, st,
+    const unsigned long long blocks = a.shares ? a.shares : static_cast<unsigned long long>(a.B) * a.per();
+    return launch_dealt<T, D>(a, blocks, static_cast<unsigned long long>(a.B) * a.Hq, most, 64 * kWaves, table, lengths, o, ws, st,
                               [&](unsigned blocks, float* part_o, float* part_ml) {
                                   if (C::kLds > 64 * 1024) {
                                       const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(f),

@@ -36,7 +36,8 @@ struct Mx4Args {
     int page_shift, num_pages, max_pages;
     int window, sinks;
     float scale;
-    int shares;  // workgroups the blocks are dealt to; 0: one workgroup per unit
+    int shares;  // workgroups the blocks are dealt to; 0: units that are not shared
+    bool alone;  // a wave for each unit, else a workgroup (shares == 0)
     int heads;   // rows of a unit: min(16, Tq * G)
     FastDiv by_group, by_tiles;  // by G and by head_tiles
 
@@ -176,6 +177,9 @@ template <typename F> __device__ __forceinline__ float over_blocks(float v, F f)
 // after the power of two, which is the same as before it.  fp32: queries and
 // weights go in as three bf16 pieces, 24 bits, and no bit of the codes is lost.
 //
+// A unit's steps go to the four waves of a workgroup in turn, joined in LDS, or all
+// to one wave (see mx4_args).
+//
 // Bound by HBM and, at half its time, by the vector ALUs.  Everything that is read
 // goes through LDS, straight from memory in whole lines: fetched into the registers
 // of the lanes that need it, each line of the keys and scales is asked for by
@@ -183,7 +187,7 @@ template <typename F> __device__ __forceinline__ float over_blocks(float v, F f)
 // sequences of 16 .. 8000 tokens, 280 MB: 89 us with the loads a step ahead in
 // registers).  Keys are refilled as soon as the scores are formed, values as soon as
 // they are summed, no barrier until the end.
-template <typename T, int D, int X>
+template <typename T, int D, int X, bool kAlone>
 __global__ __launch_bounds__(64 * kMxWaves, 2) void mx4_decode_kernel(
     Mx4Args a, const T* __restrict__ q, const uint8_t* __restrict__ k_codes, const uint8_t* __restrict__ k_scales,
     const uint8_t* __restrict__ v_codes, const uint8_t* __restrict__ v_scales, const int* __restrict__ table,
@@ -209,8 +213,11 @@ __global__ __launch_bounds__(64 * kMxWaves, 2) void mx4_decode_kernel(
     // and the unit it copies, from the start of 1024 bytes of keys: even and odd blocks
     const uint32_t unit = 16 * lane, swapped = 16 * (lane ^ 1);
 
+    constexpr int kStride = kAlone ? 1 : kMxWaves;
+    const int id = kAlone ? blockIdx.x * kMxWaves + wave : blockIdx.x;
+    if (kAlone && id >= a.B * per) return;
     Share share;
-    if (!find_share(a, lengths, lane, blockIdx.x, share)) return;
+    if (!find_share(a, lengths, lane, id, share)) return;
     int b = share.b, unit_at = share.unit, at_block = share.at_block, left = share.left;
     MxSpan sp = mx_span(a, share.len);
 
@@ -278,7 +285,7 @@ __global__ __launch_bounds__(64 * kMxWaves, 2) void mx4_decode_kernel(
 
         // The query and the pages of two steps come together, then the first copies.
         const int end = max(0, at_block + take - kUnitCost);
-        int step = max(0, at_block - kUnitCost) + wave, row[4], page[4], next[4];
+        int step = max(0, at_block - kUnitCost) + (kAlone ? 0 : wave), row[4], page[4], next[4];
         bf16x8v qf[X][KS][NP];  // copy by copy: the others' columns are zero
         {
             const T* qp = q + orow * D + (D / 4) * h4;
@@ -289,7 +296,7 @@ __global__ __launch_bounds__(64 * kMxWaves, 2) void mx4_decode_kernel(
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 page[x] = page_of(4 * step + x);
-                next[x] = page_of(4 * (step + kMxWaves) + x);
+                next[x] = page_of(4 * (step + kStride) + x);
             }
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
@@ -321,8 +328,8 @@ __global__ __launch_bounds__(64 * kMxWaves, 2) void mx4_decode_kernel(
         float m = -INFINITY, l = 0.f;
 
 #pragma unroll 1
-        for (; step < end; step += kMxWaves) {
-            const bool more = step + kMxWaves < end;
+        for (; step < end; step += kStride) {
+            const bool more = step + kStride < end;
             int shown = 0;  // blocks that exist
 #pragma unroll
             for (int x = 0; x < 4; ++x) shown |= (row[x] >= 0) << x;
@@ -383,9 +390,9 @@ __global__ __launch_bounds__(64 * kMxWaves, 2) void mx4_decode_kernel(
             }
             if (more) {
 #pragma unroll
-                for (int x = 0; x < 4; ++x) row[x] = row_of(4 * (step + kMxWaves) + x, page[x]);
+                for (int x = 0; x < 4; ++x) row[x] = row_of(4 * (step + kStride) + x, page[x]);
 #pragma unroll
-                for (int x = 0; x < 4; ++x) page[x] = page_of(4 * (step + 2 * kMxWaves) + x);
+                for (int x = 0; x < 4; ++x) page[x] = page_of(4 * (step + 2 * kStride) + x);
                 mx4_wait_lds();
                 copy_keys(row);
             }
@@ -484,6 +491,16 @@ __global__ __launch_bounds__(64 * kMxWaves, 2) void mx4_decode_kernel(
         for (int t = 0; t < DT; ++t)
 #pragma unroll
             for (int r = 0; r < 4; ++r) acc[t][r] = over_copies<X>(acc[t][r], plus);
+
+        if constexpr (kAlone) {  // the wave's only unit
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            if (c16 < rows) {  // one of the copies, which are alike now
+#pragma unroll
+                for (int t = 0; t < DT; ++t)
+                    store4<T>(o + orow * D + 16 * t + 4 * h4, acc[t][0] * inv, acc[t][1] * inv, acc[t][2] * inv, acc[t][3] * inv);
+            }
+            return;
+        }
 
         // the four waves' parts, joined in LDS in wave order
         __syncthreads();
@@ -889,11 +906,12 @@ MxPlace place_of(int N, int total, int Hkv, int page_size, int num_pages, int ma
     return pl;
 }
 
-int mx4_shares(int page_size, int max_pages, int window, int sinks, int Tq) {
-    long long keys = static_cast<long long>(max_pages) * page_size;
-    if (window && keys > static_cast<long long>(window) + Tq + sinks) keys = static_cast<long long>(window) + Tq + sinks;
-    return keys <= 512 ? 0 : 512;
+// The most keys that a sequence of the batch can have in sight.
+long long mx4_keys(int page_size, int max_pages, int window, int sinks, int Tq) {
+    const long long keys = static_cast<long long>(max_pages) * page_size, seen = static_cast<long long>(window) + Tq + sinks;
+    return window && keys > seen ? seen : keys;
 }
+constexpr int kMxShares = 512;  // two workgroups to a CU
 
 Mx4Args mx4_args(int B, int Tq, int Hq, int Hkv, int page_size, int num_pages, int max_pages, int window, int sinks,
                  float scale) {
@@ -910,7 +928,25 @@ Mx4Args mx4_args(int B, int Tq, int Hq, int Hkv, int page_size, int num_pages, i
     a.window = window;
     a.sinks = sinks;
     a.scale = scale;
-    a.shares = mx4_shares(page_size, max_pages, window, sinks, Tq);
+    // A dealt batch pays for its join and for the shares' search, a unit of its own for
+    // the longest sequence's steps one after another.  Measured with 32 heads over 8 and
+    // over 32, graph times in us:
+    //  units  keys   a wave  a workgroup  dealt
+    //     64   500     14.1      7.4
+    //    512   500     14.8     11.3
+    //   1024   500     17.1     20.5
+    //   2048   100     11.8     26.2
+    //   2048  1000     50.3     56.2      63.6
+    //   1024  2000     50.0     52.6      54.1   (16 .. 2000: 42.6, 38.6, 45.4)
+    //      8  1000     22.0      9.0      11.3
+    //      8  2000     40.2     14.6      11.7
+    //    256  4000     76.2     28.9      37.0   (16 .. 4000: 75.1, 24.8, 27.3)
+    //    256  5000     94.3     35.2      41.3   (16 .. 5000: 29.5 against 27.9, one alone 27.9 against 16.8)
+    //     64  4000     75.6     24.0      18.9
+    const long long keys = mx4_keys(page_size, max_pages, window, sinks, Tq), units = static_cast<long long>(B) * a.per();
+    const long long own = 16 * units < 1024 ? 1024 : 16 * units < 4096 ? 16 * units : 4096;
+    a.alone = keys <= (units >= 1024 ? 1024 : kQuad);
+    a.shares = a.alone || keys <= own ? 0 : kMxShares;
     a.heads = Tq * a.G < 16 ? Tq * a.G : 16;
     a.by_group = FastDiv(a.G);
     a.by_tiles = FastDiv(a.head_tiles);
@@ -923,9 +959,11 @@ hipError_t launch_mx4_decode_t(const Mx4Args& a, const void* q, const void* k_co
                                float* ws, hipStream_t st) {
     const unsigned long long rows = static_cast<unsigned long long>(a.B) * a.Tq * a.Hq;
     const unsigned long long most = (static_cast<unsigned long long>(a.max_pages) << a.page_shift) / kQuad + 2 + kUnitCost;
-    return launch_dealt<T, D>(a, rows, most, 64 * kMxWaves, table, lengths, o, ws, st,
+    const unsigned long long units = static_cast<unsigned long long>(a.B) * a.per();
+    const unsigned long long blocks = a.shares ? a.shares : a.alone ? (units + kMxWaves - 1) / kMxWaves : units;
+    return launch_dealt<T, D>(a, blocks, rows, most, 64 * kMxWaves, table, lengths, o, ws, st,
                               [&](unsigned blocks, float* part_o, float* part_ml) {
-                                  auto* f = mx4_decode_kernel<T, D, X>;
+                                  auto* f = a.alone ? mx4_decode_kernel<T, D, X, true> : mx4_decode_kernel<T, D, X, false>;
                                   constexpr int lds = Mx4Lds<D>::kBytes;
                                   if (lds > 64 * 1024) {
                                       const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(f),
@@ -946,7 +984,10 @@ hipError_t launch_mx4_decode_t(const Mx4Args& a, const void* q, const void* k_co
 }  // namespace attn
 
 size_t attn_decode_mx4_workspace_floats(int Tq, int Hq, int Hkv, int d, int page_size, int max_pages, int window, int sinks) {
-    return attn::part_floats(attn::mx4_args(1, Tq, Hq, Hkv, page_size, 0, max_pages, window, sinks, 1.f), d);
+    // by the keys alone: which batches are dealt out is free to change
+    attn::Mx4Args a = attn::mx4_args(1, Tq, Hq, Hkv, page_size, 0, max_pages, window, sinks, 1.f);
+    a.shares = attn::mx4_keys(page_size, max_pages, window, sinks, Tq) <= 512 ? 0 : attn::kMxShares;
+    return attn::part_floats(a, d);
 }
 
 hipError_t launch_attn_decode_mx4(int dtype, int B, int Tq, int Hq, int Hkv, int d, int page_size, int num_pages,

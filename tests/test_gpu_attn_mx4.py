@@ -243,6 +243,28 @@ def test_decode_long_tables(dt, Tq, Hq, Hkv, d, page, window, sinks):
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("Tq,Hq,Hkv,d,page,window,sinks", [
+    (1, 1, 1, 128, 64, 0, 0), (1, 8, 2, 64, 32, 0, 0), (1, 14, 2, 128, 32, 4100, 33), (2, 20, 1, 64, 128, 0, 0),
+])
+def test_decode_dealt(dt, Tq, Hq, Hkv, d, page, window, sinks):
+    """Tables with room for more keys than a unit takes by itself however many units there are."""
+    announce("mx4 decode dealt %s %s" % (dt, (Tq, Hq, Hkv, d, page, window, sinks)))
+    run_decode(dt, [0, 1, 127, 128, 4999, 129, 513, 1, 2500], Tq, Hq, Hkv, d, page, window, sinks)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("B,Tq,Hq,Hkv,d,page,window,sinks,longest", [
+    (147, 1, 7, 7, 128, 32, 0, 0, 300), (129, 1, 16, 8, 64, 32, 0, 0, 1024), (65, 3, 16, 16, 128, 64, 0, 0, 700),
+    (131, 1, 16, 8, 64, 32, 500, 3, 1500),
+])
+def test_decode_many_short(dt, B, Tq, Hq, Hkv, d, page, window, sinks, longest):
+    """A wave for each of many short units, the last workgroup not full."""
+    announce("mx4 decode many short %s %s" % (dt, (B, Tq, Hq, Hkv, d, page, window, sinks, longest)))
+    edges = [0, 1, 31, 32, 33, 127, 128, 129, longest]
+    run_decode(dt, edges + [1 + 37 * b % 200 for b in range(B - len(edges))], Tq, Hq, Hkv, d, page, window, sinks)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
 @pytest.mark.parametrize("scale", [0.0, -0.3, 2.0])
 def test_decode_scales(dt, scale):
     announce("mx4 decode scale %s %s" % (dt, scale))
