@@ -20,12 +20,12 @@ namespace attn {
 
 constexpr int kMxBlock = 32;   // channels of a block
 constexpr int kMxRows = 32;    // positions of a value block (16 bytes of one channel)
-constexpr uint32_t kMxNan = 255;
+constexpr uint32_t kMxMost = 252, kMxNan = 255;  // the largest scale byte, and that of NaN
 
 // The scale byte of a block from the bits of its largest magnitude.
 __device__ __forceinline__ uint32_t mx_scale(uint32_t top) {
     const int e = static_cast<int>((top + 0x1fffffu) >> 23) - 2;  // one more above a mantissa of 7/4
-    return top >= 0x7f800000u ? kMxNan : static_cast<uint32_t>(min(max(e, 1), 252));
+    return top >= 0x7f800000u ? kMxNan : static_cast<uint32_t>(min(max(e, 1), static_cast<int>(kMxMost)));
 }
 // What the values are multiplied by before the conversion; 0 for NaN blocks, whose codes are cleared anyway.
 __device__ __forceinline__ float mx_inverse(uint32_t b) { return b == kMxNan ? 0.f : __uint_as_float((254u - b) << 23); }

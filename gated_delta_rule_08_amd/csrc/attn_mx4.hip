@@ -335,8 +335,10 @@ __global__ __launch_bounds__(64 * kMxWaves, 2) void mx4_decode_kernel(
             for (int x = 0; x < 4; ++x) shown |= (row[x] >= 0) << x;
             mx4_wait<kCopies>();  // the keys; the values may still come
             // The byte 255 gives an infinite scale, which no code but 0 comes with: the scores are
-            // NaN.  Where tiles share an accumulator such a key would reach the other copies'
-            // scores too: it goes in as a finite one, and its own score is set afterwards.
+            // NaN.  253 and 254, which nothing but an unwritten slot holds, times a code leave the
+            // range of bf16.  Where tiles share an accumulator such a key would reach the other
+            // copies' scores too, as infinity times their zeros: it goes in with a finite scale,
+            // and its own score is set afterwards, to NaN unless the position is hidden.
             uint32_t kb[8];
 #pragma unroll
             for (int t = 0; t < 8; ++t) kb[t] = ksp[t * 4 * CB];
@@ -345,11 +347,11 @@ __global__ __launch_bounds__(64 * kMxWaves, 2) void mx4_decode_kernel(
                 uint32_t top = 0;
 #pragma unroll
                 for (int t = 0; t < 8; ++t) top = max(top, kb[t]);
-                odd = __any(top == kMxNan);
+                odd = __any(top > kMxMost);
                 if (odd) {
 #pragma unroll
                     for (int t = 0; t < 8; ++t)
-                        if (kb[t] == kMxNan) kb[t] = 1;
+                        if (kb[t] > kMxMost) kb[t] = 1;
                 }
             }
             f32x4 s[8 / X];
@@ -384,7 +386,7 @@ __global__ __launch_bounds__(64 * kMxWaves, 2) void mx4_decode_kernel(
                 for (int j = 0; j < kMine; ++j) {
                     bool nan = false;
 #pragma unroll
-                    for (int cb = 0; cb < CB; ++cb) nan |= own[j * CB + cb] == kMxNan;
+                    for (int cb = 0; cb < CB; ++cb) nan |= own[j * CB + cb] > kMxMost;
                     if (nan) s[j >> 2][j & 3] = NAN;
                 }
             }

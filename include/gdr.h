@@ -626,7 +626,7 @@ int gdr_attn_plan_pages(int N, int page_size, int max_pages, int n_stack, int ma
  * (0 .. 7), standing for code * 2^(b - 127).  The append takes the least scale
  * with max |x| <= 7 * 2^(b - 127), b within 1 .. 252, and the nearest code, ties to
  * the even one (6 from there on).  A block that holds an infinity or NaN stands for
- * NaN: b = 255 with codes 0.
+ * NaN: b = 255 with codes 0.  No append writes 0, 253 or 254.
  *
  *   k_codes   [num_pages, Hkv, page_size, d / 2]       uint8: the even channel in the low half
  *   v_codes   [num_pages, Hkv, page_size / 32, d, 16]  uint8: a channel's 32 positions, the

@@ -340,6 +340,28 @@ def test_decode_non_finite(dt, n):
               torch.where(keep, bound, torch.zeros(()).double()))
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("byte", [0, 252, 253, 254, 255])
+@pytest.mark.parametrize("code", [0, 7, 15])
+def test_decode_hidden_bytes_have_no_influence(dt, byte, code):
+    """Whatever lies in the slots behind a sequence, in scales that no append writes too (253 and 254 times a code
+    leave the range of bf16), the output is that of a cleared cache, bit by bit."""
+    announce("mx4 decode hidden bytes %s %d %d" % (dt, byte, code))
+    lengths = [1, 5, 33, 70, 130]
+    for Hq, Hkv, d in ((4, 2, 128), (8, 1, 64), (16, 1, 128)):  # 4, 2 and 1 copies of the rows
+        c = Mx4Cache(lengths, [0] * 5, Hkv, d, 64)
+        outs = []
+        for scale, fill in ((byte, code), (1, 0)):
+            c.ks.fill_(scale), c.vs.fill_(scale), c.kc.fill_(fill), c.vc.fill_(fill)
+            for b, n in enumerate(lengths):
+                c.put(b, 0, make(10 + b, dt, n, Hkv, d), make(50 + b, dt, n, Hkv, d))
+            q = make(1, dt, 5, 1, Hq, d).cuda()
+            outs.append(torch.full_like(q, 7.0))
+            gdr.gdr_attn_decode_mx4(q, *c.device(), ints(lengths), outs[-1])
+            torch.cuda.synchronize()
+        assert torch.isfinite(outs[1]).all() and torch.equal(outs[0], outs[1])
+
+
 def test_decode_a_nan_far_below_the_maximum_is_seen():
     """A NaN value whose weight underflows, in another wave's or another workgroup's part."""
     announce("mx4 decode underflow")
