@@ -1,6 +1,8 @@
 // C ABI of the operators around the attention layers: norm and rotation of queries
 // and keys, the page plan, and the 4-bit cache.  Argument validation and dispatch;
 // every check runs before the first HIP call.
+#include <initializer_list>
+
 #include "attn_checks.h"
 
 using namespace gdr::attn;
@@ -22,6 +24,13 @@ int stride_checks(int dtype, int tokens, int H, int d, long long stride) {
     if (H == 0 || tokens == 0) return GDR_OK;
     if (stride < static_cast<long long>(H) * d || stride > (1LL << 40) / tokens) return GDR_ERR_BAD_SHAPE;
     return stride % (dtype == GDR_DTYPE_F32 ? 4 : 8) ? GDR_ERR_MISALIGNED : GDR_OK;
+}
+
+// Whether a tensor that is written (and exists) is another of the call's.
+bool any_of(const void* out, std::initializer_list<const void*> others) {
+    for (const void* p : others)
+        if (out && out == p) return true;
+    return false;
 }
 
 // An output may be its input if it lies the same way.
@@ -61,6 +70,7 @@ int gdr_attn_norm_rope(int dtype, int flags, int tokens, int Hq, int Hkv, int d,
     if ((Hq && !same_way(q, q_out, q_stride, static_cast<long long>(Hq) * d)) ||
         (Hkv && !same_way(k, k_out, k_stride, static_cast<long long>(Hkv) * d)))
         return GDR_ERR_ALIAS;
+    if (Hq && Hkv && (any_of(q_out, {k, k_out}) || any_of(k_out, {q}))) return GDR_ERR_ALIAS;
     return status_of(gdr::launch_attn_rope(dtype, tokens, Hq, Hkv, d, rot, flags & GDR_ROPE_INTERLEAVED,
                                            !(flags & GDR_ROPE_NO_NORM), eps, q_stride, k_stride, q, k, w_q, w_k, positions,
                                            inv_freq, q_out, k_out, static_cast<hipStream_t>(stream)));
@@ -103,6 +113,11 @@ int gdr_attn_norm_rope_backward(int dtype, int flags, int tokens, int Hq, int Hk
     if (!none && ((Hq && !same_way(grad_q_out, grad_q, static_cast<long long>(Hq) * d, grad_q_stride)) ||
                   (Hkv && !same_way(grad_k_out, grad_k, static_cast<long long>(Hkv) * d, grad_k_stride))))
         return GDR_ERR_ALIAS;
+    const void *q_read = norm ? q : nullptr, *k_read = norm ? k : nullptr;
+    if (any_of(grad_w_q, {grad_w_k}) ||
+        (!none && ((Hq && any_of(grad_q, {q_read})) || (Hkv && any_of(grad_k, {k_read})) ||
+                   (Hq && Hkv && (any_of(grad_q, {k_read, grad_k_out, grad_k}) || any_of(grad_k, {q_read, grad_q_out}))))))
+        return GDR_ERR_ALIAS;
     return status_of(gdr::launch_attn_rope_backward(dtype, none ? 0 : tokens, Hq, Hkv, d, rot, flags & GDR_ROPE_INTERLEAVED, norm, eps,
                                                     q_stride, k_stride, grad_q_stride, grad_k_stride, q, k, w_q, w_k,
                                                     positions, inv_freq, grad_q_out, grad_k_out, grad_q, grad_k, grad_w_q,
@@ -122,6 +137,17 @@ int gdr_attn_plan_pages(int N, int page_size, int max_pages, int n_stack, int ma
     const void* all[] = {lengths, add, free_pages, n_free, page_table, cu_seqlens, added, lengths_out, slots, n_free_out};
     for (const void* p : all)
         if (!aligned(p, 4)) return GDR_ERR_MISALIGNED;
+    if (N) {
+        const void* outs[] = {page_table, cu_seqlens, added, lengths_out, slots, n_free_out};
+        const void* own[] = {nullptr, nullptr, add, lengths, nullptr, n_free};  // the input that each may be
+        const void* ins[] = {lengths, add, free_pages, n_free};
+        for (int i = 0; i < 6; ++i) {
+            for (int j = 0; j < i; ++j)
+                if (any_of(outs[i], {outs[j]})) return GDR_ERR_ALIAS;
+            for (const void* in : ins)
+                if (in != own[i] && any_of(outs[i], {in})) return GDR_ERR_ALIAS;
+        }
+    }
     return status_of(gdr::launch_attn_plan_pages(N, page_size, max_pages, n_stack, max_tokens, lengths, add, free_pages, n_free,
                                                  page_table, cu_seqlens, added, lengths_out, slots, n_free_out,
                                                  static_cast<hipStream_t>(stream)));
@@ -139,6 +165,7 @@ int gdr_attn_append_mx4(int dtype, int N, int total, int Hkv, int d, int page_si
     if (!aligned(k, 16) || !aligned(v, 16) || !cache_aligned(k_codes, k_scales, v_codes, v_scales) ||
         !aligned(cu_seqlens, 4) || !aligned(lengths, 4) || !aligned(page_table, 4))
         return GDR_ERR_MISALIGNED;
+    if (any_of(k_codes, {v_codes, k, v}) || any_of(v_codes, {k, v}) || any_of(k_scales, {v_scales})) return GDR_ERR_ALIAS;
     return status_of(gdr::launch_attn_append_mx4(dtype, N, total, Hkv, d, page_size, num_pages, max_pages, k, v, cu_seqlens,
                                                  lengths, k_codes, k_scales, v_codes, v_scales, page_table,
                                                  static_cast<hipStream_t>(stream)));
@@ -155,6 +182,7 @@ int gdr_attn_read_mx4(int dtype, int N, int total, int Hkv, int d, int page_size
     if (!aligned(k, 16) || !aligned(v, 16) || !cache_aligned(k_codes, k_scales, v_codes, v_scales) ||
         !aligned(cu_seqlens, 4) || !aligned(first, 4) || !aligned(page_table, 4))
         return GDR_ERR_MISALIGNED;
+    if (any_of(k, {v})) return GDR_ERR_ALIAS;
     return status_of(gdr::launch_attn_read_mx4(dtype, N, total, Hkv, d, page_size, num_pages, max_pages, k_codes, k_scales,
                                                v_codes, v_scales, page_table, cu_seqlens, first, k, v,
                                                static_cast<hipStream_t>(stream)));

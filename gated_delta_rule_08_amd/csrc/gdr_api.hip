@@ -166,7 +166,7 @@ const char* gdr_status_string(int status) {
         case GDR_ERR_WORKSPACE: return "GDR_ERR_WORKSPACE: workspace missing or too small";
         case GDR_ERR_BAD_ENUM: return "GDR_ERR_BAD_ENUM: unknown gate mode, dtype or flag";
         case GDR_ERR_HIP: return "GDR_ERR_HIP: the HIP runtime rejected a launch";
-        case GDR_ERR_ALIAS: return "GDR_ERR_ALIAS: two state buffers (partially) overlap";
+        case GDR_ERR_ALIAS: return "GDR_ERR_ALIAS: two buffers (partially) overlap";
         case GDR_ERR_SCRATCH:
             return "GDR_ERR_SCRATCH: one chunk of every head needs more than the 96 MiB fixed scratch of "
                    "gdr_chunk_prefill_noalloc";

@@ -72,7 +72,7 @@ enum {
     GDR_ERR_WORKSPACE = -5,   /* workspace missing or too small             */
     GDR_ERR_BAD_ENUM = -6,    /* gate, dtype or flags not known             */
     GDR_ERR_HIP = -7,         /* the HIP runtime rejected a launch          */
-    GDR_ERR_ALIAS = -8,       /* two state buffers (partially) overlap      */
+    GDR_ERR_ALIAS = -8,       /* two buffers (partially) overlap            */
     GDR_ERR_SCRATCH = -9      /* gdr_chunk_prefill_noalloc: the problem
                                  needs more than its fixed scratch          */
 };
@@ -557,8 +557,9 @@ enum { GDR_ROPE_INTERLEAVED = 1, GDR_ROPE_NO_NORM = 2 };
  *
  * rot is a multiple of 16 up to d.  The angle is formed in double, so a position
  * may be any int32.  Hq and Hkv are independent here, and either may be 0.  q_out
- * may be q, and k_out k, where these are dense (GDR_ERR_ALIAS otherwise).  tokens *
- * (Hq + Hkv) must stay below 2^29.  Returns a GDR_* status.
+ * may be q, and k_out k, where these are dense; an output may be no other tensor of
+ * the call (GDR_ERR_ALIAS).  tokens * (Hq + Hkv) must stay below 2^29.  Returns a
+ * GDR_* status.
  */
 int gdr_attn_norm_rope(int dtype, int flags, int tokens, int Hq, int Hkv, int d, int rot, float eps, long long q_stride,
                        long long k_stride, const void* q, const void* k, const float* w_q, const float* w_k,
@@ -576,7 +577,8 @@ int gdr_attn_norm_rope(int dtype, int flags, int tokens, int Hq, int Hkv, int d,
  *   workspace  at least gdr_attn_norm_rope_backward_workspace_bytes(...) bytes where
  *              grad_w_q or grad_w_k is wanted
  *
- * q and k are not read with GDR_ROPE_NO_NORM.  Without tokens or heads grad_w_q and
+ * An output may be no other tensor of the call (GDR_ERR_ALIAS).  q and k are not
+ * read with GDR_ROPE_NO_NORM.  Without tokens or heads grad_w_q and
  * grad_w_k are zeroed.  Returns a GDR_* status.
  */
 int gdr_attn_norm_rope_backward(int dtype, int flags, int tokens, int Hq, int Hkv, int d, int rot, float eps,
@@ -613,8 +615,9 @@ size_t gdr_attn_norm_rope_backward_workspace_bytes(int dtype, int tokens, int Hq
  *                 it was behind the last token
  *   n_free_out    [1] int32 out: pages left; may be n_free
  *
- * All device data, and nothing is read on the host.  page_size a power of two up to
- * 65536.  N == 0 writes cu_seqlens[0] and n_free_out.  Returns a GDR_* status.
+ * Other tensors of the call may not be one (GDR_ERR_ALIAS).  All device data, and
+ * nothing is read on the host.  page_size a power of two up to 65536.  N == 0 writes
+ * cu_seqlens[0] and n_free_out.  Returns a GDR_* status.
  */
 int gdr_attn_plan_pages(int N, int page_size, int max_pages, int n_stack, int max_tokens, const int* lengths, const int* add,
                         const int* free_pages, const int* n_free, int* page_table, int* cu_seqlens, int* added,

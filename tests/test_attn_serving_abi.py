@@ -86,6 +86,28 @@ def test_norm_rope_backward(lib):
     assert size(1, 1 << 20, 32, 8, 128) <= 1 << 20
 
 
+def test_outputs_that_are_other_tensors_are_refused(lib):
+    def rope(ptrs, Hq=2, Hkv=2, flags=0):
+        return lib.gdr_attn_norm_rope(1, flags, 8, Hq, Hkv, 64, 32, 1e-6, 128, 128, *ptrs, None)
+
+    def back(ptrs, Hq=2, Hkv=2, flags=0):
+        return lib.gdr_attn_norm_rope_backward(1, flags, 8, Hq, Hkv, 64, 32, 1e-6, 128, 128, 128, 128, *ptrs, P[12], 1 << 40, None)
+
+    for out, other in ((6, 1), (6, 7), (7, 0)):  # q_out: k, k_out; k_out: q
+        assert rope(swap(P[:8], out, P[other])) == ALIAS, (out, other)
+    # grad_q: q, k, grad_k_out, grad_k; grad_k: q, k, grad_q_out; grad_w_k: grad_w_q
+    for out, other in ((8, 0), (8, 1), (8, 7), (8, 9), (9, 0), (9, 1), (9, 6), (11, 10)):
+        assert back(swap(P[:12], out, P[other])) == ALIAS, (out, other)
+    for out, others in ((4, (0, 1, 2, 3, 5, 6, 7, 8, 9)), (5, (0, 1, 2, 3, 6, 7, 8, 9)), (6, (0, 2, 3, 7, 8, 9)),
+                        (7, (1, 2, 3, 8, 9)), (8, (0, 1, 2, 3, 9)), (9, (0, 1, 2))):
+        for other in others:
+            assert lib.gdr_attn_plan_pages(4, 16, 8, 9, 100, *swap(P[:10], out, P[other]), None) == ALIAS, (out, other)
+    append, read = cache_calls(lib)
+    assert read(ptrs=swap(P[:9], 8, P[7])) == ALIAS
+    for out, other in ((6, 4), (7, 5), (4, 0), (4, 1), (6, 0), (6, 1)):
+        assert append(ptrs=swap(P[:9], out, P[other])) == ALIAS, (out, other)
+
+
 def test_plan_pages(lib):
     def call(N=4, page=16, width=8, stack=9, tokens=100, ptrs=P[:10]):
         return lib.gdr_attn_plan_pages(N, page, width, stack, tokens, *ptrs, None)
