@@ -11,7 +11,7 @@
 // likewise; no registers hold them, and no barrier until the end.  The group's
 // query heads are the 16 columns of S^T = K Q^T, so a key read serves every head
 // of its group.  64 sequences of 16 .. 8000 tokens, 8 key heads, d=128 (1.05 GB):
-// 163 us and 6 for the join, 6.0 TB/s of the whole call; one of 32768: 24 + 5 us.
+// 162 us and 6 for the join, 6.1 TB/s of the whole call; one of 32768: 24 + 4 us.
 //
 // The visible keys of a sequence are a list (the sinks, then the window) in
 // blocks of 128, dealt out and joined as attn_deal.h has it.  Lengths of at

@@ -3,11 +3,10 @@
 //
 // The format of a block is attn_mx4.h's.  Keys lie row by row, a position's d / 2
 // bytes together; values lie in blocks of 32 positions, the 16 bytes of a channel
-// together, so that the operands of both products of the decode step come from
-// memory to the registers of the lanes that need them: a lane of the score product
-// wants consecutive channels of a key, a lane of the output product consecutive
-// positions of a channel.  No LDS, no transposition, and wide loads throughout.
-// Scales lie position by position.
+// together, so that both products of the decode step find their operands' bytes as
+// they want them: a lane of the score product takes consecutive channels of a key,
+// a lane of the output product consecutive positions of a channel.  The values are
+// transposed once, by the append.  Scales lie position by position.
 #include <type_traits>
 
 #include "attn_deal.h"
@@ -168,8 +167,8 @@ template <typename F> __device__ __forceinline__ float over_blocks(float v, F f)
 // takes positions 32 x / X .. of each block.  Of the keys' tiles each meets the query
 // in its own copy's columns only, zero in the others, so that X tiles share an
 // accumulator, and a lane has 32 / X positions; of the weights each product takes
-// one copy's, and the copies' sums are added at the end.  (X = 1: 960 vector
-// instructions a step, X = 4: 600.)
+// one copy's, and the copies' sums are added at the end.  (The code of a step, masks
+// among it: 1060 vector instructions with X = 1, 715 with X = 4.)
 //
 // The keys' scales are applied by the conversion to bf16, which is exact.  The
 // values' scales differ along the summed axis and are multiplied into the weights:
@@ -180,13 +179,15 @@ template <typename F> __device__ __forceinline__ float over_blocks(float v, F f)
 // A unit's steps go to the four waves of a workgroup in turn, joined in LDS, or all
 // to one wave (see mx4_args).
 //
-// Bound by HBM and, at half its time, by the vector ALUs.  Everything that is read
+// Bound by HBM: 64 sequences of 16 .. 8000 tokens, 32 heads over 8, d = 128 (280 MB)
+// 54 us and 5 for the join, 5.2 TB/s; one of 32768 14.7 + 4.3.  The vector ALUs are
+// busy for half of it, the matrix cores for an eighth.  Everything that is read
 // goes through LDS, straight from memory in whole lines: fetched into the registers
 // of the lanes that need it, each line of the keys and scales is asked for by
-// several of them while it is on its way, and the L1 cache stalls on that (64
-// sequences of 16 .. 8000 tokens, 280 MB: 89 us with the loads a step ahead in
-// registers).  Keys are refilled as soon as the scores are formed, values as soon as
-// they are summed, no barrier until the end.
+// several of them while it is on its way, and the L1 cache stalls on that (89 us
+// with the loads a step ahead in registers, where this took 63).  Keys are refilled
+// as soon as the scores are formed, values as soon as they are in registers, no
+// barrier until the end.
 template <typename T, int D, int X, bool kAlone>
 __global__ __launch_bounds__(64 * kMxWaves, 2) void mx4_decode_kernel(
     Mx4Args a, const T* __restrict__ q, const uint8_t* __restrict__ k_codes, const uint8_t* __restrict__ k_scales,
@@ -731,7 +732,7 @@ template <int D> struct MxLane {
 // in part keeps its other positions.  The values are loaded once the keys' registers
 // are free, which leaves room for four waves a SIMD (both at once: 142 registers
 // and 2 us more).  Bound by HBM: 8 prompts of 1000 .. 4096 tokens, 8 heads of 128,
-// 105 MB, 25 us; the read of the same and 100 tokens more each, 109 MB, 22 us.
+// 105 MB, 26 us; the read of the same and 100 tokens more each, 109 MB, 23 us.
 template <typename T, int D>
 __global__ __launch_bounds__(256) void mx4_append_kernel(MxPlace pl, FastDiv groups, int waves, const T* __restrict__ k,
                                                          const T* __restrict__ v, uint8_t* __restrict__ k_codes,

@@ -10,11 +10,11 @@
 //
 // Both passes move every row once each way and do little with it: HBM-bound (8192
 // tokens of 32 query and 8 key heads, d=128, bf16: forward 168 MB in 34 us, backward
-// 252 MB in 48 and 4 for the join).  A
-// lane has two groups of Q = 4 or 8 channels (8 or 16 bytes) that hold its pairs
-// whole, so a rotation needs no other lane, and a row takes d / 2Q lanes; the norm's
-// sum is two to four exchanges inside 16 lanes.  The angles' cosines and sines belong to a token and
-// are formed once for all its heads, in LDS.
+// 252 MB in 48 and 5 for the join).  A lane has two groups of Q = 4 or 8 channels (8
+// or 16 bytes) that hold its pairs whole, so a rotation needs no other lane, and a
+// row takes d / 2Q lanes; the norm's sum is two to four exchanges inside 16 lanes.
+// The angles' cosines and sines belong to a token and are formed once for all its
+// heads, in LDS.
 #include <type_traits>
 
 #include "attn_common.h"
