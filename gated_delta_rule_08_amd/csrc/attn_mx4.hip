@@ -900,11 +900,16 @@ int log2_of(int x) {
 MxPlace place_of(int N, int total, int Hkv, int page_size, int num_pages, int max_pages, const int* cu, const int* first,
                  const int* table, int d, int& groups, unsigned long long& waves) {
     // A wave goes through its runs one after another: a range holds about as many
-    // tokens as a run does.
+    // tokens as a run does, and fewer where that leaves the GPU with little to do.
+    // Append and read in us, with ranges of 32 and of 8: 5 prompts to 77 tokens, one
+    // group, 16.0 and 10.9; eight groups: 8 to 100 16.7, 13.5; 8 to 400 (1604 tokens)
+    // 20.3, 17.0; 8 to 1000 (4007) 22.5, 22.2; 32 to 300 (4831) 22.6, 24.0; one of 1000
+    // 13.4, 14.3.
     const int mean = total / N;
-    const int range = mean >= 32 ? 32 : mean >= 8 ? 8 : 2;
-    MxPlace pl{N, total, Hkv, log2_of(page_size), num_pages, max_pages, range, cu, first, table};
     groups = d == 64 ? (Hkv + 1) / 2 : Hkv;
+    const bool few = static_cast<long long>(total) * groups <= 16384;
+    const int range = mean >= 32 && !few ? 32 : mean >= 8 ? 8 : 2;
+    MxPlace pl{N, total, Hkv, log2_of(page_size), num_pages, max_pages, range, cu, first, table};
     waves = (static_cast<unsigned long long>(total) + range - 1) / range * groups;
     return pl;
 }
