@@ -30,6 +30,21 @@ __device__ __forceinline__ uint32_t mx_scale(uint32_t top) {
 // What the values are multiplied by before the conversion; 0 for NaN blocks, whose codes are cleared anyway.
 __device__ __forceinline__ float mx_inverse(uint32_t b) { return b == kMxNan ? 0.f : __uint_as_float((254u - b) << 23); }
 __device__ __forceinline__ float mx_float(uint32_t b) { return __uint_as_float(b << 23); }
+// Of byte n (a constant) of a word, in one instruction; the compiler takes two (64
+// sequences of 16 .. 4000 tokens, 16 query rows: 41.7 us against 43.5; fp32, 16 .. 8000:
+// 95 against 102).
+__device__ __forceinline__ float mx_float(uint32_t w, int n) {
+    uint32_t r;
+    if (n == 0)
+        asm("v_lshlrev_b32_sdwa %0, 23, %1 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:DWORD src1_sel:BYTE_0" : "=v"(r) : "v"(w));
+    else if (n == 1)
+        asm("v_lshlrev_b32_sdwa %0, 23, %1 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:DWORD src1_sel:BYTE_1" : "=v"(r) : "v"(w));
+    else if (n == 2)
+        asm("v_lshlrev_b32_sdwa %0, 23, %1 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:DWORD src1_sel:BYTE_2" : "=v"(r) : "v"(w));
+    else
+        asm("v_lshlrev_b32_sdwa %0, 23, %1 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:DWORD src1_sel:BYTE_3" : "=v"(r) : "v"(w));
+    return __uint_as_float(r);
+}
 
 __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 

@@ -168,7 +168,7 @@ template <typename F> __device__ __forceinline__ float over_blocks(float v, F f)
 // in its own copy's columns only, zero in the others, so that X tiles share an
 // accumulator, and a lane has 32 / X positions; of the weights each product takes
 // one copy's, and the copies' sums are added at the end.  (The code of a step, masks
-// among it: 1060 vector instructions with X = 1, 715 with X = 4.)
+// among it: 970 vector instructions with X = 1, 690 with X = 4.)
 //
 // The keys' scales are applied by the conversion to bf16, which is exact.  The
 // values' scales differ along the summed axis and are multiplied into the weights:
@@ -469,7 +469,7 @@ __global__ __launch_bounds__(64 * kMxWaves, 2) void mx4_decode_kernel(
 #pragma unroll
                     for (int y = 0; y < 8; ++y) {
                         const int byte = (8 * i + y) * CB + cb;
-                        f[y] = w[y] * mx_float((vs[byte >> 4][(byte >> 2) & 3] >> (8 * (byte & 3))) & 255u);
+                        f[y] = w[y] * mx_float(vs[byte >> 4][(byte >> 2) & 3], byte & 3);
                     }
                     bf16x8v pf[NP];
                     split8<NP>(f, pf);
