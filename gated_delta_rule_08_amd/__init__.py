@@ -751,6 +751,11 @@ def gdr_attn_append(k, v, cu_seqlens, lengths, k_pages, v_pages, page_table, str
 
 
 # ---- around the attention layers: norm and rotation, page plan, 4-bit cache
+#
+# Outputs that share memory with another tensor of the call (partly, too) are refused with
+# GDR_ERR_ALIAS, but for the input whose place an output may take.
+
+_APART = 1 << 24  # GDR_APART
 
 
 def _token_stride(name, t, H: int, d: int) -> int:
@@ -822,7 +827,7 @@ def gdr_attn_norm_rope(q, k, positions, inv_freq, q_out, k_out, w_q=None, w_k=No
     dev = _attn_device(q_out, k_out, w_q, w_k, inv_freq, positions if rot else None)
     _on_device(dev, q, k)
     sq, sk = _token_stride("q", q, Hq, d), _token_stride("k", k, Hkv, d)
-    _attn_launch(dev, stream, load_library().gdr_attn_norm_rope, code, (1 if interleaved else 0) | (0 if norm else 2), _attn_int(tokens),
+    _attn_launch(dev, stream, load_library().gdr_attn_norm_rope, code | _APART, (1 if interleaved else 0) | (0 if norm else 2), _attn_int(tokens),
                  Hq, Hkv, d, rot, eps, sq, sk, q.data_ptr(), k.data_ptr(), None if w_q is None else w_q.data_ptr(),
                  None if w_k is None else w_k.data_ptr(), positions.data_ptr() if rot else None,
                  inv_freq.data_ptr() if rot else None, q_out.data_ptr(), k_out.data_ptr())
@@ -855,7 +860,7 @@ def gdr_attn_norm_rope_backward(q, k, positions, inv_freq, grad_q_out, grad_k_ou
     weights = grad_w_q is not None or grad_w_k is not None
     need = 0 if workspace is not None or not weights else gdr_attn_norm_rope_backward_workspace_bytes(q.dtype, tokens, Hq, Hkv, d)
     ws, ws_bytes, workspace = _attn_workspace(workspace, need, dev, stream)
-    _attn_launch(dev, stream, load_library().gdr_attn_norm_rope_backward, code, (1 if interleaved else 0) | (0 if norm else 2),
+    _attn_launch(dev, stream, load_library().gdr_attn_norm_rope_backward, code | _APART, (1 if interleaved else 0) | (0 if norm else 2),
                  _attn_int(tokens), Hq, Hkv, d, rot, eps, *strides, q.data_ptr(), k.data_ptr(),
                  None if w_q is None else w_q.data_ptr(), None if w_k is None else w_k.data_ptr(),
                  positions.data_ptr() if rot else None, inv_freq.data_ptr() if rot else None, grad_q_out.data_ptr(),
@@ -891,7 +896,7 @@ def gdr_attn_plan_pages(lengths, add, free_pages, n_free, page_table, page_size:
         if max_tokens is None or max_tokens > slots.numel():
             max_tokens = slots.numel()
     dev = _attn_device(lengths, add, free_pages, n_free, page_table, cu_seqlens, added, lengths_out, n_free_out, slots)
-    _attn_launch(dev, stream, load_library().gdr_attn_plan_pages, N, _attn_int(page_size), max_pages, _attn_int(free_pages.numel()),
+    _attn_launch(dev, stream, load_library().gdr_attn_plan_pages, N, _attn_int(page_size) | _APART, max_pages, _attn_int(free_pages.numel()),
                  0x7fffffff if max_tokens is None else _attn_int(max_tokens), lengths.data_ptr(), add.data_ptr(),
                  free_pages.data_ptr(), n_free.data_ptr(), page_table.data_ptr(), cu_seqlens.data_ptr(), added.data_ptr(),
                  lengths_out.data_ptr(), None if slots is None else slots.data_ptr(), n_free_out.data_ptr())
@@ -936,7 +941,7 @@ def gdr_attn_append_mx4(k, v, cu_seqlens, lengths, k_codes, k_scales, v_codes, v
     _int32("cu_seqlens", cu_seqlens, (N + 1,))
     page, num_pages, max_pages = _mx4_checks(k_codes, k_scales, v_codes, v_scales, page_table, Hkv, d, N)
     dev = _attn_device(k, v, cu_seqlens, lengths, k_codes, k_scales, v_codes, v_scales, page_table)
-    _attn_launch(dev, stream, load_library().gdr_attn_append_mx4, code, N, _attn_int(total), Hkv, d, page, num_pages, max_pages,
+    _attn_launch(dev, stream, load_library().gdr_attn_append_mx4, code | _APART, N, _attn_int(total), Hkv, d, page, num_pages, max_pages,
                  k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), lengths.data_ptr(), k_codes.data_ptr(),
                  k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), page_table.data_ptr())
 
@@ -960,7 +965,7 @@ def gdr_attn_read_mx4(k_codes, k_scales, v_codes, v_scales, page_table, cu_seqle
         _int32("first", first, (N,))
     page, num_pages, max_pages = _mx4_checks(k_codes, k_scales, v_codes, v_scales, page_table, Hkv, d, N)
     dev = _attn_device(k, v, cu_seqlens, first, k_codes, k_scales, v_codes, v_scales, page_table)
-    _attn_launch(dev, stream, load_library().gdr_attn_read_mx4, code, N, _attn_int(total), Hkv, d, page, num_pages, max_pages,
+    _attn_launch(dev, stream, load_library().gdr_attn_read_mx4, code | _APART, N, _attn_int(total), Hkv, d, page, num_pages, max_pages,
                  k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), page_table.data_ptr(),
                  cu_seqlens.data_ptr(), None if first is None else first.data_ptr(), k.data_ptr(), v.data_ptr())
 
@@ -976,7 +981,7 @@ def gdr_attn_decode_mx4(q, k_codes, k_scales, v_codes, v_scales, page_table, len
     """Attention of each sequence's last position, or last Tq of them (up to 64:
     a draft to verify), over a 4-bit cache that holds them already: q, o
     [B,Hq,d] or [B,Tq,Hq,d], query i of sequence b at position lengths[b] - Tq + i,
-    the mask as in :func:`gdr_attn_prefill`.
+    the mask as in :func:`gdr_attn_prefill`.  o may be q.
 
     The cache as in :func:`gdr_attn_append_mx4`; page_table [B,max_pages] and
     lengths [B] are int32 device tensors.  workspace: a device tensor of at
@@ -1002,7 +1007,7 @@ def gdr_attn_decode_mx4(q, k_codes, k_scales, v_codes, v_scales, page_table, len
     need = 0 if workspace is not None else gdr_attn_decode_mx4_workspace_bytes(q.dtype, B, Tq, Hq, Hkv, d, page, max_pages, window,
                                                                                sinks)
     ws, ws_bytes, workspace = _attn_workspace(workspace, need, dev, stream)
-    _attn_launch(dev, stream, load_library().gdr_attn_decode_mx4, code, B, Tq, Hq, Hkv, d, page, num_pages, max_pages,
+    _attn_launch(dev, stream, load_library().gdr_attn_decode_mx4, code | _APART, B, Tq, Hq, Hkv, d, page, num_pages, max_pages,
                  _attn_int(window), _attn_int(sinks), d ** -0.5 if scale is None else scale, q.data_ptr(), k_codes.data_ptr(),
                  k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), page_table.data_ptr(), lengths.data_ptr(),
                  o.data_ptr(), ws, ws_bytes)

@@ -72,7 +72,8 @@ enum {
     GDR_ERR_WORKSPACE = -5,   /* workspace missing or too small             */
     GDR_ERR_BAD_ENUM = -6,    /* gate, dtype or flags not known             */
     GDR_ERR_HIP = -7,         /* the HIP runtime rejected a launch          */
-    GDR_ERR_ALIAS = -8,       /* two buffers (partially) overlap            */
+    GDR_ERR_ALIAS = -8,       /* two buffers (partially) overlap (around the
+                                 attention layers: see GDR_APART)           */
     GDR_ERR_SCRATCH = -9      /* gdr_chunk_prefill_noalloc: the problem
                                  needs more than its fixed scratch          */
 };
@@ -530,8 +531,15 @@ int gdr_attn_append(int dtype, int N, int total, int Hkv, int d, int page_size, 
  * attention, and a paged cache that holds keys and values in 4 bits.  Types, heads,
  * d, alignment and device data as in the attention calls above; fp32 arithmetic
  * throughout, outputs rounded once.
+ *
+ * An output, or the workspace, may share memory with no other tensor of the call but
+ * the input whose place it is said to take.  One that begins where another tensor does
+ * returns GDR_ERR_ALIAS.  With GDR_APART, OR'd into dtype (into page_size where there is
+ * no dtype), one that shares any byte does, views of one buffer taken row by row; without
+ * it that is the caller's to avoid.
  * ---------------------------------------------------------------------------
  */
+enum { GDR_APART = 1 << 24 };
 
 /*
  * Flags of gdr_attn_norm_rope and its backward (bitwise OR; others return
@@ -557,9 +565,8 @@ enum { GDR_ROPE_INTERLEAVED = 1, GDR_ROPE_NO_NORM = 2 };
  *
  * rot is a multiple of 16 up to d.  The angle is formed in double, so a position
  * may be any int32.  Hq and Hkv are independent here, and either may be 0.  q_out
- * may be q, and k_out k, where these are dense; an output may be no other tensor of
- * the call (GDR_ERR_ALIAS).  tokens * (Hq + Hkv) must stay below 2^29.  Returns a
- * GDR_* status.
+ * may be q, and k_out k, where these are dense.  tokens * (Hq + Hkv) must stay below
+ * 2^29.  Returns a GDR_* status.
  */
 int gdr_attn_norm_rope(int dtype, int flags, int tokens, int Hq, int Hkv, int d, int rot, float eps, long long q_stride,
                        long long k_stride, const void* q, const void* k, const float* w_q, const float* w_k,
@@ -571,14 +578,14 @@ int gdr_attn_norm_rope(int dtype, int flags, int tokens, int Hq, int Hkv, int d,
  *
  *   grad_q_out, grad_k_out  as q_out and k_out, dense
  *   grad_q, grad_k          as q and k, tokens grad_q_stride and grad_k_stride
- *                           elements apart; grad_q may be grad_q_out if it is dense
+ *                           elements apart; grad_q may be grad_q_out, and grad_k
+ *                           grad_k_out, if it is dense
  *   grad_w_q, grad_w_k      [d] fp32 or NULL (not wanted): sums over every token and
  *                           head, in a fixed order (repeated calls agree)
  *   workspace  at least gdr_attn_norm_rope_backward_workspace_bytes(...) bytes where
  *              grad_w_q or grad_w_k is wanted
  *
- * An output may be no other tensor of the call (GDR_ERR_ALIAS).  q and k are not
- * read with GDR_ROPE_NO_NORM.  Without tokens or heads grad_w_q and
+ * q and k are not read with GDR_ROPE_NO_NORM.  Without tokens or heads grad_w_q and
  * grad_w_k are zeroed.  Returns a GDR_* status.
  */
 int gdr_attn_norm_rope_backward(int dtype, int flags, int tokens, int Hq, int Hkv, int d, int rot, float eps,
@@ -615,9 +622,8 @@ size_t gdr_attn_norm_rope_backward_workspace_bytes(int dtype, int tokens, int Hq
  *                 it was behind the last token
  *   n_free_out    [1] int32 out: pages left; may be n_free
  *
- * Other tensors of the call may not be one (GDR_ERR_ALIAS).  All device data, and
- * nothing is read on the host.  page_size a power of two up to 65536.  N == 0 writes
- * cu_seqlens[0] and n_free_out.  Returns a GDR_* status.
+ * All device data, and nothing is read on the host.  page_size a power of two up to
+ * 65536.  N == 0 writes cu_seqlens[0] and n_free_out.  Returns a GDR_* status.
  */
 int gdr_attn_plan_pages(int N, int page_size, int max_pages, int n_stack, int max_tokens, const int* lengths, const int* add,
                         const int* free_pages, const int* n_free, int* page_table, int* cu_seqlens, int* added,
@@ -667,7 +673,7 @@ int gdr_attn_read_mx4(int dtype, int N, int total, int Hkv, int d, int page_size
  * a draft) of B sequences over the 4-bit cache; the mask is the attention calls'.
  * The new tokens' keys and values are in the cache already (gdr_attn_append_mx4).
  *
- *   q, o      [B, Tq, Hq, d]   dtype
+ *   q, o      [B, Tq, Hq, d]   dtype; o may be q
  *   lengths   [B] int32: positions the cache holds, the Tq new ones included: query i
  *             is at position lengths[b] - Tq + i
  *   workspace at least gdr_attn_decode_mx4_workspace_bytes(...) bytes (NULL if 0)
