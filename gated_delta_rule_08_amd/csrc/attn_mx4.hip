@@ -313,7 +313,10 @@ __global__ __launch_bounds__(64 * kMxWaves, 2) void mx4_decode_kernel(
             for (int s = 0; s < KS; ++s) {
                 float f[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) f[i] = a.scale < 0.f ? -static_cast<float>(raw[s][i]) : static_cast<float>(raw[s][i]);
+                for (int i = 0; i < 8; ++i) {
+                    f[i] = a.scale < 0.f ? -static_cast<float>(raw[s][i]) : static_cast<float>(raw[s][i]);
+                    f[i] += f[i] - f[i];  // an infinity as NaN: its scores would be -inf, as hidden keys' are, where the keys are negative
+                }
 #pragma unroll
                 for (int y = 0; y < X; ++y) {
                     split8<NP>(f, qf[y][s]);

@@ -680,8 +680,8 @@ int gdr_attn_read_mx4(int dtype, int N, int total, int Hkv, int d, int page_size
  *
  * A sequence whose length is negative or beyond its table row is skipped (o stays as
  * it was); positions of a page outside the pool are hidden; a query that sees no key (one before the first
- * position, or of an empty sequence) gets 0.  A block that stands for NaN makes the rows that see it NaN, and so does
- * a query with an infinity.  With dtype BF16 the weights enter the second product rounded to bf16.  With num_pages or
+ * position, or of an empty sequence), or whose scores all are -inf, gets 0.  A block that stands for NaN makes the
+ * rows that see it NaN, and a query with an infinity or NaN that sees a key is NaN.  With dtype BF16 the weights enter the second product rounded to bf16.  With num_pages or
  * max_pages 0 nothing is written.  Returns a GDR_* status.
  */
 int gdr_attn_decode_mx4(int dtype, int B, int Tq, int Hq, int Hkv, int d, int page_size, int num_pages, int max_pages,
