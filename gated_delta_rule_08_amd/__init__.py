@@ -879,7 +879,8 @@ def gdr_attn_plan_pages(lengths, add, free_pages, n_free, page_table, page_size:
     or no limit), do not suffice for; it and those after it add 0.  Written:
     cu_seqlens [N+1] (packed offsets of the added tokens), added [N],
     lengths_out [N] = lengths + added, n_free_out [1] and, if given, slots
-    [max_tokens]: each token's page * page_size + position % page_size.  added,
+    [max_tokens]: each token's page * page_size + position % page_size (-1 where
+    the page is negative or the slot beyond int32).  added,
     lengths_out and n_free_out may be add, lengths and n_free.  All int32;
     page_size a power of two.
     """

@@ -54,7 +54,8 @@ __device__ __forceinline__ int last_from(const int* from, int e) {
     return i;
 }
 __device__ __forceinline__ int slot_of(int page, int pos, int page_shift) {
-    return page < 0 ? -1 : static_cast<int>((static_cast<uint32_t>(page) << page_shift) + (pos & ((1 << page_shift) - 1)));
+    // no page, or one whose slots an int does not hold
+    return page < 0 || page > (0x7fffffff >> page_shift) ? -1 : (page << page_shift) + (pos & ((1 << page_shift) - 1));
 }
 
 // slots: NULL, or where the step's tokens go (few of them).

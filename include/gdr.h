@@ -618,8 +618,8 @@ size_t gdr_attn_norm_rope_backward_workspace_bytes(int dtype, int tokens, int Hq
  *   added         [N] int32 out: add[n], or 0; may be add
  *   lengths_out   [N] int32 out: lengths + added; may be lengths
  *   slots         [max_tokens] int32 out, or NULL: page * page_size + position %
- *                 page_size of every token, -1 where that page is negative; left as
- *                 it was behind the last token
+ *                 page_size of every token, -1 where that page is negative or the
+ *                 slot beyond int32; left as it was behind the last token
  *   n_free_out    [1] int32 out: pages left; may be n_free
  *
  * All device data, and nothing is read on the host.  page_size a power of two up to
