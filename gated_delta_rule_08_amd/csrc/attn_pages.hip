@@ -74,8 +74,8 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(PlanArgs a, const in
         cu[0] = 0;
     }
     __syncthreads();
-    for (int at = 0; at < a.N; at += kPlanThreads) {
-        const int n = at + tid;
+    for (long long at = 0; at < a.N; at += kPlanThreads) {  // up to 2^31 - 2 requests: at passes an int behind the last
+        const long long n = at + tid;
         const long long len = n < a.N ? lengths[n] : -1, want = n < a.N ? add[n] : 0;
         const bool fine = len >= 0 && want >= 0 && len + want <= room;
         const long long have = fine ? (len + page - 1) >> a.page_shift : 0;
@@ -134,7 +134,7 @@ __global__ __launch_bounds__(256) void slots_kernel(PlanArgs a, const int* __res
     if (t >= cu[a.N]) return;
     int s = 0;  // the request of token t
     for (int hi = a.N; hi - s > 1;) {
-        const int mid = (s + hi) >> 1;
+        const int mid = s + ((hi - s) >> 1);
         if (cu[mid] <= t)
             s = mid;
         else

@@ -44,3 +44,24 @@ def test_slots_beyond_int32(page, add):
     assert slots[:len(expect)].tolist() == expect and (slots[len(expect):] == -77).all()
     assert -1 in expect or page == 1
     assert max(expect) == 2 ** 31 - 1 or page != 1
+
+
+def test_as_many_requests_as_an_int_holds():
+    """2^31 - 2 of them: the rounds of 1024 end there.  (9 GB a tensor.)"""
+    announce("plan of 2^31 - 2 requests")
+    N = 2 ** 31 - 2
+    lengths, add = (torch.zeros(N, dtype=torch.int32, device="cuda") for _ in range(2))
+    at = [0, 1023, 1024, 2 ** 30, 2 ** 30 + 1, N - 1026, N - 1025, N - 2, N - 1]
+    for i in at:
+        add[i] = 1
+    add[5], add[N - 5] = 2, 2  # outgrow their rows
+    table = torch.full((N, 1), -5, dtype=torch.int32, device="cuda")
+    cu = torch.full((N + 1,), -5, dtype=torch.int32, device="cuda")
+    slots, left = ints([-77] * 6000), ints([0])
+    gdr.gdr_attn_plan_pages(lengths, add, ints(list(range(100, 120))), ints([20]), table, 1, cu, add, lengths, left, slots)
+    torch.cuda.synchronize()
+    assert left.tolist() == [20 - len(at)] and int(cu[N]) == len(at) and int(cu[0]) == 0
+    assert int((add != 0).sum()) == len(at) and int((lengths != 0).sum()) == len(at) and int((table != -5).sum()) == len(at)
+    for x, i in enumerate(at):
+        assert (int(cu[i]), int(cu[i + 1]), int(table[i, 0]), int(lengths[i]), int(add[i])) == (x, x + 1, 119 - x, 1, 1)
+    assert slots[:len(at)].tolist() == [119 - x for x in range(len(at))] and (slots[len(at):] == -77).all()
