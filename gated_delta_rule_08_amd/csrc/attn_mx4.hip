@@ -597,15 +597,27 @@ template <typename F> __device__ __forceinline__ void for_runs(const MxPlace& pl
     // what is left between two of them.
     int s0 = 0;
     for (int n = pl.N; n > 0;) {
-        const int step = (n + 63) / 64, at = lane * step;
+        const int step = (n - 1) / 64 + 1, at = lane * step;
         const uint64_t upto = __ballot(at < n && pl.cu[s0 + min(at, n - 1)] <= t0);
         const int k = max((upto == ~0ull ? 64 : __builtin_ctzll(~upto)) - 1, 0);
         s0 += k * step;
         n = step == 1 ? 0 : min(step, n - k * step);
     }
     if (lane < pl.range && t < pl.total) {
+        // few sequences begin within a range, but many without tokens may lie between two that have some
         int s = s0;
-        while (s + 1 < pl.N && pl.cu[s + 1] <= t) ++s;
+        for (int near = 0; s + 1 < pl.N && pl.cu[s + 1] <= t; ++near) {
+            ++s;
+            if (near < 4) continue;
+            for (int hi = pl.N; hi - s > 1;) {
+                const int mid = s + ((hi - s) >> 1);
+                if (pl.cu[mid] <= t)
+                    s = mid;
+                else
+                    hi = mid;
+            }
+            break;
+        }
         const int begin = pl.cu[s], end = min(pl.cu[s + 1], pl.total), from = pl.first ? pl.first[s] : 0;
         const long long pos = static_cast<long long>(from) + (static_cast<long long>(t) - begin);
         slot = static_cast<int>(pos & (kMxRows - 1));

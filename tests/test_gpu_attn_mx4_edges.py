@@ -54,3 +54,81 @@ def test_decode_of_a_query_that_is_not_finite(dt, sign, bad):
                 ref, bound = attend(q[b].nan_to_num(0.0, 0.0, 0.0), k, v, n, 0, 0, scale, DT[dt])
                 keep = torch.arange(Hq) != 1
                 check("o[%d]" % b, o[b][:, keep], ref[:, keep], bound[:, keep])
+
+
+# ---------------------------------------------------------------- append and read
+
+
+def offsets(counts):
+    return torch.tensor([0] + torch.tensor(counts).cumsum(0).tolist(), dtype=torch.int32).cuda()
+
+
+def append_and_read(dt, held, counts, Hkv, d, page, extra=0):
+    """The append byte by byte, then everything the cache holds read back; `extra` tokens of no sequence at the end."""
+    c = Mx4Cache(held, counts, Hkv, d, page)
+    for b, n in enumerate(held):
+        if n:
+            c.put(b, 0, make(1000 + b, dt, n, Hkv, d), make(5000 + b, dt, n, Hkv, d))
+    total = sum(counts)
+    k, v = make(1, dt, total + extra, Hkv, d), make(2, dt, total + extra, Hkv, d)
+    dev = c.device()
+    gdr.gdr_attn_append_mx4(k.cuda(), v.cuda(), offsets(counts), ints(held), *dev)
+    torch.cuda.synchronize()
+    at = 0
+    for b, n in enumerate(counts):
+        if n:
+            c.put(b, held[b], k[at:at + n], v[at:at + n])
+        at += n
+    for name, x, y in zip(("k_codes", "k_scales", "v_codes", "v_scales"), dev[:4], c.packed()):
+        assert torch.equal(x.cpu(), y), name
+    # from the middle of each sequence on
+    first = [(h + n) // 3 for h, n in zip(held, counts)]
+    there = [h + n - f for h, n, f in zip(held, counts, first)]
+    total = sum(there)
+    ko, vo = (torch.full((total + extra, Hkv, d), 9.0, dtype=DT[dt], device="cuda") for _ in range(2))
+    gdr.gdr_attn_read_mx4(*dev, offsets(there), ko, vo, first=ints(first))
+    torch.cuda.synchronize()
+    ko, vo, at = ko.double().cpu(), vo.double().cpu(), 0
+    for b, n in enumerate(there):
+        if n:
+            rk, rv = c.get(b, first[b], n)
+            assert torch.equal(ko[at:at + n], rk) and torch.equal(vo[at:at + n], rv), b
+        at += n
+    assert (ko[at:] == 9).all() and (vo[at:] == 9).all()
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_sequences_without_tokens(dt):
+    """Idle sequences between the others, from none to thousands, in front and behind."""
+    announce("mx4 sequences without tokens %s" % dt)
+    counts = []
+    for idle, n in ((0, 1), (1, 2), (3, 1), (4, 33), (5, 1), (6, 7), (63, 1), (64, 40), (1000, 3), (2500, 100), (2, 1)):
+        counts += [0] * idle + [n]
+    append_and_read(dt, [(7 * b) % 40 if b % 50 == 0 else 0 for b in range(len(counts))], counts, 2, 64, 32, extra=5)
+    append_and_read(dt, [0] * 3000, [0] * 1700 + [1, 1, 1] + [0] * 1297, 1, 128, 32)
+    append_and_read(dt, [0, 5, 0, 0], [0, 0, 0, 9], 1, 128, 32)
+
+
+def test_many_sequences_without_tokens_take_no_time():
+    """A million idle sequences between two tokens are not walked one by one (some 200 ms; the call takes 0.02)."""
+    announce("mx4 a million idle sequences")
+    N, Hkv, d, page = 1000002, 1, 64, 32
+    u8 = lambda *s: torch.zeros(*s, dtype=torch.uint8, device="cuda")  # noqa: E731
+    cache = u8(2, Hkv, page, d // 2), u8(2, Hkv, page, d // 32), u8(2, Hkv, 1, d, 16), u8(2, Hkv, page, d // 32)
+    table = torch.zeros(N, 1, dtype=torch.int32, device="cuda")
+    table[-1] = 1
+    cu = torch.ones(N + 1, dtype=torch.int32, device="cuda")
+    cu[0], cu[-1] = 0, 2
+    k, lens = make(1, "f32", 2, Hkv, d).cuda(), torch.zeros(N, dtype=torch.int32, device="cuda")
+    out = [torch.zeros_like(k) for _ in range(2)]
+    best = math.inf
+    for _ in range(5):
+        start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        start.record()
+        gdr.gdr_attn_append_mx4(k, k, cu, lens, *cache, table)
+        gdr.gdr_attn_read_mx4(*cache, table, cu, *out)
+        end.record()
+        torch.cuda.synchronize()
+        best = min(best, start.elapsed_time(end))
+    assert torch.equal(out[0], out[1]) and (out[0] != 0).any(-1).all()
+    assert best < 5, "%.2f ms" % best
