@@ -844,6 +844,7 @@ def gdr_attn_norm_rope_backward(q, k, positions, inv_freq, grad_q_out, grad_k_ou
     :func:`gdr_attn_norm_rope` for the same arguments, written into grad_q and
     grad_k (which may lie as q and k do, or be the incoming gradients
     themselves) and, where given, grad_w_q and grad_w_k (fp32 [d], overwritten).
+    Without ``norm`` q and k give their shapes only, however they lie.
     workspace: a device tensor of at least
     gdr_attn_norm_rope_backward_workspace_bytes bytes, or None to have one
     allocated for this call."""
@@ -855,8 +856,8 @@ def gdr_attn_norm_rope_backward(q, k, positions, inv_freq, grad_q_out, grad_k_ou
     _rope_weights(d, w_q, w_k, grad_w_q, grad_w_k)
     dev = _attn_device(grad_q_out, grad_k_out, w_q, w_k, grad_w_q, grad_w_k, inv_freq, positions if rot else None, workspace)
     _on_device(dev, q, k, grad_q, grad_k)
-    strides = (_token_stride("q", q, Hq, d), _token_stride("k", k, Hkv, d), _token_stride("grad_q", grad_q, Hq, d),
-               _token_stride("grad_k", grad_k, Hkv, d))
+    strides = (*((_token_stride("q", q, Hq, d), _token_stride("k", k, Hkv, d)) if norm else (0, 0)),  # else not read
+               _token_stride("grad_q", grad_q, Hq, d), _token_stride("grad_k", grad_k, Hkv, d))
     weights = grad_w_q is not None or grad_w_k is not None
     need = 0 if workspace is not None or not weights else gdr_attn_norm_rope_backward_workspace_bytes(q.dtype, tokens, Hq, Hkv, d)
     ws, ws_bytes, workspace = _attn_workspace(workspace, need, dev, stream)

@@ -116,8 +116,8 @@ int gdr_attn_norm_rope_backward(int dtype, int flags, int tokens, int Hq, int Hk
             (st = stride_checks(dtype, tokens, Hkv, d, grad_k_stride)) != GDR_OK)
             return st;
     }
-    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(grad_q_out, 16) || !aligned(grad_k_out, 16) || !aligned(grad_q, 16) ||
-        !aligned(grad_k, 16) || !aligned(w_q, 4) || !aligned(w_k, 4) || !aligned(positions, 4) || !aligned(inv_freq, 4) ||
+    if ((norm && (!aligned(q, 16) || !aligned(k, 16))) || !aligned(grad_q_out, 16) || !aligned(grad_k_out, 16) ||
+        !aligned(grad_q, 16) || !aligned(grad_k, 16) || !aligned(w_q, 4) || !aligned(w_k, 4) || !aligned(positions, 4) || !aligned(inv_freq, 4) ||
         !aligned(grad_w_q, 4) || !aligned(grad_w_k, 4) || (need && !aligned(workspace, 16)))
         return GDR_ERR_MISALIGNED;
     if (!none && ((Hq && !same_way(grad_q_out, grad_q, static_cast<long long>(Hq) * d, grad_q_stride)) ||
