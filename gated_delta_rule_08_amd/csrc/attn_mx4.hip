@@ -917,9 +917,11 @@ MxPlace place_of(int N, int total, int Hkv, int page_size, int num_pages, int ma
     // A wave goes through its runs one after another: a range holds about as many
     // tokens as a run does, and fewer where that leaves the GPU with little to do.
     // Append and read in us, with ranges of 32 and of 8: 5 prompts to 77 tokens, one
-    // group, 16.0 and 10.9; eight groups: 8 to 100 16.7, 13.5; 8 to 400 (1604 tokens)
-    // 20.3, 17.0; 8 to 1000 (4007) 22.5, 22.2; 32 to 300 (4831) 22.6, 24.0; one of 1000
-    // 13.4, 14.3.
+    // group, 16.1 and 10.9; eight groups: 8 to 100 16.6, 13.4; 8 to 400 (1604 tokens)
+    // 19.8, 17.1; 8 to 1000 (4007) 22.5, 22.2; 32 to 300 (4831) 22.6, 24.0.  One prompt:
+    // eight groups 500 tokens 12.6, 10.8, but 1000 13.3, 14.3 and 2000 15.6, 17.5 (its
+    // runs lie evenly, and three of four shorter ranges have none); one group 1000
+    // 11.7, 9.3, 16000 14.6, 12.6.
     const int mean = total / N;
     groups = d == 64 ? (Hkv + 1) / 2 : Hkv;
     const bool few = static_cast<long long>(total) * groups <= 16384;
