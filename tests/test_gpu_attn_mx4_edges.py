@@ -132,3 +132,118 @@ def test_many_sequences_without_tokens_take_no_time():
         best = min(best, start.elapsed_time(end))
     assert torch.equal(out[0], out[1]) and (out[0] != 0).any(-1).all()
     assert best < 5, "%.2f ms" % best
+
+
+def ragged(total, parts, seed):
+    """`parts` lengths that add up to total: some 0 or 1, the others far apart."""
+    g = torch.Generator().manual_seed(seed)
+    cut = [0] + sorted(torch.randint(0, total + 1, (parts - 3,), generator=g).tolist()) + [total]
+    counts = [b - a for a, b in zip(cut, cut[1:])]
+    big = max(range(len(counts)), key=counts.__getitem__)
+    counts[big] -= 1
+    return counts[:2] + [0] + counts[2:] + [1]
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("total,parts,Hkv,d,page", [
+    (2047, 14, 8, 128, 64), (2048, 14, 8, 128, 64), (2049, 14, 8, 128, 64), (2601, 9, 8, 128, 32),  # 16384 tokens x heads
+    (8191, 20, 3, 64, 32), (8193, 20, 3, 64, 128), (4097, 3, 5, 128, 1024),  # two heads of 64 to a wave
+    (2700, 120, 8, 128, 32), (3001, 420, 6, 128, 32),  # shorter sequences: ranges of 8 and of 2
+])
+def test_long_batches(dt, total, parts, Hkv, d, page):
+    """Append and read of as many tokens as take ranges of 32, on both sides of where they begin."""
+    announce("mx4 long batches %s %s" % (dt, (total, parts, Hkv, d, page)))
+    counts = ragged(total, parts, total)
+    assert sum(counts) == total
+    held = [(37 * b) % 95 if b % 4 else 32 * (b % 3) for b in range(len(counts))]
+    append_and_read(dt, held, counts, Hkv, d, page, extra=37 if total % 2 else 0)
+
+
+def test_one_long_prompt():
+    announce("mx4 one long prompt")
+    for held, n in ((0, 5000), (17, 5003)):
+        append_and_read("bf16", [held], [n], 4, 128, 64)
+
+
+def guarded(x, space):
+    """x in the middle of a larger allocation of sentinels: (the view, the allocation)."""
+    pool = torch.full((x.numel() + 2 * space,), 0xA5, dtype=torch.uint8, device="cuda")
+    view = pool[space:space + x.numel()].view(x.shape)
+    view.copy_(x)
+    return view, pool
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("Hkv,d,page", [(2, 64, 32), (3, 128, 64)])
+def test_append_writes_nowhere_else(dt, Hkv, d, page):
+    """Offsets out of order or beyond the tokens, bad lengths and bad pages: nothing before, between or behind the caches, and
+    no page that is in no row of the table."""
+    announce("mx4 append writes nowhere else %s %s" % (dt, (Hkv, d, page)))
+    N, space = 6, 1 << 16
+    c = Mx4Cache([100] * N, [60] * N, Hkv, d, page, spare=5)
+    used = set(c.table.view(-1).tolist())
+    spare = [p for p in range(c.kc.shape[0]) if p not in used]
+    assert len(spare) == 5
+    total = 300
+    k, v = make(1, dt, total, Hkv, d).cuda(), make(2, dt, total, Hkv, d).cuda()
+    top = 2 ** 31 - 1
+    pages = c.kc.shape[0]
+    for cu in ([-5, 90, 30, top, 60, 20, -9], [0, 50, 100, 150, 200, 250, top], [299, 0, 299, 0, 299, 0, 299],
+               [-2 ** 31, -1, 5, 300, 301, 10 ** 9, top], [0, 50, 100, 150, 200, 250, 300]):
+        for lens in ([0] * N, [100, -1, top, 159, -2 ** 31, 10 ** 6], [160, 128, 159, 31, 33, 1]):
+            for spoil in (False, True):
+                table = c.table.clone()
+                if spoil:
+                    table[1, 0], table[2, -1], table[4, 1], table[5, 0] = pages, -1, top, -2 ** 31
+                views, pools = zip(*(guarded(x, space) for x in c.packed()))
+                gdr.gdr_attn_append_mx4(k, v, ints(cu), ints(lens), *views, table.cuda())
+                torch.cuda.synchronize()
+                for view, pool, before in zip(views, pools, c.packed()):
+                    assert (pool[:space] == 0xA5).all() and (pool[-space:] == 0xA5).all(), (cu, lens)
+                    assert torch.equal(view[spare].cpu(), before[spare]), (cu, lens)
+    assert not torch.equal(views[0].cpu(), c.packed()[0])  # the last offsets are in order: most of it is written
+
+
+# ---------------------------------------------------------------- decode: a wave for each unit
+
+
+@pytest.mark.parametrize("B,Tq,Hq,Hkv,d,page,window,sinks,longest", [
+    (513, 1, 16, 2, 64, 32, 0, 0, 200), (515, 1, 16, 2, 128, 32, 0, 0, 600),    # 8 rows: two copies
+    (513, 2, 8, 2, 128, 64, 0, 0, 1000), (345, 1, 21, 3, 64, 64, 150, 2, 900),   # 8 and 7
+    (1025, 1, 16, 1, 128, 32, 0, 0, 300), (343, 5, 12, 3, 128, 32, 0, 0, 100),   # 16 and 20: one copy, a second tile
+    (513, 1, 17, 1, 128, 64, 300, 5, 700), (515, 9, 2, 1, 64, 32, 0, 0, 130),    # 17 and 18
+])
+def test_decode_many_short_units(B, Tq, Hq, Hkv, d, page, window, sinks, longest):
+    """bf16 with more than four rows to a unit, over 1023 units of up to 1024 keys: a wave to each, the last workgroup not full."""
+    announce("mx4 decode many short units %s" % ((B, Tq, Hq, Hkv, d, page, window, sinks, longest),))
+    units = B * Hkv * -(-Tq * Hq // Hkv // 16)
+    assert units >= 1024 and units % 4
+    edges = [0, 1, 31, 32, 33, 127, 128, 129, longest]
+    lengths = edges + [1 + 37 * b % min(200, longest) for b in range(B - len(edges))]
+    decode_and_check("bf16", lengths, Tq, Hq, Hkv, d, page, window, sinks, every=7)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("G", [7, 8, 16, 20])
+def test_decode_short_tables(dt, G):
+    """Tables of up to 128 keys, or a window that leaves as few: the same form for few units too."""
+    announce("mx4 decode short tables %s %d" % (dt, G))
+    decode_and_check(dt, [0, 1, 32, 127, 128], 1, 2 * G, 2, 128, 32, 0, 0)
+    decode_and_check(dt, [0, 1, 32, 127, 128], 1, G, 1, 64, 128, 0, 0)
+    decode_and_check(dt, [5, 300, 97, 1000, 64], 1, G, 1, 128, 64, 90, 33)
+
+
+def decode_and_check(dt, lengths, Tq, Hq, Hkv, d, page, window, sinks, every=1):
+    c = Mx4Cache(lengths, [0] * len(lengths), Hkv, d, page)
+    for b, n in enumerate(lengths):
+        c.put(b, 0, make(10 + b, dt, n, Hkv, d), make(5000 + b, dt, n, Hkv, d))
+    q = make(1, dt, len(lengths), Tq, Hq, d)
+    o = torch.full_like(q, 7.0).cuda()
+    gdr.gdr_attn_decode_mx4(q.cuda(), *c.device(), ints(lengths), o, window=window, sinks=sinks)
+    torch.cuda.synchronize()
+    o = o.cpu()
+    for b in list(range(9)) + list(range(9, len(lengths), every)) + [len(lengths) - 1]:
+        if b < len(lengths):
+            k, v = c.get(b, 0, lengths[b])
+            ref, bound = attend(q[b], k, v, lengths[b], window, sinks, d ** -0.5, DT[dt])
+            check("o[%d]" % b, o[b], ref, bound)
