@@ -87,6 +87,25 @@ template <int NP> __device__ __forceinline__ void split8(const float (&x)[8], bf
     }
 }
 
+// 8 elements of a query as operands, with the sign turned.  An infinity goes in as NaN (the
+// pieces of one are): where the keys are negative its scores would all be -inf, as hidden keys'
+// are.
+__device__ __forceinline__ void query8(const f32x8& q, bool turned, bf16x8v (&to)[3]) {
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = turned ? -q[i] : q[i];
+    split8<3>(f, to);
+}
+__device__ __forceinline__ void query8(const bf16x8v& q, bool turned, bf16x8v (&to)[1]) {
+    u32x4 w = __builtin_bit_cast(u32x4, q);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // an exponent of ones gets a mantissa
+        w[i] |= ((w[i] & 0x7fff7fffu) + 0x00800080u) >> 15 & 0x00010001u;
+        w[i] ^= turned ? 0x80008000u : 0u;
+    }
+    to[0] = __builtin_bit_cast(bf16x8v, w);
+}
+
 // LDS of the decode step: for each wave the keys, values and scales of one step.
 // Keys are read 16 (d = 64: 8) bytes a lane, four positions of each of the four
 // blocks at a time.  d = 128: odd blocks have their 16-byte units swapped in
@@ -311,17 +330,12 @@ __global__ __launch_bounds__(64 * kMxWaves, 2) void mx4_decode_kernel(
             // (waiting for the query, the compiler waits for the copies too, once a unit)
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
-                float f[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    f[i] = a.scale < 0.f ? -static_cast<float>(raw[s][i]) : static_cast<float>(raw[s][i]);
-                    f[i] += f[i] - f[i];  // an infinity as NaN: its scores would be -inf, as hidden keys' are, where the keys are negative
-                }
+                bf16x8v f[NP];
+                query8(raw[s], a.scale < 0.f, f);
 #pragma unroll
                 for (int y = 0; y < X; ++y) {
-                    split8<NP>(f, qf[y][s]);
 #pragma unroll
-                    for (int p = 0; p < NP; ++p) qf[y][s][p] = X > 1 ? kept(of_copy(qf[y][s][p], x == y)) : qf[y][s][p];
+                    for (int p = 0; p < NP; ++p) qf[y][s][p] = X > 1 ? kept(of_copy(f[p], x == y)) : f[p];
                 }
             }
         }
