@@ -186,21 +186,25 @@ template <typename F> __device__ __forceinline__ float over_blocks(float v, F f)
 // takes positions 32 x / X .. of each block.  Of the keys' tiles each meets the query
 // in its own copy's columns only, zero in the others, so that X tiles share an
 // accumulator, and a lane has 32 / X positions; of the weights each product takes
-// one copy's, and the copies' sums are added at the end.  (The code of a step, masks
-// among it: 970 vector instructions with X = 1, 690 with X = 4.)
+// one copy's, and the copies' sums are added at the end.  (The code of a step as
+// compiled for d = 128, masks and the path of NaN bytes among it: 967 vector
+// instructions with X = 1, 896 with 2, 687 with 4; fp32 1671.)
 //
 // The keys' scales are applied by the conversion to bf16, which is exact.  The
 // values' scales differ along the summed axis and are multiplied into the weights:
 // one set of weights for every 32 channels.  bf16: the weights are rounded to bf16
 // after the power of two, which is the same as before it.  fp32: queries and
 // weights go in as three bf16 pieces, 24 bits, and no bit of the codes is lost.
+// Either holds while a weight times the power of two, or its last piece, stays above
+// 2^-126; what falls below is an absolute error of that size (values of 2^-100 and
+// more show nothing of it).
 //
 // A unit's steps go to the four waves of a workgroup in turn, joined in LDS, or all
 // to one wave (see mx4_args).
 //
 // Bound by HBM: 64 sequences of 16 .. 8000 tokens, 32 heads over 8, d = 128 (280 MB)
 // 54 us and 5 for the join, 5.2 TB/s; one of 32768 14.7 + 4.3.  The vector ALUs are
-// busy for half of it, the matrix cores for an eighth.  Everything that is read
+// busy for 30% of it, the matrix cores for 10% (fp32: 98 us, 52% and 22%).  Everything that is read
 // goes through LDS, straight from memory in whole lines: fetched into the registers
 // of the lanes that need it, each line of the keys and scales is asked for by
 // several of them while it is on its way, and the L1 cache stalls on that (89 us
@@ -968,7 +972,10 @@ Mx4Args mx4_args(int B, int Tq, int Hq, int Hkv, int page_size, int num_pages, i
     a.sinks = sinks;
     a.scale = scale;
     // A dealt batch pays for its join and for the shares' search, a unit of its own for
-    // the longest sequence's steps one after another.  Measured with 32 heads over 8 and
+    // the longest sequence's steps one after another.  The lengths are device data: the
+    // rule goes by what the table has room for, and short sequences behind a wide table
+    // are dealt out too (128 of 50 .. 100 tokens, 32 heads over 32: 17.6 us in a table of
+    // 128 keys, 47.2 in one of 32768; over 8: 8.3 and 17.5).  Measured with 32 heads over 8 and
     // over 32, graph times in us:
     //  units  keys   a wave  a workgroup  dealt
     //     64   500     14.1      7.4
@@ -1023,7 +1030,7 @@ hipError_t launch_mx4_decode_t(const Mx4Args& a, const void* q, const void* k_co
 }  // namespace attn
 
 size_t attn_decode_mx4_workspace_floats(int Tq, int Hq, int Hkv, int d, int page_size, int max_pages, int window, int sinks) {
-    // by the keys alone: which batches are dealt out is free to change
+    // by the keys alone, from 513 of them: which batches are dealt out is free to change
     attn::Mx4Args a = attn::mx4_args(1, Tq, Hq, Hkv, page_size, 0, max_pages, window, sinks, 1.f);
     a.shares = attn::mx4_keys(page_size, max_pages, window, sinks, Tq) <= 512 ? 0 : attn::kMxShares;
     return attn::part_floats(a, d);

@@ -554,7 +554,9 @@ enum { GDR_ROPE_INTERLEAVED = 1, GDR_ROPE_NO_NORM = 2 };
  * channels by the token's position, in one pass: with x one head's d channels,
  *     y = x / sqrt(mean(x^2) + eps) * w,
  *     (y_a, y_b) <- (y_a cos t - y_b sin t, y_b cos t + y_a sin t),
- * t = positions[token] * inv_freq[i] for pair i of rot / 2.
+ * t = positions[token] * inv_freq[i] for pair i of rot / 2.  x^2 is summed in fp32: a
+ * row whose sum passes 3.4e38 gives 0, and with eps 0 one whose sum falls below 1e-38
+ * infinities or NaN.
  *
  *   q      [tokens, Hq, d]    dtype, token after token q_stride elements apart (a
  *   k      [tokens, Hkv, d]   view of a fused projection; k_stride likewise); the
@@ -681,8 +683,10 @@ int gdr_attn_read_mx4(int dtype, int N, int total, int Hkv, int d, int page_size
  * A sequence whose length is negative or beyond its table row is skipped (o stays as
  * it was); positions of a page outside the pool are hidden; a query that sees no key (one before the first
  * position, or of an empty sequence), or whose scores all are -inf, gets 0.  A block that stands for NaN makes the
- * rows that see it NaN, and a query with an infinity or NaN that sees a key is NaN.  With dtype BF16 the weights enter the second product rounded to bf16.  With num_pages or
- * max_pages 0 nothing is written.  Returns a GDR_* status.
+ * rows that see it NaN, and a query with an infinity or NaN that sees a key is NaN.
+ * With dtype BF16 the weights enter the second product rounded to bf16; with either, a
+ * weight times its value's scale below 2^-126 (F32: the last bits of one below 2^-110) is
+ * lost.  With num_pages or max_pages 0 nothing is written.  Returns a GDR_* status.
  */
 int gdr_attn_decode_mx4(int dtype, int B, int Tq, int Hq, int Hkv, int d, int page_size, int num_pages, int max_pages,
                         int window, int sinks, float scale, const void* q, const void* k_codes, const void* k_scales,
