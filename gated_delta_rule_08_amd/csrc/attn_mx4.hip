@@ -193,7 +193,10 @@ template <typename F> __device__ __forceinline__ float over_blocks(float v, F f)
 // The keys' scales are applied by the conversion to bf16, which is exact.  The
 // values' scales differ along the summed axis and are multiplied into the weights:
 // one set of weights for every 32 channels.  bf16: the weights are rounded to bf16
-// after the power of two, which is the same as before it.  fp32: queries and
+// after the power of two, which is the same as before it.  (A second piece of them
+// would bring the output's error from 2.0e-3 to 1.65e-3, that of exact weights, and
+// take 62 us instead of 59 for 64 sequences of 16 .. 8000, 53 instead of 42 with 16
+// rows of 16 .. 4000; the codes themselves stand for values within 11%.)  fp32: queries and
 // weights go in as three bf16 pieces, 24 bits, and no bit of the codes is lost.
 // Either holds while a weight times the power of two, or its last piece, stays above
 // 2^-126; what falls below is an absolute error of that size (values of 2^-100 and
